@@ -1,0 +1,411 @@
+"""Cases of the operators around a linear layer in microscaled formats.
+
+RMS norm with the residual's addition and an output in MXFP8 (E4M3 elements,
+one E8M0 scale per 32), its backward pass, the MXFP8 x MXFP8 / MXFP4 product
+with bias, activation (plain or gated) and residual in its epilogue, and the
+backward pass of that epilogue. `run` computes them in elementary torch
+operations, or, with `own`, with the package's operators.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+EPS = 1e-5
+DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0)
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+def _norm(rows, cols, stream="bf16", residual=True, train=False, **more):
+    return dict(op="norm", rows=rows, cols=cols, stream=stream, residual=residual, train=train, **more)
+
+
+def _norm_grad(rows, cols, stream="bf16", dh=True, **more):
+    return dict(op="norm_grad", rows=rows, cols=cols, stream=stream, dh=dh, **more)
+
+
+def _linear(m, n, K, weight, act="NONE", gated=False, bias=False, residual=False, out="bf16",
+            save_z=False, **more):
+    return dict(op="linear", m=m, n=n, K=K, weight=weight, act=act, gated=gated, bias=bias,
+                residual=residual, out=out, save_z=save_z, **more)
+
+
+def _act_grad(m, n, act, gated=False, bias=False, **more):
+    return dict(op="act_grad", m=m, n=n, act=act, gated=gated, bias=bias, **more)
+
+
+def listed():
+    return [
+        # serving, one token: the norm before a Llama3.1-8B sublayer
+        _norm(1, 4096, name="norm_token"),
+        # a ragged batch whose residual stream is kept in 32 bits, training
+        _norm(1531, 2080, stream="f32", train=True, name="norm_ragged_f32"),
+        # training, 8 sequences of 4096 tokens at Llama3.1-8B's width
+        _norm(32768, 4096, train=True, name="norm_train"),
+        # training, Llama3.2-1B's width: the gradient with the residual path's
+        _norm_grad(16384, 2048, name="norm_grad"),
+        # a ragged micro-batch with the residual stream in 32 bits
+        _norm_grad(3001, 4096, stream="f32", name="norm_grad_ragged_f32"),
+        # serving, one token: Llama3.1-8B down-proj from 4-bit weights, added to the stream
+        _linear(1, 4096, 14336, "mxfp4", residual=True, name="linear_token"),
+        # serving, a small batch of sequences: gate/up from 4-bit weights, MXFP8 for the next product
+        _linear(24, 14336, 4096, "mxfp4", act="SILU", gated=True, out="mxfp8", name="gate_up_batch"),
+        # a ragged batch through an ordinary bias + GELU layer, training
+        _linear(333, 2050, 2080, "mxfp8", act="GELU_TANH", bias=True, save_z=True,
+                name="linear_gelu_ragged"),
+        # serving, a prompt of 4096 tokens: gate/up from 4-bit weights
+        _linear(4096, 14336, 4096, "mxfp4", act="SILU", gated=True, out="mxfp8", name="gate_up_prompt"),
+        # training, Llama3.1-8B down-proj over 8 sequences of 4096 tokens
+        _linear(32768, 4096, 14336, "mxfp8", residual=True, name="linear_train"),
+        # training: gradient of the gated activation of Llama3.1-8B over 4 sequences
+        _act_grad(16384, 14336, "SILU", gated=True, name="act_grad_gated"),
+        # a ragged batch: gradient of bias + GELU, an odd width
+        _act_grad(2050, 8191, "GELU", bias=True, name="act_grad_bias_odd"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("norm", "norm_grad", "linear", "linear", "linear", "act_grad"))
+    if op == "norm":
+        rows, cols = _log(rng, 1, 32768), 32 * _log(rng, 2, 256)
+        rows = min(rows, (32768 * 4096) // cols)
+        return _norm(rows, cols, stream=rng.choice(("bf16", "f32")), residual=rng.random() < 0.8,
+                     train=rng.random() < 0.5)
+    if op == "norm_grad":
+        cols = _log(rng, 64, 8192)
+        cols = cols if rng.random() < 0.3 else -(-cols // 8) * 8
+        rows = min(_log(rng, 1, 32768), (16384 * 2048) // cols)
+        return _norm_grad(rows, cols, stream=rng.choice(("bf16", "f32")), dh=rng.random() < 0.8)
+    if op == "linear":
+        m, n, K = _log(rng, 1, 16384), _log(rng, 64, 14336), 32 * _log(rng, 4, 448)
+        gated = rng.random() < 0.3
+        out = rng.choice(("bf16", "bf16", "f32", "mxfp8"))
+        if out == "mxfp8" or rng.random() < 0.6:
+            n = -(-n // 32) * 32
+        if rng.random() < 0.5:
+            K = -(-K // 512) * 512
+        n = min(n, 8192) if gated else n
+        return _linear(m, n, K, rng.choice(("mxfp4", "mxfp8")), gated=gated,
+                       act=rng.choice(("SILU", "GELU", "GELU_TANH", "RELU") if gated else
+                                      ("NONE", "NONE", "SILU", "GELU", "GELU_TANH", "RELU")),
+                       bias=rng.random() < 0.4, residual=out != "mxfp8" and rng.random() < 0.5,
+                       out=out, save_z=rng.random() < 0.3)
+    gated = rng.random() < 0.5
+    n = _log(rng, 64, 14336)
+    n = n if rng.random() < 0.3 else -(-n // 8) * 8
+    return _act_grad(_log(rng, 1, 16384), n, rng.choice(("SILU", "GELU", "GELU_TANH", "RELU")),
+                     gated=gated, bias=rng.random() < 0.5)
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+def prepare(case, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def normal(*shape, std=1.0, dtype=torch.float32):
+        return (torch.randn(*shape, generator=gen, device=DEV) * std).to(dtype)
+
+    def activations(rows, cols):
+        """Normal values, 1 % of the columns 30 times as large."""
+        v = torch.randn(rows, cols, generator=gen, device=DEV)
+        lines = torch.randint(0, cols, (max(1, cols // 100),), generator=gen, device=DEV)
+        v[:, lines] *= 30.0
+        return v
+
+    s = {"case": case}
+    if case["op"] in ("norm", "norm_grad"):
+        rows, cols, stream = case["rows"], case["cols"], DTYPE[case["stream"]]
+        s["gain"] = (1.0 + 0.1 * normal(cols)).to(torch.bfloat16)
+        if case["op"] == "norm":
+            s["x"] = normal(rows, cols, std=0.5, dtype=torch.bfloat16 if case["residual"] else stream)
+            s["residual"] = activations(rows, cols).to(stream) if case["residual"] else None
+        else:
+            s["h"] = activations(rows, cols).to(stream)
+            s["rstd"] = torch.rsqrt(s["h"].double().square().mean(1) + EPS).float()
+            s["dy"] = normal(rows, cols, std=1e-3, dtype=torch.bfloat16)
+            s["dh"] = normal(rows, cols, std=1e-3, dtype=stream) if case["dh"] else None
+    elif case["op"] == "linear":
+        m, n, K = case["m"], case["n"], case["K"]
+        N = 2 * n if case["gated"] else n
+        s["a"] = _pack_mxfp8(activations(m, K))
+        w = normal(N, K, std=0.02)
+        s["b"] = _pack_mxfp8(w) if case["weight"] == "mxfp8" else _pack_mxfp4(w)
+        s["bias"] = normal(N, std=0.5) if case["bias"] else None
+        s["residual"] = (activations(m, n).to(DTYPE["f32" if case["out"] == "f32" else "bf16"])
+                         if case["residual"] else None)
+    else:
+        m, n = case["m"], case["n"]
+        s["z"] = normal(m, 2 * n if case["gated"] else n, std=1.5, dtype=torch.bfloat16)
+        s["dout"] = normal(m, n, std=1e-3, dtype=torch.bfloat16)
+    return s
+
+
+def _pack_mxfp8(v):
+    """(codes [rows, K] and scales [rows, K/32], bytes) of a matrix in MXFP8."""
+    b, byte = _blocks(v)
+    codes = (b / _power(byte)).to(torch.float8_e4m3fn).view(torch.uint8)
+    return codes.view(v.shape), byte.squeeze(2).to(torch.uint8)
+
+
+def _pack_mxfp4(v):
+    """(codes [rows, K/2], element 2j in the low nibble, and scales [rows, K/32])
+    of a matrix in MXFP4: scale 2^(floor(log2 amax) - 2), nearest E2M1 value."""
+    b = v.view(v.shape[0], -1, 32)
+    byte = torch.clamp(torch.frexp(b.abs().amax(2, keepdim=True))[1] + 124, min=1)
+    y = b / _power(byte)
+    edges = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device=v.device)
+    code = torch.bucketize(y.abs(), edges).to(torch.uint8) | ((y < 0).to(torch.uint8) << 3)
+    code = code.view(v.shape[0], -1, 2)
+    return code[..., 0] | (code[..., 1] << 4), byte.squeeze(2).to(torch.uint8)
+
+
+# ---------------------------------------------------------------------------
+# the plain form
+# ---------------------------------------------------------------------------
+def _power(byte):
+    """2^(byte - 127) for bytes 1 .. 254, in 32 bits."""
+    return (byte.to(torch.int32) << 23).view(torch.float32)
+
+
+def _blocks(v):
+    """Blocks of 32 of a matrix and their E8M0 bytes: the least power of two
+    that leaves the block's largest magnitude at 448 or below."""
+    b = v.view(v.shape[0], -1, 32)
+    mant, exp = torch.frexp(b.abs().amax(2, keepdim=True))
+    return b, torch.clamp(exp + 118 + (mant > 0.875).to(torch.int32), min=1)
+
+
+def _mxfp8_values(v):
+    """The values of v rounded to MXFP8 (exact in bf16)."""
+    b, byte = _blocks(v)
+    p = _power(byte)
+    return ((b / p).to(torch.float8_e4m3fn).float() * p).view(v.shape).to(torch.bfloat16)
+
+
+def _values(codes, scales, K):
+    """The matrix that packed codes (MXFP8, or MXFP4 in half the bytes) stand for."""
+    if codes.shape[1] == K:
+        v = codes.view(torch.float8_e4m3fn).float()
+    else:
+        table = torch.tensor(E2M1, device=codes.device)
+        v = table[torch.stack((codes & 15, codes >> 4), 2).to(torch.int32)]
+    return (v.view(codes.shape[0], -1, 32) * _power(scales).unsqueeze(2)).view(codes.shape[0], K)
+
+
+def _act(z, act):
+    if act == "NONE":
+        return z
+    if act == "RELU":
+        return torch.clamp(z, min=0)
+    if act == "SILU":
+        return z * torch.sigmoid(z)
+    if act == "GELU":
+        return 0.5 * z * (1 + torch.erf(z * math.sqrt(0.5)))
+    return 0.5 * z * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z * z * z)))
+
+
+def _act_slope(z, act):
+    if act == "RELU":
+        return (z > 0).to(z.dtype)
+    if act == "SILU":
+        s = torch.sigmoid(z)
+        return s * (1 + z * (1 - s))
+    if act == "GELU":
+        return 0.5 * (1 + torch.erf(z * math.sqrt(0.5))) + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    c = math.sqrt(2 / math.pi)
+    t = torch.tanh(c * (z + 0.044715 * z * z * z))
+    return 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * c * (1 + 3 * 0.044715 * z * z)
+
+
+def _plain(s):
+    c = s["case"]
+    if c["op"] == "norm":
+        x = s["x"]
+        h = x if s["residual"] is None else (x.float() + s["residual"].float()).to(s["residual"].dtype)
+        v = h.float()
+        rstd = 1 / torch.sqrt((v * v).mean(1) + EPS)
+        y = _mxfp8_values(v * rstd[:, None] * s["gain"].float())
+        return {"h": h, "y": y, "rstd": rstd} if c["train"] else {"h": h, "y": y}
+    if c["op"] == "norm_grad":
+        v, g = s["h"].float(), s["dy"].float()
+        n = v * s["rstd"][:, None]
+        dgain = (g * n).sum(0)
+        g = g * s["gain"].float()
+        dx = s["rstd"][:, None] * (g - n * (g * n).mean(1, keepdim=True))
+        if s["dh"] is not None:
+            dx = dx + s["dh"].float()
+        return {"dx": dx.to(s["h"].dtype), "dgain": dgain}
+    if c["op"] == "linear":
+        n = c["n"]
+        z = torch.matmul(_values(*s["a"], c["K"]), _values(*s["b"], c["K"]).t())
+        if s["bias"] is not None:
+            z = z + s["bias"]
+        out = _act(z[:, :n], c["act"])
+        if c["gated"]:
+            out = out * z[:, n:]
+        if s["residual"] is not None:
+            out = out + s["residual"].float()
+        out = _mxfp8_values(out) if c["out"] == "mxfp8" else out.to(DTYPE[c["out"]])
+        return {"out": out, "z": z.to(torch.bfloat16)} if c["save_z"] else {"out": out}
+    n = c["n"]
+    z, g = s["z"].float(), s["dout"].float()
+    dz = g * _act_slope(z[:, :n], c["act"])
+    if c["gated"]:
+        dz = torch.cat((dz * z[:, n:], g * _act(z[:, :n], c["act"])), 1)
+    got = {"dz": dz.to(torch.bfloat16)}
+    if c["bias"]:
+        got["dbias"] = dz.sum(0)
+    return got
+
+
+# ---------------------------------------------------------------------------
+# the package's operators
+# ---------------------------------------------------------------------------
+def _own(s):
+    import mxfp4_precision_gemms_amd as A
+
+    c = s["case"]
+    if c["op"] == "norm":
+        r = A.adahop_rmsnorm(s["x"], s["gain"], s["residual"], eps=EPS, save_rstd=c["train"])
+        h = s["x"] if r.h is None else r.h
+        y = A.adahop_mx8_dequant(r.codes, r.scales)
+        return {"h": h, "y": y, "rstd": r.rstd} if c["train"] else {"h": h, "y": y}
+    if c["op"] == "norm_grad":
+        dx, dgain = A.adahop_rmsnorm_backward(s["dy"], s["h"], s["gain"], s["rstd"], s["dh"])
+        return {"dx": dx, "dgain": dgain}
+    if c["op"] == "linear":
+        r = A.adahop_linear_mx(s["a"], s["b"], bias=s["bias"], act=c["act"], gated=c["gated"],
+                               residual=s["residual"],
+                               out_dtype="MXFP8" if c["out"] == "mxfp8" else DTYPE[c["out"]],
+                               save_z=c["save_z"])
+        out = A.adahop_mx8_dequant(r.out, r.scales) if c["out"] == "mxfp8" else r.out
+        return {"out": out, "z": r.z} if c["save_z"] else {"out": out}
+    dz, dbias = A.adahop_act_backward(s["dout"], s["z"], act=c["act"], gated=c["gated"],
+                                      bias_grad=c["bias"])
+    return {"dz": dz, "dbias": dbias} if c["bias"] else {"dz": dz}
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ---------------------------------------------------------------------------
+# what a pass cannot do without
+# ---------------------------------------------------------------------------
+def work(case):
+    if case["op"] == "norm":
+        e, t = case["rows"] * case["cols"], 2 if case["stream"] == "bf16" else 4
+        # x, residual and h; codes and scales
+        b = e * (2 + 2 * t if case["residual"] else t) + e * 33 // 32 + 2 * case["cols"]
+        return {"bytes": b + (4 * case["rows"] if case["train"] else 0), "flops": 8 * e}
+    if case["op"] == "norm_grad":
+        e, t = case["rows"] * case["cols"], 2 if case["stream"] == "bf16" else 4
+        return {"bytes": e * (2 + t * (3 if case["dh"] else 2)) + 4 * case["rows"] + 6 * case["cols"],
+                "flops": 12 * e}
+    if case["op"] == "linear":
+        m, n, K = case["m"], case["n"], case["K"]
+        N = 2 * n if case["gated"] else n
+        b = m * K * 33 // 32 + N * K * (33 if case["weight"] == "mxfp8" else 17) // 32
+        b += 4 * N if case["bias"] else 0
+        t = {"bf16": 2.0, "f32": 4.0, "mxfp8": 33 / 32}[case["out"]]
+        b += m * n * t * (2 if case["residual"] else 1) + (2 * m * N if case["save_z"] else 0)
+        return {"bytes": b, "flops": 2 * m * N * K}
+    e, parts = case["m"] * case["n"], 2 if case["gated"] else 1
+    b = 2 * e * (1 + 2 * parts) + (4 * parts * case["n"] if case["bias"] else 0)
+    return {"bytes": b, "flops": 20 * e}
+
+
+# ---------------------------------------------------------------------------
+# the definitions in 64 bits
+# ---------------------------------------------------------------------------
+def exact(case, seed):
+    s = prepare(case, seed)
+
+    def to_bf16(v):
+        """Nearest value with 8 significant bits, ties to even (normal range)."""
+        step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=1e-30))) - 7)
+        return torch.round(v / step) * step
+
+    def to_mxfp8(v):
+        b = v.reshape(v.shape[0], -1, 32)
+        amax = b.abs().amax(2, keepdim=True).clamp(min=1e-30)
+        p = torch.exp2(torch.ceil(torch.log2(amax / 448)))
+        p = torch.where(amax > 448 * p, 2 * p, p)
+        p = torch.where(amax <= 224 * p, p / 2, p)
+        u = b / p
+        step = torch.exp2(torch.floor(torch.log2(u.abs().clamp(min=2.0 ** -6))) - 3)
+        return (torch.round(u / step) * step * p).reshape(v.shape)
+
+    def matrix(codes, scales):
+        if codes.shape[1] == case["K"]:
+            i = codes.int()
+            e, f = (i >> 3) & 15, (i & 7).double()
+            v = torch.where(e > 0, (8 + f) * torch.exp2(e.double() - 10), f * 2.0 ** -9)
+            v = torch.where(i > 127, -v, v)
+        else:
+            i = torch.stack((codes & 15, codes >> 4), 2).view(codes.shape[0], -1).int()
+            e, f = (i >> 1) & 3, (i & 1).double()
+            v = torch.where(e > 0, (2 + f) * torch.exp2(e.double() - 2), f * 0.5)
+            v = torch.where(i > 7, -v, v)
+        p = torch.exp2(scales.double() - 127)
+        return v * p.repeat_interleave(32, 1)
+
+    def activation(z):
+        """(f(z), f'(z))."""
+        one = torch.ones_like(z)
+        if case["act"] == "NONE":
+            return z, one
+        if case["act"] == "RELU":
+            return torch.where(z > 0, z, 0 * z), torch.where(z > 0, one, 0 * z)
+        if case["act"] == "SILU":
+            e = torch.exp(-z)
+            return z / (1 + e), (1 + e + z * e) / (1 + e) ** 2
+        if case["act"] == "GELU":
+            cdf = 0.5 * torch.erfc(-z / 2 ** 0.5)
+            return z * cdf, cdf + z * torch.exp(-z * z / 2) / (2 * math.pi) ** 0.5
+        u = (8 / math.pi) ** 0.5 * (z + 0.044715 * z ** 3)
+        p = 1 / (1 + torch.exp(-u))
+        return z * p, p + z * p * (1 - p) * (8 / math.pi) ** 0.5 * (1 + 0.134145 * z * z)
+
+    if case["op"] == "norm":
+        h = s["x"].double()
+        if s["residual"] is not None:
+            h = h + s["residual"].double()
+            h = to_bf16(h) if case["stream"] == "bf16" else h.float().double()
+        rstd = (h.square().sum(1) / case["cols"] + EPS) ** -0.5
+        y = to_mxfp8(h * rstd[:, None] * s["gain"].double())
+        return {"h": h, "y": y, "rstd": rstd} if case["train"] else {"h": h, "y": y}
+    if case["op"] == "norm_grad":
+        h, dy, gain = s["h"].double(), s["dy"].double(), s["gain"].double()
+        r = s["rstd"].double()[:, None]
+        inner = (dy * gain * h).sum(1, keepdim=True)
+        dx = r * dy * gain - h * inner * r ** 3 / case["cols"]
+        dx = dx if s["dh"] is None else dx + s["dh"].double()
+        return {"dx": dx, "dgain": (dy * h * r).sum(0)}
+    if case["op"] == "linear":
+        z = matrix(*s["a"]) @ matrix(*s["b"]).t()
+        if s["bias"] is not None:
+            z += s["bias"].double()
+        n = case["n"]
+        out = activation(z[:, :n])[0]
+        if case["gated"]:
+            out = out * z[:, n:]
+        if s["residual"] is not None:
+            out = out + s["residual"].double()
+        out = to_mxfp8(out) if case["out"] == "mxfp8" else out
+        return {"out": out, "z": z} if case["save_z"] else {"out": out}
+    n = case["n"]
+    z, g = s["z"].double(), s["dout"].double()
+    f, slope = activation(z[:, :n])
+    dz = torch.cat((g * z[:, n:] * slope, g * f), 1) if case["gated"] else g * slope
+    return {"dz": dz, "dbias": dz.sum(0)} if case["bias"] else {"dz": dz}

@@ -88,7 +88,7 @@ def draw(rng):
     if op == "linear":
         m, n, K = _log(rng, 1, 16384), _log(rng, 64, 14336), 32 * _log(rng, 4, 448)
         gated = rng.random() < 0.3
-        out = rng.choice(("bf16", "bf16", "f32", "mxfp8"))
+        out = rng.choice(("bf16", "bf16", "mxfp8"))
         if out == "mxfp8" or rng.random() < 0.6:
             n = -(-n // 32) * 32
         if rng.random() < 0.5:
@@ -141,8 +141,7 @@ def prepare(case, seed):
         w = normal(N, K, std=0.02)
         s["b"] = _pack_mxfp8(w) if case["weight"] == "mxfp8" else _pack_mxfp4(w)
         s["bias"] = normal(N, std=0.5) if case["bias"] else None
-        s["residual"] = (activations(m, n).to(DTYPE["f32" if case["out"] == "f32" else "bf16"])
-                         if case["residual"] else None)
+        s["residual"] = activations(m, n).to(torch.bfloat16) if case["residual"] else None
     else:
         m, n = case["m"], case["n"]
         s["z"] = normal(m, 2 * n if case["gated"] else n, std=1.5, dtype=torch.bfloat16)
@@ -255,7 +254,7 @@ def _plain(s):
             out = out * z[:, n:]
         if s["residual"] is not None:
             out = out + s["residual"].float()
-        out = _mxfp8_values(out) if c["out"] == "mxfp8" else out.to(DTYPE[c["out"]])
+        out = _mxfp8_values(out) if c["out"] == "mxfp8" else out.to(torch.bfloat16)
         return {"out": out, "z": z.to(torch.bfloat16)} if c["save_z"] else {"out": out}
     n = c["n"]
     z, g = s["z"].float(), s["dout"].float()
@@ -286,7 +285,7 @@ def _own(s):
     if c["op"] == "linear":
         r = A.adahop_linear_mx(s["a"], s["b"], bias=s["bias"], act=c["act"], gated=c["gated"],
                                residual=s["residual"],
-                               out_dtype="MXFP8" if c["out"] == "mxfp8" else DTYPE[c["out"]],
+                               out_dtype="MXFP8" if c["out"] == "mxfp8" else torch.bfloat16,
                                save_z=c["save_z"])
         out = A.adahop_mx8_dequant(r.out, r.scales) if c["out"] == "mxfp8" else r.out
         return {"out": out, "z": r.z} if c["save_z"] else {"out": out}
@@ -317,7 +316,7 @@ def work(case):
         N = 2 * n if case["gated"] else n
         b = m * K * 33 // 32 + N * K * (33 if case["weight"] == "mxfp8" else 17) // 32
         b += 4 * N if case["bias"] else 0
-        t = {"bf16": 2.0, "f32": 4.0, "mxfp8": 33 / 32}[case["out"]]
+        t = {"bf16": 2.0, "mxfp8": 33 / 32}[case["out"]]
         b += m * n * t * (2 if case["residual"] else 1) + (2 * m * N if case["save_z"] else 0)
         return {"bytes": b, "flops": 2 * m * N * K}
     e, parts = case["m"] * case["n"], 2 if case["gated"] else 1

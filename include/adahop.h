@@ -466,6 +466,165 @@ ADAHOP_API adahop_status adahop_gemm_timed(adahop_op op, const uint16_t* lhs,
                                            size_t ws_bytes, void* stream,
                                            void* const* stage_events);
 
+/* ---------------------------------------------------------------------------
+ * Around the products: RMS norm, the linear layer on microscaled operands with
+ * its epilogue, and their gradients. They share the conventions above (device
+ * pointers, the caller's workspace, launches on `stream`, host checks before
+ * any launch), except that infinities and NaNs are supported: they propagate.
+ *
+ * MXFP8 (OCP Microscaling v1.0): E4M3 codes, one byte each, [rows][ld_codes],
+ * and one E8M0 scale byte per 32 consecutive elements of a row,
+ * [rows][ld_scales]. Conversion to MXFP8 here: the scale exponent is the least
+ * e with (block amax) <= 448 * 2^e, clamped to [-127, 127] and stored as the
+ * byte e + 127 (0x00 for an all-zero block), so no element saturates; the
+ * codes are v / 2^e rounded to nearest even. A block that holds an infinity
+ * or a NaN gets the scale byte 0xFF and codes 0x7F (NaN).
+ *
+ * bf16 and fp32 matrices here may start at any element-aligned address and
+ * have any leading dimension >= their columns (elements). Matrices with 0
+ * rows are allowed: nothing is read, and column sums over them are 0. */
+typedef enum { ADAHOP_MX_E2M1 = 0, ADAHOP_MX_E4M3 = 1 } adahop_mx_format;
+
+/* MXFP8 codes and scales of src [rows, cols] (bf16 or fp32, `dtype`), and the
+ * values that codes and scales stand for, in bf16 (where the values are exact
+ * down to bf16's smallest subnormal) or fp32. cols must be a multiple of 32.
+ * Errors: INVALID for NULL pointers (rows > 0), rows < 0, cols < 1 or not a
+ * multiple of 32, a leading dimension too small, a bad dtype. */
+ADAHOP_API adahop_status adahop_mx8_quant(const void* src, adahop_out_dtype dtype, int64_t rows,
+                                          int64_t cols, int64_t ld, uint8_t* codes,
+                                          int64_t ld_codes, uint8_t* scales, int64_t ld_scales,
+                                          void* stream);
+ADAHOP_API adahop_status adahop_mx8_dequant(const uint8_t* codes, int64_t ld_codes,
+                                            const uint8_t* scales, int64_t ld_scales,
+                                            int64_t rows, int64_t cols, void* dst,
+                                            adahop_out_dtype dtype, int64_t ld, void* stream);
+
+/* RMS norm of a residual stream. With a residual r (bf16 or fp32, the type of
+ * the stream): h = x + r rounded to r's type, written to h (which may be r
+ * itself); without (residual NULL): h = x, nothing is written. Then
+ *   rstd = 1 / sqrt(mean_j h_j^2 + eps),   y_j = h_j * rstd * gain_j,
+ * sums in fp32. y goes to codes and scales (MXFP8) and / or to y (bf16); at
+ * least one is required. rstd (fp32 [rows]) may be NULL.
+ * Errors: INVALID for missing pointers, cols < 1, rows < 0, leading dimensions
+ * too small, a bad dtype, cols % 32 != 0 with an MXFP8 output, eps negative or
+ * not finite, reserved not 0; UNSUPPORTED for cols > 32768 or more than
+ * 2^31 - 1 rows. */
+typedef struct {
+  int64_t rows, cols;
+  const void* x; int64_t ld_x;
+  const void* residual; int64_t ld_residual;     /* NULL: none */
+  const void* gain;                              /* [cols] */
+  void* h; int64_t ld_h;                         /* required with a residual */
+  uint16_t* y; int64_t ld_y;                     /* bf16, or NULL */
+  uint8_t* codes; int64_t ld_codes;              /* MXFP8, or NULL */
+  uint8_t* scales; int64_t ld_scales;
+  float* rstd;
+  int32_t x_dtype, residual_dtype, gain_dtype;   /* adahop_out_dtype */
+  float eps;
+  int32_t reserved[4];
+} adahop_rmsnorm_args;
+
+ADAHOP_API adahop_status adahop_rmsnorm(const adahop_rmsnorm_args* args, void* stream);
+
+/* Gradient of the norm at h, given dy (the gradient of y; the MXFP8 rounding
+ * is passed through) and, if not NULL, dh (the gradient that reaches h along
+ * the residual stream), with n = h * rstd and u = gain * dy:
+ *   dx = dh + rstd * (u - n * mean_j(u_j n_j)),   dgain = sum_rows dy * n.
+ * dx is the gradient of x and of the residual alike; dx and dh have h's type,
+ * and dx may be dh, dy or h itself (where the types agree). dgain is fp32
+ * [cols], or NULL; its sums are taken in a fixed order and need
+ * adahop_rmsnorm_backward_workspace_size(rows, cols) bytes of workspace (none
+ * without dgain). Errors: as adahop_rmsnorm, and WORKSPACE. */
+typedef struct {
+  int64_t rows, cols;
+  const void* dy; int64_t ld_dy;
+  const void* h; int64_t ld_h;
+  const void* gain;
+  const float* rstd;
+  const void* dh; int64_t ld_dh;                 /* NULL: none */
+  void* dx; int64_t ld_dx;
+  float* dgain;
+  int32_t dy_dtype, h_dtype, gain_dtype;
+  int32_t reserved[5];
+} adahop_rmsnorm_backward_args;
+
+ADAHOP_API size_t adahop_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+ADAHOP_API adahop_status adahop_rmsnorm_backward(const adahop_rmsnorm_backward_args* args, void* ws,
+                                                 size_t ws_bytes, void* stream);
+
+/* Activations of a linear layer. GELU is z * Phi(z); GELU_TANH its tanh form
+ * z / 2 * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))). */
+typedef enum {
+  ADAHOP_ACT_NONE = 0,
+  ADAHOP_ACT_RELU = 1,
+  ADAHOP_ACT_SILU = 2,
+  ADAHOP_ACT_GELU = 3,
+  ADAHOP_ACT_GELU_TANH = 4
+} adahop_act;
+
+/* Linear layer on microscaled operands:
+ *   z = deq(A) * deq(B)^T + bias                             [m, N]
+ *   out = act(z) + residual                                  [m, n], n = N
+ *   gated: out = act(z[:, :n]) * z[:, n:] + residual         [m, n], n = N / 2
+ * A: MXFP8 [m, K]. B: MXFP8 or MXFP4 [N, K] (MXFP4: codes as
+ * adahop_iht_quant writes them, two to a byte, rows ld_b_codes bytes apart;
+ * gated: the n gate rows, then the n up rows). The products are formed on the
+ * scaled matrix cores (within about 5e-5 of the result, root mean square, on
+ * operands with outlier columns; see the notes in csrc/linear_mx.hip), sums
+ * over K, bias, activation and residual in fp32, with one rounding to the
+ * output: bf16 (out, ld_out elements) or, with out_scales not NULL, MXFP8
+ * (out: codes, ld_out bytes; n a multiple of 32). z (bf16 [m, N], or NULL)
+ * keeps z for adahop_act_backward. residual is bf16 and may be out itself.
+ * Needs adahop_linear_mx_workspace_size(...) bytes of 16-byte aligned
+ * workspace (0 for most sizes).
+ * Errors: INVALID for NULL operands or out (m > 0), m < 0, N or K < 1, K not
+ * a multiple of 32, leading dimensions too small, N odd with gated, n not a
+ * multiple of 32 with an MXFP8 output, a bad format, dtype or activation,
+ * reserved not 0; UNSUPPORTED for codes of A or B that are not 16-byte
+ * aligned or whose leading dimension is not a multiple of 16, and for m, N or
+ * K of 2^30 and more; WORKSPACE. */
+typedef struct {
+  int64_t m, N, K;
+  const uint8_t* a_codes; int64_t ld_a_codes;
+  const uint8_t* a_scales; int64_t ld_a_scales;
+  const uint8_t* b_codes; int64_t ld_b_codes;
+  const uint8_t* b_scales; int64_t ld_b_scales;
+  const void* bias;                              /* [N], or NULL */
+  const uint16_t* residual; int64_t ld_residual; /* NULL: none */
+  void* out; int64_t ld_out;
+  uint8_t* out_scales; int64_t ld_out_scales;    /* NULL: out is bf16 */
+  uint16_t* z; int64_t ld_z;                     /* NULL: not kept */
+  int32_t b_format;                              /* adahop_mx_format */
+  int32_t bias_dtype;                            /* adahop_out_dtype */
+  int32_t act;                                   /* adahop_act */
+  int32_t gated;                                 /* 0 or 1 */
+  int32_t reserved[4];
+} adahop_linear_args;
+
+ADAHOP_API size_t adahop_linear_mx_workspace_size(int64_t m, int64_t N, int64_t K,
+                                                  adahop_mx_format b_format, int32_t gated);
+ADAHOP_API adahop_status adahop_linear_mx(const adahop_linear_args* args, void* ws,
+                                          size_t ws_bytes, void* stream);
+
+/* Gradient of that epilogue: from dout [m, n] (bf16 or fp32) and the kept z
+ * (bf16 [m, N]) to dz (bf16 [m, N], the GY of adahop_gemm's DGRAD and WGRAD;
+ * may be z itself)
+ *   dz = dout * act'(z);   gated: dz = [dout * z_up * act'(z_gate),
+ *                                       dout * act(z_gate)]
+ * and, if not NULL, dbias = sum_rows dz (fp32 [N], summed before dz is
+ * rounded, in a fixed order; it needs
+ * adahop_act_backward_workspace_size(m, N, gated) bytes of workspace). The
+ * residual's gradient is dout. Relu's slope at 0 is 0.
+ * Errors: INVALID for NULL dout, z or dz (m > 0), m < 0, N < 1, N odd with
+ * gated, leading dimensions too small, a bad dtype or activation;
+ * UNSUPPORTED for m or N of 2^30 and more; WORKSPACE. */
+ADAHOP_API size_t adahop_act_backward_workspace_size(int64_t m, int64_t N, int32_t gated);
+ADAHOP_API adahop_status adahop_act_backward(const void* dout, adahop_out_dtype dout_dtype,
+                                             int64_t ld_dout, const uint16_t* z, int64_t ld_z,
+                                             int64_t m, int64_t N, adahop_act act, int32_t gated,
+                                             uint16_t* dz, int64_t ld_dz, float* dbias, void* ws,
+                                             size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

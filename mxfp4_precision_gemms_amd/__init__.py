@@ -9,7 +9,7 @@ There is no CPU fallback: if the library is missing this module raises.
 """
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import numpy as np
 import torch
@@ -70,6 +70,32 @@ class CtxPlan(ctypes.Structure):
                 ("wgrad_ws_bytes", _sz)]
 
 
+class RmsnormArgs(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("x", _p), ("ld_x", _i64),
+                ("residual", _p), ("ld_residual", _i64), ("gain", _p), ("h", _p), ("ld_h", _i64),
+                ("y", _p), ("ld_y", _i64), ("codes", _p), ("ld_codes", _i64),
+                ("scales", _p), ("ld_scales", _i64), ("rstd", _p),
+                ("x_dtype", _i32), ("residual_dtype", _i32), ("gain_dtype", _i32),
+                ("eps", ctypes.c_float), ("reserved", _i32 * 4)]
+
+
+class RmsnormBackwardArgs(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("dy", _p), ("ld_dy", _i64), ("h", _p),
+                ("ld_h", _i64), ("gain", _p), ("rstd", _p), ("dh", _p), ("ld_dh", _i64),
+                ("dx", _p), ("ld_dx", _i64), ("dgain", _p), ("dy_dtype", _i32),
+                ("h_dtype", _i32), ("gain_dtype", _i32), ("reserved", _i32 * 5)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("m", _i64), ("N", _i64), ("K", _i64),
+                ("a_codes", _p), ("ld_a_codes", _i64), ("a_scales", _p), ("ld_a_scales", _i64),
+                ("b_codes", _p), ("ld_b_codes", _i64), ("b_scales", _p), ("ld_b_scales", _i64),
+                ("bias", _p), ("residual", _p), ("ld_residual", _i64), ("out", _p),
+                ("ld_out", _i64), ("out_scales", _p), ("ld_out_scales", _i64), ("z", _p),
+                ("ld_z", _i64), ("b_format", _i32), ("bias_dtype", _i32), ("act", _i32),
+                ("gated", _i32), ("reserved", _i32 * 4)]
+
+
 # Exported symbols and their C signatures (argtypes, restype).
 SIGNATURES = {
     "adahop_status_string": ([_int], ctypes.c_char_p),
@@ -104,6 +130,16 @@ SIGNATURES = {
                         _int),
     "adahop_gemm_wgrad_ctx": ([_p, _p, _sz, _i64, _i64, _i64, _int, _int, _int, _i32, _p, _int,
                                _p, _sz, _p, _p], _int),
+    "adahop_mx8_quant": ([_p, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p], _int),
+    "adahop_mx8_dequant": ([_p, _i64, _p, _i64, _i64, _i64, _p, _int, _i64, _p], _int),
+    "adahop_rmsnorm": ([ctypes.POINTER(RmsnormArgs), _p], _int),
+    "adahop_rmsnorm_backward_workspace_size": ([_i64, _i64], _sz),
+    "adahop_rmsnorm_backward": ([ctypes.POINTER(RmsnormBackwardArgs), _p, _sz, _p], _int),
+    "adahop_linear_mx_workspace_size": ([_i64, _i64, _i64, _int, _i32], _sz),
+    "adahop_linear_mx": ([ctypes.POINTER(LinearArgs), _p, _sz, _p], _int),
+    "adahop_act_backward_workspace_size": ([_i64, _i64, _i32], _sz),
+    "adahop_act_backward": ([_p, _int, _i64, _p, _i64, _i64, _i64, _int, _i32, _p, _i64, _p, _p,
+                             _sz, _p], _int),
 }
 
 _lib = None
@@ -491,3 +527,236 @@ def ctx_views(ctx: torch.Tensor, plan: CtxPlan) -> dict:
             "codes": c, "scales": sc,
             "lines": None if plan.off_lines == none
             else ctx[plan.off_lines:plan.off_lines + 2 * k * T].view(torch.int16).view(k, T)}
+
+
+# ---------------------------------------------------------------------------
+# Around the products: norm, MXFP8, the linear layer with its epilogue, and
+# their gradients
+# ---------------------------------------------------------------------------
+ACT = {"NONE": 0, "RELU": 1, "SILU": 2, "GELU": 3, "GELU_TANH": 4}
+MX_FORMAT = {"MXFP4": 0, "MXFP8": 1}
+_FLOAT = {torch.bfloat16: 0, torch.int16: 0, torch.float32: 1}
+_BF16 = {torch.bfloat16: 0, torch.int16: 0}
+_CODES = {torch.uint8: 0, torch.float8_e4m3fn: 0}
+_SCALES = {torch.uint8: 0, torch.float8_e8m0fnu: 0}
+
+
+def _matrix(t: torch.Tensor, name: str, types: dict, rows: int, cols: int, device: int):
+    """(address, leading dimension, type) of a 2-D device matrix of that size."""
+    kind = types.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name}: unexpected dtype {t.dtype}")
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name}: must be on the same device as the other operands")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name}: expected unit column stride")
+    return t.data_ptr(), (s0 if rows > 1 else max(s0, cols)), kind
+
+
+def _vector(t: torch.Tensor, name: str, types: dict, n: int, device: int):
+    kind = types.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name}: unexpected dtype {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: must be on the same device as the other operands")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected {n} contiguous elements")
+    return t.data_ptr(), kind
+
+
+def _size(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor")
+    return t.shape
+
+
+def _scratch(need: int, ws: Optional[torch.Tensor], device):
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return (None, 0, ws) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size(), ws)
+
+
+def adahop_mx8_quant(src: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                     scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(codes [rows, cols], scales [rows, cols / 32]), uint8, of a bf16 or fp32
+    matrix in MXFP8."""
+    rows, cols = _size(src, "src")
+    dev = src.device
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+    d = src.get_device()
+    p, ld, kind = _matrix(src, "src", _FLOAT, rows, cols, d)
+    c, ldc, _ = _matrix(codes, "codes", _CODES, rows, cols, d)
+    sc, lds, _ = _matrix(scales, "scales", _SCALES, rows, cols // 32, d)
+    _check(lib().adahop_mx8_quant(p, kind, rows, cols, ld, c, ldc, sc, lds, _stream(dev)))
+    return codes, scales
+
+
+def adahop_mx8_dequant(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.bfloat16,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of an MXFP8 matrix, in bf16 (exact) or fp32."""
+    rows, cols = _size(codes, "codes")
+    dev = codes.device
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    d = codes.get_device()
+    c, ldc, _ = _matrix(codes, "codes", _CODES, rows, cols, d)
+    sc, lds, _ = _matrix(scales, "scales", _SCALES, rows, cols // 32, d)
+    p, ld, kind = _matrix(out, "out", _FLOAT, rows, cols, d)
+    _check(lib().adahop_mx8_dequant(c, ldc, sc, lds, rows, cols, p, kind, ld, _stream(dev)))
+    return out
+
+
+class RmsnormOut(NamedTuple):
+    h: Optional[torch.Tensor]        # the new residual stream (None without a residual)
+    y: Optional[torch.Tensor]        # bf16, if asked for
+    codes: Optional[torch.Tensor]    # MXFP8, if asked for
+    scales: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]     # fp32 [rows], if asked for
+
+
+def adahop_rmsnorm(x: torch.Tensor, gain: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, mx8: bool = True, bf16: bool = False,
+                   save_rstd: bool = False, h: Optional[torch.Tensor] = None) -> RmsnormOut:
+    """RMS norm of x (+ residual): h = x + residual in the residual's type,
+    y = h / sqrt(mean h^2 + eps) * gain as MXFP8 codes and scales (mx8) and /
+    or in bf16. h may be given (the residual itself, to update it in place)."""
+    rows, cols = _size(x, "x")
+    dev, d = x.device, x.get_device()
+    xp, ldx, xk = _matrix(x, "x", _FLOAT, rows, cols, d)
+    gp, gk = _vector(gain, "gain", _FLOAT, cols, d)
+    a = RmsnormArgs(rows=rows, cols=cols, x=xp, ld_x=ldx, gain=gp, x_dtype=xk, gain_dtype=gk, eps=eps)
+    if residual is not None:
+        a.residual, a.ld_residual, a.residual_dtype = _matrix(residual, "residual", _FLOAT, rows, cols, d)
+        if h is None:
+            h = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
+        elif h.dtype != residual.dtype:
+            raise TypeError("h must have the residual's dtype")
+        a.h, a.ld_h, _ = _matrix(h, "h", _FLOAT, rows, cols, d)
+    elif h is not None:
+        raise ValueError("h goes with a residual")
+    codes = scales = y = rstd = None
+    if mx8:
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+        a.codes, a.ld_codes, a.scales, a.ld_scales = codes.data_ptr(), cols, scales.data_ptr(), cols // 32
+    if bf16:
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        a.y, a.ld_y = y.data_ptr(), cols
+    if save_rstd:
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        a.rstd = rstd.data_ptr()
+    _check(lib().adahop_rmsnorm(ctypes.byref(a), _stream(dev)))
+    return RmsnormOut(h, y, codes, scales, rstd)
+
+
+def adahop_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, gain: torch.Tensor,
+                            rstd: torch.Tensor, dh: Optional[torch.Tensor] = None,
+                            gain_grad: bool = True, dx: Optional[torch.Tensor] = None,
+                            ws: Optional[torch.Tensor] = None):
+    """(dx, dgain): the gradient at h -- of x and of the residual alike -- from
+    dy and, if given, the residual stream's dh; dgain is fp32 (None without
+    gain_grad)."""
+    rows, cols = _size(h, "h")
+    dev, d = h.device, h.get_device()
+    yp, ldy, yk = _matrix(dy, "dy", _FLOAT, rows, cols, d)
+    hp, ldh, hk = _matrix(h, "h", _FLOAT, rows, cols, d)
+    gp, gk = _vector(gain, "gain", _FLOAT, cols, d)
+    rp, _ = _vector(rstd, "rstd", {torch.float32: 1}, rows, d)
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=h.dtype, device=dev)
+    xp, ldx, xk = _matrix(dx, "dx", _FLOAT, rows, cols, d)
+    a = RmsnormBackwardArgs(rows, cols, yp, ldy, hp, ldh, gp, rp, None, 0, xp, ldx, None, yk, hk, gk)
+    if dh is not None:
+        a.dh, a.ld_dh, ek = _matrix(dh, "dh", _FLOAT, rows, cols, d)
+    if xk != hk or (dh is not None and ek != hk):
+        raise TypeError("dx and dh must have h's dtype")
+    dgain, wp, wn = None, None, 0
+    if gain_grad:
+        dgain = torch.empty(cols, dtype=torch.float32, device=dev)
+        a.dgain = dgain.data_ptr()
+        wp, wn, ws = _scratch(lib().adahop_rmsnorm_backward_workspace_size(rows, cols), ws, dev)
+    _check(lib().adahop_rmsnorm_backward(ctypes.byref(a), wp, wn, _stream(dev)))
+    return dx, dgain
+
+
+class LinearOut(NamedTuple):
+    out: torch.Tensor                # bf16, or MXFP8 codes
+    scales: Optional[torch.Tensor]   # MXFP8 scales
+    z: Optional[torch.Tensor]        # bf16 pre-activation, if asked for
+
+
+def adahop_linear_mx(a: Tuple[torch.Tensor, torch.Tensor], b: Tuple[torch.Tensor, torch.Tensor],
+                     bias: Optional[torch.Tensor] = None, act: str = "NONE", gated: bool = False,
+                     residual: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                     save_z: bool = False, out: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None) -> LinearOut:
+    """act(z) + residual with z = A B^T + bias; gated: act(z[:, :n]) * z[:, n:].
+
+    a: MXFP8 (codes [m, K], scales [m, K/32]); b: weights [N, K] in MXFP8, or
+    in MXFP4 (codes [N, K/2], as adahop_iht_quant gives them). out_dtype:
+    torch.bfloat16, or "MXFP8" for codes and scales. out (bf16) may be given,
+    the residual itself among others."""
+    (ac, asc), (bc, bsc) = a, b
+    m, K = _size(ac, "a codes")
+    N, Kb = _size(bc, "b codes")
+    dev, d = ac.device, ac.get_device()
+    if Kb != K and Kb * 2 != K:
+        raise ValueError(f"b codes: {Kb} bytes a row fit neither MXFP8 nor MXFP4 of K = {K}")
+    n = N // 2 if gated else N
+    g = LinearArgs(m, N, K, *_matrix(ac, "a codes", _CODES, m, K, d)[:2],
+                   *_matrix(asc, "a scales", _SCALES, m, K // 32, d)[:2],
+                   *_matrix(bc, "b codes", _CODES, N, Kb, d)[:2],
+                   *_matrix(bsc, "b scales", _SCALES, N, K // 32, d)[:2])
+    g.b_format, g.act, g.gated = (1 if Kb == K else 0), ACT[act], 1 if gated else 0
+    if bias is not None:
+        g.bias, g.bias_dtype = _vector(bias, "bias", _FLOAT, N, d)
+    if residual is not None:
+        g.residual, g.ld_residual, _ = _matrix(residual, "residual", _BF16, m, n, d)
+    scales = z = None
+    if out_dtype == "MXFP8":
+        if out is not None:
+            raise ValueError("out is for a bf16 output")
+        out = torch.empty((m, n), dtype=torch.uint8, device=dev)
+        scales = torch.empty((m, n // 32), dtype=torch.uint8, device=dev)
+        g.out, g.ld_out, g.out_scales, g.ld_out_scales = out.data_ptr(), n, scales.data_ptr(), n // 32
+    elif out_dtype == torch.bfloat16:
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        g.out, g.ld_out, _ = _matrix(out, "out", _BF16, m, n, d)
+    else:
+        raise TypeError(f"out_dtype: torch.bfloat16 or \"MXFP8\", not {out_dtype}")
+    if save_z:
+        z = torch.empty((m, N), dtype=torch.bfloat16, device=dev)
+        g.z, g.ld_z = z.data_ptr(), N
+    wp, wn, ws = _scratch(lib().adahop_linear_mx_workspace_size(m, N, K, g.b_format, g.gated), ws, dev)
+    _check(lib().adahop_linear_mx(ctypes.byref(g), wp, wn, _stream(dev)))
+    return LinearOut(out, scales, z)
+
+
+def adahop_act_backward(dout: torch.Tensor, z: torch.Tensor, act: str = "NONE", gated: bool = False,
+                        bias_grad: bool = False, dz: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None):
+    """(dz, dbias): the gradient of z [m, N] (bf16: the GY of adahop_gemm's
+    DGRAD and WGRAD) and, if asked for, of the bias (fp32 [N])."""
+    m, N = _size(z, "z")
+    n = N // 2 if gated else N
+    dev, d = z.device, z.get_device()
+    gp, ldg, gk = _matrix(dout, "dout", _FLOAT, m, n, d)
+    zp, ldz, _ = _matrix(z, "z", _BF16, m, N, d)
+    if dz is None:
+        dz = torch.empty((m, N), dtype=torch.bfloat16, device=dev)
+    op, ldo, _ = _matrix(dz, "dz", _BF16, m, N, d)
+    dbias, bp, wp, wn = None, None, None, 0
+    if bias_grad:
+        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+        bp = dbias.data_ptr()
+        wp, wn, ws = _scratch(lib().adahop_act_backward_workspace_size(m, N, int(gated)), ws, dev)
+    _check(lib().adahop_act_backward(gp, gk, ldg, zp, ldz, m, N, ACT[act], int(gated), op, ldo, bp, wp,
+                                     wn, _stream(dev)))
+    return dz, dbias

@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libadahop.so")
 # --mfma-ceiling); not part of the AdaHOP path, built as its own library.
 PROBE_SRC = "probe_mfma.hip"
 PROBE_LIB = os.path.join(HERE, "libadahop_probe.so")
-SOURCES = ["adahop_api.hip", "foid.hip", "iht_quant.hip", "gemm_mx.hip"]
+SOURCES = ["adahop_api.hip", "foid.hip", "iht_quant.hip", "gemm_mx.hip", "mx8_api.hip",
+           "mx8_norm.hip", "mx8_act.hip", "linear_mx.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

@@ -178,4 +178,59 @@ adahop_status gemm_mx_launch(const uint8_t* a_codes, const uint8_t* a_scales,
 // split fixup, the outlier scatter).
 adahop_status record_main_done(hipEvent_t main_done, hipStream_t stream, const char* what);
 
+// ---- norm, quantizer and linear layer in MXFP8 ------------------------------
+// Arguments as the public entry points', already checked; leading dimensions
+// in elements (codes and scales in bytes).
+adahop_status rmsnorm_launch(const void* x, int x_f32, const void* r, int r_f32, const void* gain,
+                             int gain_f32, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                             float eps, void* h, int64_t ldh, uint16_t* y, int64_t ldy,
+                             uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds, float* rstd,
+                             hipStream_t stream);
+// Workgroups of the backward kernel: `partial` holds that many rows of cols
+// fp32 (unused, may be null, without dgain).
+int rmsnorm_backward_groups(int64_t rows, int64_t cols);
+adahop_status rmsnorm_backward_launch(const void* dy, int dy_f32, const void* h, int h_f32,
+                                      const void* gain, int gain_f32, const float* rstd,
+                                      const void* dh, int64_t rows, int64_t cols, int64_t lddy,
+                                      int64_t ldh, int64_t lddh, int64_t lddx, void* dx,
+                                      float* dgain, float* partial, hipStream_t stream);
+// out[c] = sum over p < parts of partial[p][c], in a fixed order.
+adahop_status column_reduce_launch(const float* partial, int parts, int64_t cols, float* out,
+                                   hipStream_t stream);
+adahop_status mx8_quant_launch(const void* src, int f32, int64_t rows, int64_t cols, int64_t ld,
+                               uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds,
+                               hipStream_t stream);
+adahop_status mx8_dequant_launch(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                                 int64_t rows, int64_t cols, void* dst, int f32, int64_t ldd,
+                                 hipStream_t stream);
+// Row groups of the epilogue's backward kernel: `partial` holds that many
+// rows of n (gated: 2 n) fp32 (unused without dbias).
+int64_t act_backward_groups(int64_t m, int64_t n);
+adahop_status act_backward_launch(const void* dout, int d_f32, const uint16_t* z, int act, int gated,
+                                  int64_t m, int64_t n, int64_t lddo, int64_t ldz, uint16_t* dz,
+                                  int64_t lddz, float* dbias, float* partial, hipStream_t stream);
+
+struct LinearArgs {
+  const uint8_t* a_codes;
+  const uint8_t* a_scales;
+  const uint8_t* b_codes;
+  const uint8_t* b_scales;
+  int64_t lda, ldas, ldb, ldbs;
+  int64_t m, n, K;           // n: output columns (gated: B has 2 n rows)
+  const void* bias;          // [N] or null
+  int bias_f32;
+  int act;                   // adahop_act
+  const uint16_t* residual;  // bf16 [m][n] or null
+  int64_t ldr;
+  void* out;                 // bf16, or E4M3 codes with out_scales
+  int64_t ldo;
+  uint8_t* out_scales;       // null for a bf16 output
+  int64_t ldos;
+  uint16_t* z;               // bf16 [m][N] or null
+  int64_t ldz;
+};
+size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated);
+adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* scratch,
+                               size_t scratch_bytes, hipStream_t stream);
+
 }  // namespace adahop

@@ -1,0 +1,409 @@
+// RMS norm with the residual's addition and an MXFP8 output, its backward
+// pass, and the MXFP8 quantizer / dequantizer (gfx950).
+//
+//   h = x + r (rounded to the stream's type), s = 1 / sqrt(mean(h^2) + eps),
+//   y = h * s * gain, stored as MXFP8 and / or bf16.
+// All are bound by HBM: every operand is read once and every result written
+// once, with a row's values held in registers between the sum of squares and
+// the scaling. Sums run in fp32 along fixed trees: results do not change from
+// run to run.
+#include "adahop_internal.h"
+#include "mx8_common.h"
+
+namespace adahop {
+namespace {
+
+using namespace mx8;
+
+struct NormArgs {
+  const void* x;
+  const void* r;
+  const void* gain;
+  int gain_f32;
+  int64_t rows, cols;
+  int64_t ldx, ldr, ldh, ldy, ldc, lds;
+  float eps;
+  void* h;
+  uint16_t* y;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* rstd;
+};
+
+// Sum over a workgroup of Waves waves, in every thread (one barrier).
+template <int Waves>
+__device__ __forceinline__ float group_sum(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (Waves > 1) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < Waves; ++w) v += red[w];
+  }
+  return v;
+}
+
+__device__ __forceinline__ void load_gain(const void* gain, int f32, int64_t c, int64_t cols,
+                                          float (&g)[8]) {
+  if (f32)
+    load_group<true>(static_cast<const float*>(gain), c, cols, g);
+  else
+    load_group<false>(static_cast<const uint16_t*>(gain), c, cols, g);
+}
+
+// XF32: x in fp32; Res: 0 none, 1 bf16, 2 fp32 residual stream. A row is
+// spread over Waves waves, each thread holding NV groups of 8 columns; with
+// Waves == 1 a workgroup takes 4 rows, one a wave, and needs no barrier.
+template <bool XF32, int Res, int Waves, int NV>
+__global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
+    rmsnorm_kernel(NormArgs a) {
+  constexpr bool RF32 = Res == 2;
+  using TX = typename Elem<XF32>::type;
+  using TR = typename Elem<RF32>::type;
+  constexpr int T = Waves == 1 ? 64 : 64 * Waves;
+  __shared__ float red[Waves];
+  const int64_t row = Waves == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (Waves == 1 && row >= a.rows) return;
+  const int t = Waves == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const TX* x = static_cast<const TX*>(a.x) + row * a.ldx;
+  float v[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) load_group<XF32>(x, 8 * (int64_t)(t + k * T), a.cols, v[k]);
+  if constexpr (Res != 0) {
+    const TR* r = static_cast<const TR*>(a.r) + row * a.ldr;
+    float q[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) load_group<RF32>(r, 8 * (int64_t)(t + k * T), a.cols, q[k]);
+    TR* h = static_cast<TR*>(a.h) + row * a.ldh;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      // The norm takes h as the stream holds it (rounded to its type), so
+      // that the backward pass, which reads h, differentiates what was run.
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] = Elem<RF32>::rounded(v[k][i] + q[k][i]);
+      store_group<RF32>(h, 8 * (int64_t)(t + k * T), a.cols, v[k]);
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(v[k][i], v[k][i], s);
+  s = group_sum<Waves>(s, red);
+  const float rstd = 1.0f / sqrtf(s / (float)a.cols + a.eps);
+  if (a.rstd != nullptr && t == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = 8 * (int64_t)(t + k * T);
+    float g[8];
+    load_gain(a.gain, a.gain_f32, c, a.cols, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * rstd * g[i];
+    if (a.y != nullptr) store_group<false>(a.y + row * a.ldy, c, a.cols, v[k]);
+    if (a.codes != nullptr && c < a.cols)
+      mx8_store_quad(v[k], a.codes + row * a.ldc + c, a.scales + row * a.lds + c / 32);
+  }
+}
+
+// ---- backward ---------------------------------------------------------------
+struct NormBackArgs {
+  const void* dy;
+  const void* h;
+  const void* gain;
+  int gain_f32;
+  const float* rstd;
+  const void* dh;
+  int64_t rows, cols;
+  int64_t lddy, ldh, lddh, lddx;
+  void* dx;
+  float* partial;     // [workgroups][cols], or null without dgain
+};
+
+// With n = h * s and u = gain * dy:  dx = dh + s * (u - n * mean(u * n)),
+// and a workgroup's part of dgain = sum over its rows of dy * n, which stays
+// in registers over all rows that the workgroup takes (every gridDim.x-th
+// group of rows) and goes out once.
+template <bool DyF32, bool HF32, int Waves, int NV>
+__global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
+    rmsnorm_backward_kernel(NormBackArgs a) {
+  using TD = typename Elem<DyF32>::type;
+  using TH = typename Elem<HF32>::type;
+  constexpr int T = Waves == 1 ? 64 : 64 * Waves;
+  constexpr int RowsPer = Waves == 1 ? 4 : 1;
+  __shared__ float red[2][Waves];
+  __shared__ float part[Waves == 1 ? 3 * 64 * 8 : 1];
+  const int wave = threadIdx.x >> 6;
+  const int t = Waves == 1 ? threadIdx.x & 63 : threadIdx.x;
+  float acc[NV][8], g[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    load_gain(a.gain, a.gain_f32, 8 * (int64_t)(t + k * T), a.cols, g[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[k][i] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RowsPer + (Waves == 1 ? wave : 0); row < a.rows;
+       row += (int64_t)gridDim.x * RowsPer, turn ^= 1) {
+    const TD* dy = static_cast<const TD*>(a.dy) + row * a.lddy;
+    const TH* h = static_cast<const TH*>(a.h) + row * a.ldh;
+    float u[NV][8], n[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) load_group<DyF32>(dy, 8 * (int64_t)(t + k * T), a.cols, u[k]);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) load_group<HF32>(h, 8 * (int64_t)(t + k * T), a.cols, n[k]);
+    float e[NV][8];
+    if (a.dh != nullptr) {
+      const TH* dh = static_cast<const TH*>(a.dh) + row * a.lddh;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) load_group<HF32>(dh, 8 * (int64_t)(t + k * T), a.cols, e[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[k][i] = 0.0f;
+    }
+    const float s = a.rstd[row];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[k][i] *= s;
+        acc[k][i] = __builtin_fmaf(u[k][i], n[k][i], acc[k][i]);
+        u[k][i] *= g[k][i];
+        sum = __builtin_fmaf(u[k][i], n[k][i], sum);
+      }
+    // Two sets of partial sums in turn: a wave that is a row ahead writes
+    // the other set, and is held at that row's barrier until all have read.
+    const float c = group_sum<Waves>(sum, red[turn]) / (float)a.cols;
+    TH* dx = static_cast<TH*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[k][i] += s * (u[k][i] - n[k][i] * c);
+      store_group<HF32>(dx, 8 * (int64_t)(t + k * T), a.cols, e[k]);
+    }
+  }
+  if (a.partial == nullptr) return;
+  float* out = a.partial + (int64_t)blockIdx.x * a.cols;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t c = 8 * (int64_t)(t + k * T);
+    if constexpr (Waves == 1) {
+      // The four waves' parts of the same columns, added in wave order.
+      __syncthreads();
+      if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[(wave - 1) * 512 + i * 64 + t] = acc[k][i];
+      }
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          acc[k][i] = ((acc[k][i] + part[i * 64 + t]) + part[512 + i * 64 + t]) + part[1024 + i * 64 + t];
+      }
+    }
+    if (Waves > 1 || wave == 0) store_group<true>(out, c, a.cols, acc[k]);
+  }
+}
+
+// out[c] = sum over p of partial[p][c]: a workgroup takes 64 columns, its 16
+// waves every 16th part; the waves' sums are added in wave order.
+__global__ void __launch_bounds__(1024) column_reduce_kernel(const float* __restrict__ partial,
+                                                             int parts, int64_t cols,
+                                                             float* __restrict__ out) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int p = wave; p < parts; p += 16) s += partial[(int64_t)p * cols + c];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    out[c] = s;
+  }
+}
+
+// ---- quantizer and dequantizer ----------------------------------------------
+struct Mx8Args {
+  const void* src;
+  int64_t ld;
+  int64_t rows, cols;      // cols a multiple of 32
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ldc, lds;
+  void* dst;               // dequantizer's output
+  int64_t ldd;
+};
+
+// Group of 8 elements `i` of the matrix: its row and first column.
+__device__ __forceinline__ void group_at(int64_t i, int64_t rows, int64_t cols, int64_t* r, int64_t* c) {
+  if (rows == 1) {
+    *r = 0;
+    *c = 8 * i;
+  } else if (rows * (cols / 8) < (1LL << 31)) {
+    const uint32_t per = (uint32_t)(cols / 8), q = (uint32_t)i / per;
+    *r = q;
+    *c = 8 * (int64_t)((uint32_t)i - q * per);
+  } else {
+    *r = i / (cols / 8);
+    *c = 8 * (i - *r * (cols / 8));
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(256) mx8_quant_kernel(Mx8Args a) {
+  using TS = typename Elem<F32>::type;
+  const int64_t n = a.rows * (a.cols / 8);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    int64_t r, c;
+    group_at(i, a.rows, a.cols, &r, &c);
+    float v[8];
+    Elem<F32>::load8(static_cast<const TS*>(a.src) + r * a.ld + c, v);
+    mx8_store_quad(v, a.codes + r * a.ldc + c, a.scales + r * a.lds + c / 32);
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(256) mx8_dequant_kernel(Mx8Args a) {
+  using TD = typename Elem<F32>::type;
+  const int64_t n = a.rows * (a.cols / 8);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    int64_t r, c;
+    group_at(i, a.rows, a.cols, &r, &c);
+    u32x2 w;
+    __builtin_memcpy(&w, a.codes + r * a.ldc + c, 8);
+    const float s = mx8_scale(a.scales[r * a.lds + c / 32]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
+      const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+      v[4 * j] = lo[0] * s;
+      v[4 * j + 1] = lo[1] * s;
+      v[4 * j + 2] = hi[0] * s;
+      v[4 * j + 3] = hi[1] * s;
+    }
+    Elem<F32>::store8(static_cast<TD*>(a.dst) + r * a.ldd + c, v);
+  }
+}
+
+int flat_grid(int64_t groups) {
+  const int64_t wg = (groups + 255) / 256;
+  return (int)(wg < 1 ? 1 : wg < 16384 ? wg : 16384);
+}
+
+template <bool XF32, int Res>
+adahop_status norm_dispatch(const NormArgs& a, hipStream_t stream) {
+  const int64_t c = a.cols;
+  // Up to 2048 columns a wave holds a row; above, 4 waves, then 16, share it:
+  // at most 4 groups of 8 columns a thread.
+#define ADAHOP_NORM(WAVES, NV)                                                                   \
+  rmsnorm_kernel<XF32, Res, WAVES, NV>                                                           \
+      <<<dim3((unsigned)(WAVES == 1 ? (a.rows + 3) / 4 : a.rows)), dim3(WAVES == 1 ? 256 : 64 * WAVES), 0, \
+         stream>>>(a)
+  if (c <= 512) ADAHOP_NORM(1, 1);
+  else if (c <= 1024) ADAHOP_NORM(1, 2);
+  else if (c <= 2048) ADAHOP_NORM(1, 4);
+  else if (c <= 4096) ADAHOP_NORM(4, 2);
+  else if (c <= 8192) ADAHOP_NORM(4, 4);
+  else if (c <= 16384) ADAHOP_NORM(16, 2);
+  else ADAHOP_NORM(16, 4);
+#undef ADAHOP_NORM
+  return check_launch("rmsnorm");
+}
+
+template <bool DyF32, bool HF32>
+adahop_status norm_back_dispatch(const NormBackArgs& a, int grid, hipStream_t stream) {
+  const int64_t c = a.cols;
+#define ADAHOP_NORM_BACK(WAVES, NV)                                                              \
+  rmsnorm_backward_kernel<DyF32, HF32, WAVES, NV>                                                \
+      <<<dim3((unsigned)grid), dim3(WAVES == 1 ? 256 : 64 * WAVES), 0, stream>>>(a)
+  if (c <= 512) ADAHOP_NORM_BACK(1, 1);
+  else if (c <= 1024) ADAHOP_NORM_BACK(1, 2);
+  else if (c <= 2048) ADAHOP_NORM_BACK(1, 4);
+  else if (c <= 4096) ADAHOP_NORM_BACK(4, 2);
+  else if (c <= 8192) ADAHOP_NORM_BACK(8, 2);
+  else if (c <= 16384) ADAHOP_NORM_BACK(16, 2);
+  else ADAHOP_NORM_BACK(16, 4);
+#undef ADAHOP_NORM_BACK
+  return check_launch("rmsnorm_backward");
+}
+
+}  // namespace
+
+adahop_status rmsnorm_launch(const void* x, int x_f32, const void* r, int r_f32, const void* gain,
+                             int gain_f32, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                             float eps, void* h, int64_t ldh, uint16_t* y, int64_t ldy,
+                             uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds, float* rstd,
+                             hipStream_t stream) {
+  if (rows == 0) return ADAHOP_OK;
+  const NormArgs a = {x, r, gain, gain_f32, rows, cols, ldx, ldr, ldh, ldy, ldc, lds,
+                      eps, h, y, codes, scales, rstd};
+  if (r == nullptr) return x_f32 ? norm_dispatch<true, 0>(a, stream) : norm_dispatch<false, 0>(a, stream);
+  if (x_f32) return r_f32 ? norm_dispatch<true, 2>(a, stream) : norm_dispatch<true, 1>(a, stream);
+  return r_f32 ? norm_dispatch<false, 2>(a, stream) : norm_dispatch<false, 1>(a, stream);
+}
+
+int rmsnorm_backward_groups(int64_t rows, int64_t cols) {
+  const int64_t need = cols <= 2048 ? (rows + 3) / 4 : rows;
+  const int64_t most = 1024;
+  return (int)(need < 1 ? 1 : need < most ? need : most);
+}
+
+adahop_status rmsnorm_backward_launch(const void* dy, int dy_f32, const void* h, int h_f32,
+                                      const void* gain, int gain_f32, const float* rstd,
+                                      const void* dh, int64_t rows, int64_t cols, int64_t lddy,
+                                      int64_t ldh, int64_t lddh, int64_t lddx, void* dx,
+                                      float* dgain, float* partial, hipStream_t stream) {
+  const int grid = rmsnorm_backward_groups(rows, cols);
+  const NormBackArgs a = {dy, h, gain, gain_f32, rstd, dh, rows, cols, lddy, ldh, lddh, lddx, dx,
+                          dgain != nullptr ? partial : nullptr};
+  adahop_status st;
+  if (dy_f32) st = h_f32 ? norm_back_dispatch<true, true>(a, grid, stream)
+                         : norm_back_dispatch<true, false>(a, grid, stream);
+  else st = h_f32 ? norm_back_dispatch<false, true>(a, grid, stream)
+                  : norm_back_dispatch<false, false>(a, grid, stream);
+  if (st != ADAHOP_OK || dgain == nullptr) return st;
+  return column_reduce_launch(partial, grid, cols, dgain, stream);
+}
+
+adahop_status column_reduce_launch(const float* partial, int parts, int64_t cols, float* out,
+                                   hipStream_t stream) {
+  column_reduce_kernel<<<dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, stream>>>(partial, parts,
+                                                                                      cols, out);
+  return check_launch("column_reduce");
+}
+
+adahop_status mx8_quant_launch(const void* src, int f32, int64_t rows, int64_t cols, int64_t ld,
+                               uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds,
+                               hipStream_t stream) {
+  if (rows == 0) return ADAHOP_OK;
+  if (ld == cols && ldc == cols && lds == cols / 32) { cols *= rows; rows = 1; }
+  const Mx8Args a = {src, ld, rows, cols, codes, scales, ldc, lds, nullptr, 0};
+  const dim3 grid((unsigned)flat_grid(rows * (cols / 8)));
+  if (f32) mx8_quant_kernel<true><<<grid, dim3(256), 0, stream>>>(a);
+  else mx8_quant_kernel<false><<<grid, dim3(256), 0, stream>>>(a);
+  return check_launch("mx8_quant");
+}
+
+adahop_status mx8_dequant_launch(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds,
+                                 int64_t rows, int64_t cols, void* dst, int f32, int64_t ldd,
+                                 hipStream_t stream) {
+  if (rows == 0) return ADAHOP_OK;
+  if (ldd == cols && ldc == cols && lds == cols / 32) { cols *= rows; rows = 1; }
+  const Mx8Args a = {nullptr, 0, rows, cols, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales),
+                     ldc, lds, dst, ldd};
+  const dim3 grid((unsigned)flat_grid(rows * (cols / 8)));
+  if (f32) mx8_dequant_kernel<true><<<grid, dim3(256), 0, stream>>>(a);
+  else mx8_dequant_kernel<false><<<grid, dim3(256), 0, stream>>>(a);
+  return check_launch("mx8_dequant");
+}
+
+}  // namespace adahop

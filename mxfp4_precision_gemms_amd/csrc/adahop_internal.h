@@ -178,6 +178,9 @@ adahop_status gemm_mx_launch(const uint8_t* a_codes, const uint8_t* a_scales,
 // split fixup, the outlier scatter).
 adahop_status record_main_done(hipEvent_t main_done, hipStream_t stream, const char* what);
 
+// Compute units of the current device.
+int64_t device_cus();
+
 // ---- norm, quantizer and linear layer in MXFP8 ------------------------------
 // Arguments as the public entry points', already checked; leading dimensions
 // in elements (codes and scales in bytes).
@@ -229,6 +232,20 @@ struct LinearArgs {
   uint16_t* z;               // bf16 [m][N] or null
   int64_t ldz;
 };
+// Tile kernel of a product (linear_tiles.hip) and its workspace: scale words
+// by stage, then the K parts' sums.
+enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+struct TilePlan {
+  TileShape shape;
+  int parts;
+  size_t scale_bytes, part_bytes;
+};
+TilePlan linear_tile_plan(int64_t m, int64_t n, int64_t K, int b_fp4, int gated);
+// Whether the rows of a matrix, a tile's rows past its end included, lie
+// within the 31-bit offsets that the tile kernel uses.
+bool linear_tiles_reach(int64_t rows, int64_t ld);
+adahop_status linear_tiles_launch(const LinearArgs& a, int b_fp4, int gated, const TilePlan& p, void* scratch,
+                                  hipStream_t stream);
 size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated);
 adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* scratch,
                                size_t scratch_bytes, hipStream_t stream);

@@ -19,7 +19,7 @@
 // The sums over K, the bias, the activation and the residual are in fp32;
 // one rounding to the output.
 #include "adahop_internal.h"
-#include "mx8_common.h"
+#include "linear_epilogue.h"
 
 namespace adahop {
 namespace {
@@ -28,59 +28,6 @@ using namespace mx8;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ float act_runtime(int act, float z) {
-  switch (act) {
-    case kActRelu: return act_value<kActRelu>(z);
-    case kActSilu: return act_value<kActSilu>(z);
-    case kActGelu: return act_value<kActGelu>(z);
-    case kActGeluTanh: return act_value<kActGeluTanh>(z);
-    default: return z;
-  }
-}
-
-__device__ __forceinline__ void add_bias(const LinearArgs& a, int64_t c, int64_t end, float (&z)[8]) {
-  float b[8];
-  if (a.bias_f32)
-    load_group<true>(static_cast<const float*>(a.bias), c, end, b);
-  else
-    load_group<false>(static_cast<const uint16_t*>(a.bias), c, end, b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] += b[i];
-}
-
-// Epilogue of columns c .. c + 7 (c a multiple of 8, below n) of row r: z
-// (and, gated, up) hold the products. For an MXFP8 output (n a multiple of
-// 32) the four lanes of a quad hold the four groups of one block.
-template <bool Gated>
-__device__ __forceinline__ void epilogue8(const LinearArgs& a, int64_t r, int64_t c, float (&z)[8],
-                                          float (&up)[8]) {
-  if (a.bias != nullptr) {
-    add_bias(a, c, a.n, z);
-    if constexpr (Gated) add_bias(a, a.n + c, 2 * a.n, up);
-  }
-  if (a.z != nullptr) {
-    store_group<false>(a.z + r * a.ldz, c, a.n, z);
-    if constexpr (Gated) store_group<false>(a.z + r * a.ldz + a.n, c, a.n, up);
-  }
-  float o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    o[i] = act_runtime(a.act, z[i]);
-    if constexpr (Gated) o[i] *= up[i];
-  }
-  if (a.residual != nullptr) {
-    float e[8];
-    load_group<false>(a.residual + r * a.ldr, c, a.n, e);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] += e[i];
-  }
-  if (a.out_scales != nullptr)
-    mx8_store_quad(o, static_cast<uint8_t*>(a.out) + r * a.ldo + c, a.out_scales + r * a.ldos + c / 32);
-  else
-    store_group<false>(static_cast<uint16_t*>(a.out) + r * a.ldo, c, a.n, o);
-}
 
 // ---- few rows ---------------------------------------------------------------
 // A workgroup computes 16 MT rows by 32 columns of the output (gated: 32 gate
@@ -209,15 +156,71 @@ adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
   return check_launch("linear_mx");
 }
 
-}  // namespace
+// Up to kFewRows rows the weights are streamed once past all of them.
+constexpr int64_t kFewRows = 32;
 
-size_t linear_mx_scratch_bytes(int64_t, int64_t, int64_t, int, int) { return 0; }
-
-adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void*, size_t,
-                               hipStream_t stream) {
-  if (a.m == 0) return ADAHOP_OK;
+adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t stream) {
   if (b_fp4) return gated ? few_dispatch<true, true>(a, stream) : few_dispatch<true, false>(a, stream);
   return gated ? few_dispatch<false, true>(a, stream) : few_dispatch<false, false>(a, stream);
+}
+
+// Rows r0 .. r0 + rows - 1 and output columns c0 .. c0 + cols - 1 (a multiple
+// of 32, and all of them for a gated layer).
+LinearArgs part_of(const LinearArgs& a, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+  LinearArgs p = a;
+  p.m = rows;
+  p.n = cols;
+  p.a_codes += r0 * a.lda;
+  p.a_scales += r0 * a.ldas;
+  p.b_codes += c0 * a.ldb;
+  p.b_scales += c0 * a.ldbs;
+  if (a.bias) p.bias = static_cast<const char*>(a.bias) + c0 * (a.bias_f32 ? 4 : 2);
+  if (a.residual) p.residual += r0 * a.ldr + c0;
+  p.out = static_cast<char*>(a.out) + (r0 * a.ldo + c0) * (a.out_scales ? 1 : 2);
+  if (a.out_scales) p.out_scales += r0 * a.ldos + c0 / 32;
+  if (a.z) p.z += r0 * a.ldz + c0;
+  return p;
+}
+
+}  // namespace
+
+size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
+  if (m <= kFewRows) return 0;
+  const TilePlan p = linear_tile_plan(m, n, K, b_fp4, gated);
+  return p.scale_bytes + p.part_bytes;
+}
+
+adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* scratch, size_t,
+                               hipStream_t stream) {
+  if (a.m == 0) return ADAHOP_OK;
+  if (a.m <= kFewRows) return few_launch(a, b_fp4, gated, stream);
+  if (linear_tiles_reach(a.m, a.lda) && linear_tiles_reach(a.n, a.ldb))
+    return linear_tiles_launch(a, b_fp4, gated, linear_tile_plan(a.m, a.n, a.K, b_fp4, gated), scratch, stream);
+  // Operands of 2 GB and more: in pieces that the tile kernel's offsets
+  // reach. Rows 4 MB apart and gated weights of 2 GB a part go by the
+  // streaming kernel, in launches that fit its grid.
+  auto most = [](int64_t rows, int64_t ld) {
+    if (linear_tiles_reach(rows, ld)) return rows;
+    int64_t c = ((int64_t{1} << 31) / ld - 1024) / 512 * 512;
+    return c > 0 && linear_tiles_reach(c, ld) ? c : int64_t{0};
+  };
+  const int64_t rows = most(a.m, a.lda), cols = most(a.n, a.ldb);
+  const bool tiles = rows > 0 && cols > 0 && (!gated || cols == a.n);
+  const int64_t dr = tiles ? rows : int64_t{1} << 20, dc = tiles ? cols : a.n;
+  for (int64_t r = 0; r < a.m; r += dr)
+    for (int64_t c = 0; c < a.n; c += dc) {
+      const LinearArgs p = part_of(a, r, a.m - r < dr ? a.m - r : dr, c, a.n - c < dc ? a.n - c : dc);
+      adahop_status st;
+      if (tiles) {
+        TilePlan t = linear_tile_plan(p.m, p.n, p.K, b_fp4, gated);
+        t.parts = 1;
+        st = linear_tiles_launch(p, b_fp4, gated, t, scratch, stream);
+      } else {
+        st = few_launch(p, b_fp4, gated, stream);
+      }
+      if (st != ADAHOP_OK) return st;
+    }
+  return ADAHOP_OK;
 }
 
 }  // namespace adahop

@@ -1,0 +1,101 @@
+"""The linear layer's tile kernels at sizes that take each of their shapes:
+whole and ragged tiles, several tiles a workgroup, one stage of K to many,
+odd numbers of stages, K that ends inside a stage. Rows that lie on and next
+to the tiles' borders are compared with the definition in 64 bits; tolerances
+as derived in test_gpu_linear.py."""
+import pytest
+import torch
+
+import mxfp4_precision_gemms_amd as A
+from test_gpu_linear import BF, DEV, DT, activations, check_mx8, linear_ref, rand, strided, weights
+
+pytestmark = pytest.mark.gpu
+
+
+def some_rows(m):
+    at = {0, 1, m - 1, m // 2}
+    for edge in (16, 31, 32, 63, 64, 127, 128, 255, 256, 511, 512, m // 256 * 256):
+        at |= {edge - 1, edge}
+    return torch.tensor(sorted(r for r in at if 0 <= r < m))
+
+
+def check(m, n, K, fmt, act="NONE", gated=False, bias=None, residual=False, mx8=False, save_z=False,
+          strides=False, seed=100):
+    N = 2 * n if gated else n
+    a, va = activations(m, K, seed)
+    b, vb = weights(N, K, fmt, seed + 1)
+    bv = None if bias is None else rand(N, seed=seed + 2).to(DT[bias])
+    res = rand(m, n, seed=seed + 3, std=4.0, dtype=torch.bfloat16) if residual else None
+    if strides:
+        a = (strided(a[0].cpu(), 32), strided(a[1].cpu(), 5, 3))
+        b = (strided(b[0].cpu(), 16), strided(b[1].cpu(), 3, 1))
+    got = A.adahop_linear_mx(a, b, bias=None if bv is None else bv.to(DEV), act=act, gated=gated,
+                             residual=None if res is None else res.to(DEV),
+                             out_dtype="MXFP8" if mx8 else torch.bfloat16, save_z=save_z)
+    at = some_rows(m)
+    z, dz, out, dout = linear_ref(va[at], vb, bv, act, gated, None if res is None else res[at])
+    if save_z:
+        err = (got.z.cpu()[at].double() - z).abs()
+        assert bool((err <= dz + BF * (z.abs() + dz)).all())
+    if mx8:
+        check_mx8(got.out.cpu()[at], got.scales.cpu()[at], out, dout)
+    else:
+        err = (got.out.cpu()[at].double() - out).abs()
+        assert bool((err <= dout + BF * (out.abs() + dout)).all())
+
+
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m,n,K", [
+    (33, 32, 32), (40, 70, 128), (63, 129, 256), (64, 256, 384), (129, 500, 1184),     # 64 rows
+    (700, 2100, 160), (1000, 1700, 640), (1536, 1536, 544),                            # 128 rows
+    (2100, 5410, 288), (4096, 4096, 128), (4200, 4200, 96), (2049, 6200, 1024),        # 256 rows
+])
+def test_tiles(m, n, K, fmt, gated):
+    check(m, n, K, fmt, act="SILU" if gated else "NONE", gated=gated, save_z=m < 1000, residual=n % 4 == 0)
+
+
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+@pytest.mark.parametrize("m,n,K", [(50, 96, 288), (1100, 1824, 416), (2300, 5600, 224), (4300, 4160, 512)])
+def test_tiles_mx8_out(m, n, K, fmt):
+    check(m, n, K, fmt, act="GELU", bias="f32", mx8=True)
+    check(m, n // 64 * 32, K, fmt, act="SILU", gated=True, bias="bf16", mx8=True)
+
+
+@pytest.mark.parametrize("act", list(A.ACT))
+@pytest.mark.parametrize("m,n,K", [(2200, 5200, 128), (1100, 1800, 96)])
+def test_tiles_epilogues(m, n, K, act):
+    check(m, n, K, "MXFP4", act=act, bias="f32", residual=True, save_z=True)
+    check(m, n // 2, K, "MXFP8", act=act, gated=True, bias="bf16", residual=True, save_z=True)
+
+
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+@pytest.mark.parametrize("m,n,K", [(90, 210, 192), (1100, 1800, 256), (2200, 5200, 384)])
+def test_tiles_strides(m, n, K, fmt):
+    """Operands inside larger buffers whose other bytes are NaN."""
+    check(m, n, K, fmt, strides=True, residual=True)
+
+
+@pytest.mark.parametrize("m,n", [(100, 320), (1200, 1600), (2400, 5200)])
+def test_tiles_non_finite(m, n):
+    """A NaN or an infinity reaches its own row and no other; the codes that
+    follow a row in memory are another row's, some of them NaN."""
+    K = 160
+    x = rand(m, K, seed=110)
+    bad_rows = [3, m // 2, m - 1]
+    x[bad_rows[0], 5], x[bad_rows[1], K - 1], x[bad_rows[2], 0] = float("nan"), float("inf"), float("-inf")
+    a = A.adahop_mx8_quant(x.to(DEV))
+    b, _ = weights(n, K, "MXFP8", 111)
+    bad = A.adahop_linear_mx(a, b).out.isnan().cpu()
+    want = torch.zeros(m, dtype=torch.bool)
+    want[bad_rows] = True
+    assert torch.equal(bad.all(1), want) and torch.equal(bad.any(1), want)
+
+
+def test_tiles_deterministic():
+    for m, n, K in ((100, 512, 8192), (1024, 2048, 1024), (2048, 8192, 512)):
+        a, _ = activations(m, K, 112)
+        b, _ = weights(n, K, "MXFP4", 113)
+        first = A.adahop_linear_mx(a, b).out
+        for _ in range(3):
+            assert torch.equal(A.adahop_linear_mx(a, b).out, first)

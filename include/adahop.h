@@ -576,13 +576,15 @@ typedef enum {
  * (out: codes, ld_out bytes; n a multiple of 32). z (bf16 [m, N], or NULL)
  * keeps z for adahop_act_backward. residual is bf16 and may be out itself.
  * Needs adahop_linear_mx_workspace_size(...) bytes of 16-byte aligned
- * workspace (0 for most sizes).
+ * workspace (0 for few rows, else the scales in another order and, where K is
+ * split, the parts' sums).
  * Errors: INVALID for NULL operands or out (m > 0), m < 0, N or K < 1, K not
  * a multiple of 32, leading dimensions too small, N odd with gated, n not a
  * multiple of 32 with an MXFP8 output, a bad format, dtype or activation,
  * reserved not 0; UNSUPPORTED for codes of A or B that are not 16-byte
- * aligned or whose leading dimension is not a multiple of 16, and for m, N or
- * K of 2^30 and more; WORKSPACE. */
+ * aligned or whose leading dimension is not a multiple of 16, for m, N or K of
+ * 2^30 and more, and for leading dimensions of B's codes or scales of 2^25
+ * bytes and more; WORKSPACE. */
 typedef struct {
   int64_t m, N, K;
   const uint8_t* a_codes; int64_t ld_a_codes;

@@ -167,7 +167,9 @@ def _check(status: int):
 
 
 def _stream(device=None) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream's handle (without a Stream object: 0.1 us for 2)."""
+    index = None if device is None else device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _bf16_ptr(t: torch.Tensor, name: str) -> int:

@@ -178,8 +178,8 @@ adahop_status gemm_mx_launch(const uint8_t* a_codes, const uint8_t* a_scales,
 // split fixup, the outlier scatter).
 adahop_status record_main_done(hipEvent_t main_done, hipStream_t stream, const char* what);
 
-// Compute units of the current device.
-int64_t device_cus();
+// Compute units of the current device (256 where none can be asked).
+int64_t compute_units();
 
 // ---- norm, quantizer and linear layer in MXFP8 ------------------------------
 // Arguments as the public entry points', already checked; leading dimensions
@@ -234,11 +234,12 @@ struct LinearArgs {
 };
 // Tile kernel of a product (linear_tiles.hip) and its workspace: scale words
 // by stage, then the K parts' sums.
-enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2 };
+enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile32 = 3 };
 struct TilePlan {
   TileShape shape;
   int parts;
   size_t scale_bytes, part_bytes;
+  double us;                 // estimate
 };
 TilePlan linear_tile_plan(int64_t m, int64_t n, int64_t K, int b_fp4, int gated);
 // Whether the rows of a matrix, a tile's rows past its end included, lie

@@ -1628,8 +1628,6 @@ bool ring_shape_ok(int64_t m, int64_t n, int64_t K) {
 // device's, queried once per device (256 on a whole gfx950, and when no
 // device can be queried, e.g. for a plan made without a GPU).
 constexpr int64_t kDefaultCUs = 256;
-}  // namespace
-
 int64_t device_cus() {
   static std::mutex mu;
   static int cus[64] = {};
@@ -1649,9 +1647,6 @@ int64_t device_cus() {
   }
   return cus[dev];
 }
-
-namespace {
-
 struct TailSplit {
   int64_t full, split;   // whole tiles, split tiles
   int parts;

@@ -30,134 +30,221 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 
 // ---- few rows ---------------------------------------------------------------
-// A workgroup computes 16 MT rows by 32 columns of the output (gated: 32 gate
-// and 32 up rows of B), its 8 waves each taking every 8th run of 512 along K
-// straight from memory into registers; their sums meet in LDS and one wave
-// per 16 rows finishes. B is read once, by the workgroup that owns its rows.
-constexpr int kFewWaves = 8;
+// A workgroup computes 16 MT rows by 16 NB columns of the output (gated: 16 NB
+// gate and as many up rows of B). Its WV waves each take every WV-th run of
+// 128 T elements along K straight from memory into registers, the next run's
+// loads issued before a run's products; their sums meet in LDS, added in wave
+// order. B is read once, by the workgroup that owns its rows: bound by HBM,
+// and by the bytes in flight that the registers of all waves hold.
+template <bool FP4, int MT, int NF, int T>
+struct Run {
+  v4i a[MT][T][2];
+  v4i b[NF][T][FP4 ? 1 : 2];
+  uint32_t sa[MT][T], sb[NF][T];
+};
 
-template <bool FP4, bool Gated, int MT>
-__global__ void __launch_bounds__(64 * kFewWaves) linear_few_kernel(LinearArgs a) {
-  constexpr int NB = Gated ? 4 : 2;         // 16-row blocks of B
-  constexpr int Pitch = NB * 16 + 4;
-  __shared__ float red[kFewWaves][MT * 16][Pitch];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+constexpr int kBufferFlags = 0x00020000;   // raw buffer descriptor word 3
+constexpr int kPastEnd = 0x7FFFFFF0;       // an offset past the end of every buffer here
+
+template <bool FP4, bool Gated, int MT, int NB, int WV, int T>
+__global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
+  constexpr int NF = Gated ? 2 * NB : NB;   // 16-row blocks of B
+  constexpr int Cols = 16 * NF, Pitch = Cols + 4, KR = 128 * T;
+  __shared__ float red[WV][MT * 16][Pitch];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 32, m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NB), m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int K = (int)a.K, Kb = FP4 ? K / 2 : K;
+  // A's rows may lie far apart: a pointer each; rows past the end repeat the
+  // last one (what they give is not stored). B's 16 NB rows of a part are a
+  // buffer, past whose end loads return 0.
   const uint8_t* ac[MT];
   const uint8_t* as[MT];
-  const uint8_t* bc[NB];
-  const uint8_t* bs[NB];
-  // Rows past the end repeat the last one: what they give is not stored.
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     int64_t r = m0 + 16 * i + r16;
     r = r < a.m ? r : a.m - 1;
-    ac[i] = a.a_codes + r * a.lda;
+    ac[i] = a.a_codes + r * a.lda + 16 * g;
     as[i] = a.a_scales + r * a.ldas;
   }
+  const int rows_b = (int)(a.n - n0 < 16 * NB ? a.n - n0 : 16 * NB);
+  auto part = [&](const uint8_t* p, int64_t ld, int bytes, int up) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + (n0 + up * a.n) * ld), 0,
+                                             (int)((rows_b - 1) * ld) + bytes, kBufferFlags);
+  };
+  const __amdgpu_buffer_rsrc_t bc0 = part(a.b_codes, a.ldb, Kb, 0), bs0 = part(a.b_scales, a.ldbs, K / 32, 0);
+  const __amdgpu_buffer_rsrc_t bc1 = part(a.b_codes, a.ldb, Kb, Gated), bs1 = part(a.b_scales, a.ldbs, K / 32, Gated);
+  int oc[NB], os[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    int64_t c = n0 + 16 * (j & 1) + r16;
-    c = (c < a.n ? c : a.n - 1) + (j >= 2 ? a.n : 0);
-    bc[j] = a.b_codes + c * a.ldb;
-    bs[j] = a.b_scales + c * a.ldbs;
+    oc[j] = (16 * j + r16) * (int)a.ldb + 16 * g;
+    os[j] = (16 * j + r16) * (int)a.ldbs;
   }
-  v4f acc[MT][NB];
+  v4f acc[MT][NF];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    for (int j = 0; j < NF; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-  const v4i zero = {0, 0, 0, 0};
-  for (int64_t k0 = 512 * (int64_t)wave; k0 < a.K; k0 += 512 * kFewWaves) {
-    const bool full = k0 + 512 <= a.K;
-    uint32_t sa[MT][4], sb[NB][4];
-    auto scales = [&](const uint8_t* row, uint32_t (&s)[4]) {
-      if (full) {
-        u32x4 w;
-        __builtin_memcpy(&w, row + k0 / 32, 16);
+  using R = Run<FP4, MT, NF, T>;
+  auto load = [&](R& r, int k0) {
+    const v4i zero = {0, 0, 0, 0};
+    const bool full = k0 + KR <= K;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) s[t] = w[t] >> (8 * g);
-      } else {
+    for (int j = 0; j < NF; ++j)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) s[t] = k0 + 128 * t + 32 * g < a.K ? row[k0 / 32 + 4 * t + g] : 127u;
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int h = 0; h < (FP4 ? 1 : 2); ++h) {
+          // What lies past the end of K is 0 * 2^0, for both operands.
+          const int k = k0 + 128 * t + (FP4 ? 32 * g : 64 * h + 16 * g);
+          const int off = full || k < K ? oc[j % NB] : kPastEnd;
+          const int at = FP4 ? (k0 + 128 * t) / 2 : k0 + 128 * t + 64 * h;
+          r.b[j][t][h] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(j < NB ? bc0 : bc1, off + (full ? at : k < K ? at : 0), 0, 0));
+        }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int at = k0 + 128 * t + 64 * h;
+          r.a[i][t][h] = full || at + 16 * g < K ? *reinterpret_cast<const v4i*>(ac[i] + at) : zero;
+        }
+    if (full) {
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        uint32_t w[T];
+        const __amdgpu_buffer_rsrc_t b = j < NB ? bs0 : bs1;
+        if constexpr (T == 4) {
+          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(b, os[j % NB] + k0 / 32, 0, 0);
+          __builtin_memcpy(w, &v, 16);
+        } else if constexpr (T == 2) {
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(b, os[j % NB] + k0 / 32, 0, 0);
+          __builtin_memcpy(w, &v, 8);
+        } else {
+          w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, os[j % NB] + k0 / 32, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) r.sb[j][t] = w[t];
       }
-    };
-    // 16 bytes of a row's codes, 0 past the end of K (k: first element).
-    auto piece = [&](const uint8_t* row, int64_t k, int64_t byte) {
-      return full || k < a.K ? *reinterpret_cast<const v4i*>(row + byte) : zero;
-    };
 #pragma unroll
-    for (int i = 0; i < MT; ++i) scales(as[i], sa[i]);
+      for (int i = 0; i < MT; ++i) __builtin_memcpy(r.sa[i], as[i] + k0 / 32, 4 * T);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) scales(bs[j], sb[j]);
+      for (int t = 0; t < T; ++t) {
+        const int k = k0 + 128 * t + 32 * g;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int64_t k = k0 + 128 * t;
-      v8i fa[MT], fb[NB];
+        for (int j = 0; j < NF; ++j)
+          r.sb[j][t] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(j < NB ? bs0 : bs1,
+                                                                     k < K ? os[j % NB] + k / 32 : kPastEnd, 0, 0)
+                       << (8 * g);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) r.sa[i][t] = (k < K ? (uint32_t)as[i][k / 32] : 127u) << (8 * g);
+      }
+    }
+  };
+  auto products = [&](const R& r) {
+#pragma unroll
+    for (int t = 0; t < T; ++t)
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const v4i lo = piece(ac[i], k + 16 * g, k + 16 * g);
-        const v4i hi = piece(ac[i], k + 64 + 16 * g, k + 64 + 16 * g);
-        fa[i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      }
+        const v4i al = r.a[i][t][0], ah = r.a[i][t][1];
+        const v8i fa = {al[0], al[1], al[2], al[3], ah[0], ah[1], ah[2], ah[3]};
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        if constexpr (FP4) {
-          const v4i lo = piece(bc[j], k + 32 * g, k / 2 + 16 * g);
-          fb[j] = v8i{lo[0], lo[1], lo[2], lo[3], 0, 0, 0, 0};
-        } else {
-          const v4i lo = piece(bc[j], k + 16 * g, k + 16 * g);
-          const v4i hi = piece(bc[j], k + 64 + 16 * g, k + 64 + 16 * g);
-          fb[j] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        for (int j = 0; j < NF; ++j) {
+          const v4i lo = r.b[j][t][0], hi = FP4 ? v4i{0, 0, 0, 0} : r.b[j][t][FP4 ? 0 : 1];
+          // B first: lane l then holds row l % 16 and columns 4 (l / 16) .. +3.
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, fa, acc[i][j], FP4 ? 4 : 0, 0, 0,
+              (int)(r.sb[j][t] >> (8 * g)), 0, (int)(r.sa[i][t] >> (8 * g)));
         }
       }
-      // B first: lane l then holds row l % 16 and columns 4 (l / 16) .. +3.
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              fb[j], fa[i], acc[i][j], FP4 ? 4 : 0, 0, 0, (int)sb[j][t], 0, (int)sa[i][t]);
-    }
+  };
+  const int runs = (K + KR - 1) / KR;
+  R x, y;
+  int i = wave;
+  if (i < runs) load(x, KR * i);
+  while (i < runs) {
+    if (i + WV < runs) load(y, KR * (i + WV));
+    products(x);
+    i += WV;
+    if (i >= runs) break;
+    if (i + WV < runs) load(x, KR * (i + WV));
+    products(y);
+    i += WV;
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+    for (int j = 0; j < NF; ++j)
       *reinterpret_cast<v4f*>(&red[wave][16 * i + r16][16 * j + 4 * g]) = acc[i][j];
   __syncthreads();
-  // Thread t of the first MT waves: row t / 4 of the tile, columns 8 (t % 4).
-  if (threadIdx.x >= 64 * MT) return;
-  const int row = threadIdx.x >> 2, col = 8 * (threadIdx.x & 3);
-  float z[8], up[8];
+  // Every thread adds the waves' sums of some elements, into the first
+  // wave's place; then 2 NB lanes a row finish it, 8 columns each.
+  for (int e = threadIdx.x; e < MT * 16 * Cols; e += 64 * WV) {
+    const int row = e / Cols, col = e % Cols;
+    float s = red[0][row][col];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = up[i] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kFewWaves; ++w)
+    for (int w = 1; w < WV; ++w) s += red[w][row][col];
+    red[0][row][col] = s;
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < MT * 16 * 2 * NB; u += 64 * WV) {
+    const int row = u / (2 * NB), col = 8 * (u % (2 * NB));
+    float z[8], up[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      z[i] += red[w][row][col + i];
-      if constexpr (Gated) up[i] += red[w][row][32 + col + i];
+      z[i] = red[0][row][col + i];
+      up[i] = Gated ? red[0][row][16 * NB + col + i] : 0.0f;
     }
-  if (m0 + row < a.m && n0 + col < a.n) epilogue8<Gated>(a, m0 + row, n0 + col, z, up);
+    if (m0 + row < a.m && n0 + col < a.n) epilogue8<Gated>(a, m0 + row, n0 + col, z, up);
+  }
 }
+
+template <bool FP4, bool Gated, int MT, int NB, int WV, int T>
+void few_start(const LinearArgs& a, hipStream_t stream) {
+  linear_few_kernel<FP4, Gated, MT, NB, WV, T>
+      <<<dim3((unsigned)((a.n + 16 * NB - 1) / (16 * NB)), (unsigned)((a.m + 16 * MT - 1) / (16 * MT))),
+         dim3(64 * WV), 0, stream>>>(a);
+}
+
+// 16 columns and 8 waves a workgroup while that makes at most two for each
+// compute unit (1 x 4096 x 14336, E2M1: 10.6 us, with 32 columns and 4 waves
+// 17.1), else 32 columns and 4 waves, which read A half as often (16 x 14336
+// gated x 4096: 21.0, with 16 columns 23.9). An MXFP8 block needs 32.
+bool few_narrow(int64_t n, bool mx8) { return !mx8 && n <= 16 * 512; }
 
 template <bool FP4, bool Gated>
 adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
-  const unsigned gx = (unsigned)((a.n + 31) / 32);
-#define ADAHOP_FEW(MT)                                                                       \
-  linear_few_kernel<FP4, Gated, MT>                                                          \
-      <<<dim3(gx, (unsigned)((a.m + 16 * MT - 1) / (16 * MT))), dim3(64 * kFewWaves), 0, stream>>>(a)
-  if (a.m <= 16) ADAHOP_FEW(1);
-  else ADAHOP_FEW(2);
-#undef ADAHOP_FEW
+  if (few_narrow(a.n, a.out_scales != nullptr)) {
+    if (a.m <= 16) few_start<FP4, Gated, 1, 1, 8, 2>(a, stream);
+    else few_start<FP4, Gated, 2, 1, 8, 2>(a, stream);
+  } else {
+    if (a.m <= 16) few_start<FP4, Gated, 1, 2, 4, 2>(a, stream);
+    else few_start<FP4, Gated, 2, 2, 4, 2>(a, stream);
+  }
   return check_launch("linear_mx");
 }
 
-// Up to kFewRows rows the weights are streamed once past all of them.
-constexpr int64_t kFewRows = 32;
+// Estimate in microseconds, as linear_tile_plan's: a launch 3.5, all of B at
+// 5 TB/s, and what a compute unit reads of A and B (again for every 32 rows)
+// at 28 KB / us (32 columns a workgroup 20). It takes no workspace, so it does
+// not look at the output's type: the two differ little where the choice lies
+// near.
+double few_us(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
+  const double kb = (double)K / 1024, b = b_fp4 ? 17.0 / 32 : 33.0 / 32, a = 33.0 / 32;
+  const bool narrow = few_narrow(n, false);
+  const int cols = narrow ? 16 : 32;
+  const double down = (double)((m + 31) / 32), rows = (double)m / down;
+  const double groups = down * (double)((n + cols - 1) / cols) / (double)compute_units();
+  const double group_kb = kb * (cols * (gated ? 2 : 1) * b + rows * a);
+  const double cu = (groups < 1 ? 1 : groups) * group_kb / (narrow ? 28 : 20);
+  const double hbm = (double)n * (gated ? 2 : 1) * kb * b / 4883;
+  return 3.5 + (cu > hbm ? cu : hbm);
+}
 
 adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t stream) {
   if (b_fp4) return gated ? few_dispatch<true, true>(a, stream) : few_dispatch<true, false>(a, stream);
@@ -184,18 +271,22 @@ LinearArgs part_of(const LinearArgs& a, int64_t r0, int64_t rows, int64_t c0, in
 
 }  // namespace
 
+bool take_few(int64_t m, const TilePlan& p, int64_t n, int64_t K, int b_fp4, int gated) {
+  return few_us(m, n, K, b_fp4, gated) <= p.us;
+}
+
 size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
-  if (m <= kFewRows) return 0;
   const TilePlan p = linear_tile_plan(m, n, K, b_fp4, gated);
-  return p.scale_bytes + p.part_bytes;
+  return take_few(m, p, n, K, b_fp4, gated) ? 0 : p.scale_bytes + p.part_bytes;
 }
 
 adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* scratch, size_t,
                                hipStream_t stream) {
   if (a.m == 0) return ADAHOP_OK;
-  if (a.m <= kFewRows) return few_launch(a, b_fp4, gated, stream);
+  const TilePlan plan = linear_tile_plan(a.m, a.n, a.K, b_fp4, gated);
+  if (take_few(a.m, plan, a.n, a.K, b_fp4, gated)) return few_launch(a, b_fp4, gated, stream);
   if (linear_tiles_reach(a.m, a.lda) && linear_tiles_reach(a.n, a.ldb))
-    return linear_tiles_launch(a, b_fp4, gated, linear_tile_plan(a.m, a.n, a.K, b_fp4, gated), scratch, stream);
+    return linear_tiles_launch(a, b_fp4, gated, plan, scratch, stream);
   // Operands of 2 GB and more: in pieces that the tile kernel's offsets
   // reach. Rows 4 MB apart and gated weights of 2 GB a part go by the
   // streaming kernel, in launches that fit its grid.

@@ -1,6 +1,7 @@
 // Host side of the norm, MXFP8 and linear-layer entry points: argument checks
 // and launches. Every check runs before the first launch; nothing allocates
 // device memory or synchronizes.
+#include <atomic>
 #include <cmath>
 #include <new>
 #include <string>
@@ -13,6 +14,7 @@ namespace {
 constexpr int64_t kMaxCols = 32768;                 // columns of a norm's row
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxDim = int64_t{1} << 30;       // sizes of a product
+constexpr int64_t kMaxRowBytes = int64_t{1} << 25;  // row of its weights
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_dtype(int d) { return d == ADAHOP_OUT_BF16 || d == ADAHOP_OUT_F32; }
@@ -158,6 +160,8 @@ adahop_status linear(const adahop_linear_args* a, void* ws, size_t ws_bytes, hip
   if (!aligned16(a->a_codes) || !aligned16(a->b_codes) || a->ld_a_codes % 16 != 0 ||
       a->ld_b_codes % 16 != 0)
     return unsupported("linear_mx: codes of A and B must be 16-byte aligned, rows included");
+  if (a->ld_b_codes >= kMaxRowBytes || a->ld_b_scales >= kMaxRowBytes)
+    return unsupported("linear_mx: rows of B 32 MB or more apart");
   ADAHOP_TRY(need_workspace(ws, ws_bytes, linear_mx_scratch_bytes(a->m, n, a->K, fp4, a->gated),
                             "linear_mx"));
   const LinearArgs g = {a->a_codes, a->a_scales, a->b_codes, a->b_scales, a->ld_a_codes,
@@ -173,6 +177,23 @@ size_t act_back_bytes(int64_t m, int64_t N, int32_t gated) {
 }
 
 }  // namespace
+
+int64_t compute_units() {
+  static std::atomic<int> known[64];
+  int dev = 0, v = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) {
+    (void)hipGetLastError();
+    return 256;
+  }
+  if ((v = known[dev].load(std::memory_order_relaxed)) > 0) return v;
+  if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v < 1) {
+    (void)hipGetLastError();
+    v = 256;
+  }
+  known[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
 }  // namespace adahop
 
 using namespace adahop;

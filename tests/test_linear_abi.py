@@ -138,3 +138,8 @@ def test_mx8_refusals(rows, cols, ld, ldc, lds, dtype, src, status):
     lib = A.lib()
     assert lib.adahop_mx8_quant(src, dtype, rows, cols, ld, P, ldc, P, lds, None) == status
     assert lib.adahop_mx8_dequant(P, ldc, P, lds, rows, cols, src, dtype, ld, None) == status
+
+
+def test_linear_far_rows_of_b():
+    for change in (dict(ld_b_codes=1 << 25), dict(ld_b_scales=1 << 25)):
+        assert A.lib().adahop_linear_mx(ctypes.byref(linear_args(**change)), None, 0, None) == UNSUPPORTED

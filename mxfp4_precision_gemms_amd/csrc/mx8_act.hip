@@ -42,11 +42,24 @@ __global__ void __launch_bounds__(256) act_backward_kernel(ActBackArgs a) {
   const int64_t r0 = (int64_t)blockIdx.y * a.rows_per;
   const int64_t r1 = r0 + a.rows_per < a.m ? r0 + a.rows_per : a.m;
   if (c < a.n) {
-    for (int64_t r = r0 + rl; r < r1; r += 8) {
-      float g[8], z[P][8], d[P][8];
-      load_group<DF32>(static_cast<const TD*>(a.dout) + r * a.lddo, c, a.n, g);
+    // A row's loads are in flight while the one before is computed.
+    struct Row {
+      Raw8<DF32> g;
+      Raw8<false> z[P];
+    };
+    auto load = [&](Row& x, int64_t r) {
+      x.g.template load<false>(static_cast<const TD*>(a.dout) + r * a.lddo, c, a.n);
 #pragma unroll
-      for (int p = 0; p < P; ++p) load_group<false>(a.z + r * a.ldz + p * a.n, c, a.n, z[p]);
+      for (int p = 0; p < P; ++p) x.z[p].template load<false>(a.z + r * a.ldz + p * a.n, c, a.n);
+    };
+    Row now, next;
+    if (r0 + rl < r1) load(now, r0 + rl);
+    for (int64_t r = r0 + rl; r < r1; r += 8) {
+      if (r + 8 < r1) load(next, r + 8);
+      float g[8], z[P][8], d[P][8];
+      now.g.get(g, c, a.n);
+#pragma unroll
+      for (int p = 0; p < P; ++p) now.z[p].get(z[p], c, a.n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float value, slope;
@@ -62,6 +75,7 @@ __global__ void __launch_bounds__(256) act_backward_kernel(ActBackArgs a) {
       }
 #pragma unroll
       for (int p = 0; p < P; ++p) store_group<false>(a.dz + r * a.lddz + p * a.n, c, a.n, d[p]);
+      now = next;
     }
   }
   if (a.partial == nullptr) return;

@@ -80,6 +80,81 @@ struct Elem<true> {
   static __device__ __forceinline__ float rounded(float v) { return v; }
 };
 
+// The k < 8 elements at p as 8 elements' words, 0 after them, and back: in
+// pieces of 4, 2 and 1.
+template <typename T>
+__device__ __forceinline__ T read_as(const void* p) {
+  T v;
+  __builtin_memcpy(&v, p, sizeof(T));
+  return v;
+}
+template <bool F32, int N>
+__device__ __forceinline__ void load_part(const typename Elem<F32>::type* p, int k, uint32_t (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = 0;
+  if constexpr (F32) {
+    const int two = k & 4, one = k & 6;
+    if (k & 4) {
+      const u32x4 v = read_as<u32x4>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = v[i];
+    }
+    if (k & 2) {
+      const u32x2 v = read_as<u32x2>(p + two);
+      const uint32_t a = v[0], b = v[1];
+      (two ? x[4] : x[0]) = a;
+      (two ? x[5] : x[1]) = b;
+    }
+    if (k & 1) {
+      const uint32_t v = read_as<uint32_t>(p + one);
+      (one == 0 ? x[0] : one == 2 ? x[2] : one == 4 ? x[4] : x[6]) = v;
+    }
+  } else {
+    const int two = k & 4, one = k & 6;
+    if (k & 4) {
+      const u32x2 v = read_as<u32x2>(p);
+      x[0] = v[0];
+      x[1] = v[1];
+    }
+    if (k & 2) (two ? x[2] : x[0]) = read_as<uint32_t>(p + two);
+    if (k & 1) {
+      const uint32_t v = read_as<uint16_t>(p + one);
+      (one == 0 ? x[0] : one == 2 ? x[1] : one == 4 ? x[2] : x[3]) = v;
+    }
+  }
+}
+template <bool F32, int N>
+__device__ __forceinline__ void store_part(typename Elem<F32>::type* p, int k, const uint32_t (&x)[N]) {
+  const int two = k & 4, one = k & 6;
+  if constexpr (F32) {
+    if (k & 4) {
+      const u32x4 v = {x[0], x[1], x[2], x[3]};
+      __builtin_memcpy(p, &v, 16);
+    }
+    if (k & 2) {
+      const u32x2 v = {two ? x[4] : x[0], two ? x[5] : x[1]};
+      __builtin_memcpy(p + two, &v, 8);
+    }
+    if (k & 1) {
+      const uint32_t v = one == 0 ? x[0] : one == 2 ? x[2] : one == 4 ? x[4] : x[6];
+      __builtin_memcpy(p + one, &v, 4);
+    }
+  } else {
+    if (k & 4) {
+      const u32x2 v = {x[0], x[1]};
+      __builtin_memcpy(p, &v, 8);
+    }
+    if (k & 2) {
+      const uint32_t v = two ? x[2] : x[0];
+      __builtin_memcpy(p + two, &v, 4);
+    }
+    if (k & 1) {
+      const uint16_t v = (uint16_t)(one == 0 ? x[0] : one == 2 ? x[1] : one == 4 ? x[2] : x[3]);
+      __builtin_memcpy(p + one, &v, 2);
+    }
+  }
+}
+
 // Elements c .. c + 7 of a row of `cols`; those past the end read as 0 and
 // are not stored.
 template <bool F32>
@@ -88,8 +163,11 @@ __device__ __forceinline__ void load_group(const typename Elem<F32>::type* row, 
   if (c + 8 <= cols) {
     Elem<F32>::load8(row + c, v);
   } else {
+    uint32_t x[F32 ? 8 : 4];
+    load_part<F32>(row + c, c < cols ? (int)(cols - c) : 0, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? Elem<F32>::load(row + c + i) : 0.0f;
+    for (int i = 0; i < 8; ++i)
+      v[i] = __builtin_bit_cast(float, F32 ? x[F32 ? i : 0] : i % 2 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16);
   }
 }
 template <bool F32>
@@ -97,11 +175,75 @@ __device__ __forceinline__ void store_group(typename Elem<F32>::type* row, int64
                                             const float (&v)[8]) {
   if (c + 8 <= cols) {
     Elem<F32>::store8(row + c, v);
-  } else {
+  } else if (c < cols) {
+    uint32_t x[F32 ? 8 : 4];
+#pragma unroll
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+      if constexpr (F32) x[i] = __builtin_bit_cast(uint32_t, v[i]);
+      else x[i] = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    store_part<F32>(row + c, (int)(cols - c), x);
+  }
+}
+
+// Elements c .. c + 7 as they are stored, for loads issued long before their
+// use. A row's last group is the row's last 8 elements, moved into place when
+// they are used: loads under a branch would be waited for in it (a row of 8191
+// then costs its last wave a latency for each: 2050 x 8191 in 39 us instead of
+// 26). Once: nontemporal, where whole cache lines are read at once and not
+// again (reads stream at 6.9 TB/s instead of 6.1; lines read in pieces are
+// fetched again: 2050 x 8191 in 48 us).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <bool F32>
+struct Raw8 {
+  u32x4 w[F32 ? 2 : 1];
+  template <bool Once>
+  __device__ __forceinline__ void load(const typename Elem<F32>::type* row, int64_t c, int64_t cols) {
+    if (cols >= 8) {
+      const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + (c + 8 <= cols ? c : cols - 8));
+#pragma unroll
+      for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+        // (an fp32 group's two loads each read half of every 32 bytes)
+        if constexpr (Once && !F32) w[i] = __builtin_nontemporal_load(p + i);
+        else w[i] = p[i];
+      }
+    } else {
+      uint32_t x[F32 ? 8 : 4];
+      load_part<F32>(row + c, c < cols ? (int)(cols - c) : 0, x);
+#pragma unroll
+      for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = u32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+    }
+  }
+  // The elements, 0 past the end of the row.
+  __device__ __forceinline__ void get(float (&v)[8], int64_t c, int64_t cols) const {
+    constexpr int N = F32 ? 8 : 4;
+    uint32_t x[N + 1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = w[i / 4][i % 4];
+    x[N] = 0;
+    if (cols >= 8 && c + 8 > cols) {
+      const int s = c < cols ? (int)(c + 8 - cols) : 8;      // elements to move by
+      constexpr int W = F32 ? 1 : 2;                         // elements of a word
+#pragma unroll
+      for (int b = 8; b >= W; b /= 2)
+        if (s & b) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[i] = i + b / W < N ? x[i + b / W < N ? i + b / W : 0] : 0u;
+        }
+      if (!F32 && (s & 1)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = x[i] >> 16 | x[i + 1] << 16;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < cols) Elem<F32>::store(row + c + i, v[i]);
+      v[i] = __builtin_bit_cast(float, F32 ? x[F32 ? i : 0] : i % 2 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16);
   }
+};
+
+// Whether every row of a matrix starts at a cache line.
+inline bool line_aligned(const void* p, int64_t ld, int f32) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (f32 ? 4 : 2))) & 127u) == 0;
 }
 
 // ---- cross-lane -------------------------------------------------------------

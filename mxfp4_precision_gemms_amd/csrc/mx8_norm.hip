@@ -123,67 +123,97 @@ struct NormBackArgs {
 // With n = h * s and u = gain * dy:  dx = dh + s * (u - n * mean(u * n)),
 // and a workgroup's part of dgain = sum over its rows of dy * n, which stays
 // in registers over all rows that the workgroup takes (every gridDim.x-th
-// group of rows) and goes out once.
-template <bool DyF32, bool HF32, int Waves, int NV>
+// group of rows) and goes out once. Bound by HBM: 8 columns a thread, so that
+// 16 waves a compute unit fit, each with its next row's loads in flight
+// (16384 x 2048 in bf16 with dh: 51 us, 5.3 TB/s; a wave a row without loads
+// ahead 76).
+// Once: every row starts at a cache line.
+template <bool DyF32, bool HF32, bool Once, int Waves, int NV>
 __global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
     rmsnorm_backward_kernel(NormBackArgs a) {
   using TD = typename Elem<DyF32>::type;
   using TH = typename Elem<HF32>::type;
-  constexpr int T = Waves == 1 ? 64 : 64 * Waves;
+  constexpr int T = 64 * Waves;
   constexpr int RowsPer = Waves == 1 ? 4 : 1;
   __shared__ float red[2][Waves];
   __shared__ float part[Waves == 1 ? 3 * 64 * 8 : 1];
   const int wave = threadIdx.x >> 6;
   const int t = Waves == 1 ? threadIdx.x & 63 : threadIdx.x;
-  float acc[NV][8], g[NV][8];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    load_gain(a.gain, a.gain_f32, 8 * (int64_t)(t + k * T), a.cols, g[k]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[k][i] = 0.0f;
-  }
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RowsPer + (Waves == 1 ? wave : 0); row < a.rows;
-       row += (int64_t)gridDim.x * RowsPer, turn ^= 1) {
+  struct Row {
+    Raw8<DyF32> dy[NV];
+    Raw8<HF32> h[NV], dh[NV];
+    float s;
+  };
+  const int64_t step = (int64_t)gridDim.x * RowsPer;
+  auto load = [&](Row& r, int64_t row) {
     const TD* dy = static_cast<const TD*>(a.dy) + row * a.lddy;
     const TH* h = static_cast<const TH*>(a.h) + row * a.ldh;
-    float u[NV][8], n[NV][8];
+    r.s = a.rstd[row];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) load_group<DyF32>(dy, 8 * (int64_t)(t + k * T), a.cols, u[k]);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) load_group<HF32>(h, 8 * (int64_t)(t + k * T), a.cols, n[k]);
-    float e[NV][8];
-    if (a.dh != nullptr) {
-      const TH* dh = static_cast<const TH*>(a.dh) + row * a.lddh;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) load_group<HF32>(dh, 8 * (int64_t)(t + k * T), a.cols, e[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[k][i] = 0.0f;
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = 8 * (int64_t)(t + k * T);
+      r.dy[k].template load<Once>(dy, c, a.cols);
+      r.h[k].template load<Once>(h, c, a.cols);
+      if (a.dh != nullptr) r.dh[k].template load<Once>(static_cast<const TH*>(a.dh) + row * a.lddh, c, a.cols);
     }
-    const float s = a.rstd[row];
+  };
+  // More than 8 columns a thread leave no registers for a row ahead, nor for
+  // the gain.
+  constexpr bool Ahead = NV == 1;
+  float acc[NV][8], g[8];
+  if constexpr (Ahead) load_gain(a.gain, a.gain_f32, 8 * (int64_t)t, a.cols, g);
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[k][i] = 0.0f;
+  int turn = 0;
+  int64_t row = (int64_t)blockIdx.x * RowsPer + (Waves == 1 ? wave : 0);
+  Row now, next;
+  if (Ahead && row < a.rows) load(now, row);
+  for (; row < a.rows; row += step, turn ^= 1) {
+    if constexpr (Ahead) {
+      if (row + step < a.rows) load(next, row + step);
+    } else {
+      load(now, row);
+    }
     float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+      float u[8], n[8];
+      const int64_t at = 8 * (int64_t)(t + k * T);
+      now.dy[k].get(u, at, a.cols);
+      now.h[k].get(n, at, a.cols);
+      if constexpr (!Ahead) load_gain(a.gain, a.gain_f32, 8 * (int64_t)(t + k * T), a.cols, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        n[k][i] *= s;
-        acc[k][i] = __builtin_fmaf(u[k][i], n[k][i], acc[k][i]);
-        u[k][i] *= g[k][i];
-        sum = __builtin_fmaf(u[k][i], n[k][i], sum);
+        n[i] *= now.s;
+        acc[k][i] = __builtin_fmaf(u[i], n[i], acc[k][i]);
+        u[i] *= g[i];
+        sum = __builtin_fmaf(u[i], n[i], sum);
       }
+    }
     // Two sets of partial sums in turn: a wave that is a row ahead writes
     // the other set, and is held at that row's barrier until all have read.
     const float c = group_sum<Waves>(sum, red[turn]) / (float)a.cols;
     TH* dx = static_cast<TH*>(a.dx) + row * a.lddx;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+      float u[8], n[8], e[8];
+      const int64_t at = 8 * (int64_t)(t + k * T);
+      now.dy[k].get(u, at, a.cols);
+      now.h[k].get(n, at, a.cols);
+      if constexpr (!Ahead) load_gain(a.gain, a.gain_f32, 8 * (int64_t)(t + k * T), a.cols, g);
+      if (a.dh != nullptr) {
+        now.dh[k].get(e, at, a.cols);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[k][i] += s * (u[k][i] - n[k][i] * c);
-      store_group<HF32>(dx, 8 * (int64_t)(t + k * T), a.cols, e[k]);
+        for (int i = 0; i < 8; ++i) e[i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] += now.s * (u[i] * g[i] - n[i] * now.s * c);
+      store_group<HF32>(dx, 8 * (int64_t)(t + k * T), a.cols, e);
     }
+    if constexpr (Ahead) now = next;
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + (int64_t)blockIdx.x * a.cols;
@@ -208,26 +238,28 @@ __global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
   }
 }
 
-// out[c] = sum over p of partial[p][c]: a workgroup takes 64 columns, its 16
-// waves every 16th part; the waves' sums are added in wave order.
+// out[c] = sum over p of partial[p][c]: a workgroup takes 16 columns, its 64
+// groups of 16 lanes every 64th part; their sums are added in pairs, in a
+// fixed tree. (64 columns a workgroup leave most compute units without work:
+// 5.0 us instead of 3.4 for 1024 x 2048.)
 __global__ void __launch_bounds__(1024) column_reduce_kernel(const float* __restrict__ partial,
                                                              int parts, int64_t cols,
                                                              float* __restrict__ out) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ float red[64][17];
+  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + lane;
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = wave; p < parts; p += 16) s += partial[(int64_t)p * cols + c];
+    for (int p = group; p < parts; p += 64) s += partial[(int64_t)p * cols + c];
   }
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && c < cols) {
+  red[group][lane] = s;
 #pragma unroll
-    for (int w = 1; w < 16; ++w) s += red[w][lane];
-    out[c] = s;
+  for (int half = 32; half >= 1; half /= 2) {
+    __syncthreads();
+    if (group < half) red[group][lane] += red[group + half][lane];
   }
+  if (group == 0 && c < cols) out[c] = red[0][lane];
 }
 
 // ---- quantizer and dequantizer ----------------------------------------------
@@ -319,19 +351,29 @@ adahop_status norm_dispatch(const NormArgs& a, hipStream_t stream) {
   return check_launch("rmsnorm");
 }
 
-template <bool DyF32, bool HF32>
+// Waves that share a row: 8 columns a lane, up to 16 waves.
+int norm_back_waves(int64_t cols) {
+  int w = 1;
+  while (w < 16 && 512 * w < cols) w *= 2;
+  return w;
+}
+
+template <bool DyF32, bool HF32, bool Once>
 adahop_status norm_back_dispatch(const NormBackArgs& a, int grid, hipStream_t stream) {
   const int64_t c = a.cols;
 #define ADAHOP_NORM_BACK(WAVES, NV)                                                              \
-  rmsnorm_backward_kernel<DyF32, HF32, WAVES, NV>                                                \
+  rmsnorm_backward_kernel<DyF32, HF32, Once, WAVES, NV>                                                \
       <<<dim3((unsigned)grid), dim3(WAVES == 1 ? 256 : 64 * WAVES), 0, stream>>>(a)
-  if (c <= 512) ADAHOP_NORM_BACK(1, 1);
-  else if (c <= 1024) ADAHOP_NORM_BACK(1, 2);
-  else if (c <= 2048) ADAHOP_NORM_BACK(1, 4);
-  else if (c <= 4096) ADAHOP_NORM_BACK(4, 2);
-  else if (c <= 8192) ADAHOP_NORM_BACK(8, 2);
-  else if (c <= 16384) ADAHOP_NORM_BACK(16, 2);
-  else ADAHOP_NORM_BACK(16, 4);
+  switch (norm_back_waves(c)) {
+    case 1: ADAHOP_NORM_BACK(1, 1); break;
+    case 2: ADAHOP_NORM_BACK(2, 1); break;
+    case 4: ADAHOP_NORM_BACK(4, 1); break;
+    case 8: ADAHOP_NORM_BACK(8, 1); break;
+    default:
+      if (c <= 8192) ADAHOP_NORM_BACK(16, 1);
+      else if (c <= 16384) ADAHOP_NORM_BACK(16, 2);
+      else ADAHOP_NORM_BACK(16, 4);
+  }
 #undef ADAHOP_NORM_BACK
   return check_launch("rmsnorm_backward");
 }
@@ -352,8 +394,10 @@ adahop_status rmsnorm_launch(const void* x, int x_f32, const void* r, int r_f32,
 }
 
 int rmsnorm_backward_groups(int64_t rows, int64_t cols) {
-  const int64_t need = cols <= 2048 ? (rows + 3) / 4 : rows;
-  const int64_t most = 1024;
+  // 4096 waves, 16 a compute unit; each workgroup leaves one row of partial
+  // sums (8 MB in all).
+  const int waves = norm_back_waves(cols);
+  const int64_t need = waves == 1 ? (rows + 3) / 4 : rows, most = waves == 1 ? 1024 : 4096 / waves;
   return (int)(need < 1 ? 1 : need < most ? need : most);
 }
 
@@ -363,20 +407,25 @@ adahop_status rmsnorm_backward_launch(const void* dy, int dy_f32, const void* h,
                                       int64_t ldh, int64_t lddh, int64_t lddx, void* dx,
                                       float* dgain, float* partial, hipStream_t stream) {
   const int grid = rmsnorm_backward_groups(rows, cols);
+  const bool once = line_aligned(dy, lddy, dy_f32) && line_aligned(h, ldh, h_f32) &&
+                    (dh == nullptr || line_aligned(dh, lddh, h_f32));
   const NormBackArgs a = {dy, h, gain, gain_f32, rstd, dh, rows, cols, lddy, ldh, lddh, lddx, dx,
                           dgain != nullptr ? partial : nullptr};
   adahop_status st;
-  if (dy_f32) st = h_f32 ? norm_back_dispatch<true, true>(a, grid, stream)
-                         : norm_back_dispatch<true, false>(a, grid, stream);
-  else st = h_f32 ? norm_back_dispatch<false, true>(a, grid, stream)
-                  : norm_back_dispatch<false, false>(a, grid, stream);
+#define ADAHOP_NORM_TYPES(ONCE)                                                                        \
+  (dy_f32 ? (h_f32 ? norm_back_dispatch<true, true, ONCE>(a, grid, stream)                             \
+                   : norm_back_dispatch<true, false, ONCE>(a, grid, stream))                           \
+          : (h_f32 ? norm_back_dispatch<false, true, ONCE>(a, grid, stream)                            \
+                   : norm_back_dispatch<false, false, ONCE>(a, grid, stream)))
+  st = once ? ADAHOP_NORM_TYPES(true) : ADAHOP_NORM_TYPES(false);
+#undef ADAHOP_NORM_TYPES
   if (st != ADAHOP_OK || dgain == nullptr) return st;
   return column_reduce_launch(partial, grid, cols, dgain, stream);
 }
 
 adahop_status column_reduce_launch(const float* partial, int parts, int64_t cols, float* out,
                                    hipStream_t stream) {
-  column_reduce_kernel<<<dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, stream>>>(partial, parts,
+  column_reduce_kernel<<<dim3((unsigned)((cols + 15) / 16)), dim3(1024), 0, stream>>>(partial, parts,
                                                                                       cols, out);
   return check_launch("column_reduce");
 }

@@ -605,7 +605,7 @@ def adahop_mx8_dequant(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torc
     rows, cols = _size(codes, "codes")
     dev = codes.device
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        out = codes.new_empty((rows, cols), dtype=out_dtype)
     d = codes.get_device()
     c, ldc, _ = _matrix(codes, "codes", _CODES, rows, cols, d)
     sc, lds, _ = _matrix(scales, "scales", _SCALES, rows, cols // 32, d)
@@ -629,31 +629,36 @@ def adahop_rmsnorm(x: torch.Tensor, gain: torch.Tensor, residual: Optional[torch
     y = h / sqrt(mean h^2 + eps) * gain as MXFP8 codes and scales (mx8) and /
     or in bf16. h may be given (the residual itself, to update it in place)."""
     rows, cols = _size(x, "x")
-    dev, d = x.device, x.get_device()
+    d = x.get_device()
     xp, ldx, xk = _matrix(x, "x", _FLOAT, rows, cols, d)
     gp, gk = _vector(gain, "gain", _FLOAT, cols, d)
-    a = RmsnormArgs(rows=rows, cols=cols, x=xp, ld_x=ldx, gain=gp, x_dtype=xk, gain_dtype=gk, eps=eps)
+    rp = hp = yp = cp = sp = tp = None
+    ldr = ldh = rk = 0
     if residual is not None:
-        a.residual, a.ld_residual, a.residual_dtype = _matrix(residual, "residual", _FLOAT, rows, cols, d)
+        rp, ldr, rk = _matrix(residual, "residual", _FLOAT, rows, cols, d)
         if h is None:
-            h = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
-        elif h.dtype != residual.dtype:
-            raise TypeError("h must have the residual's dtype")
-        a.h, a.ld_h, _ = _matrix(h, "h", _FLOAT, rows, cols, d)
+            h = residual.new_empty((rows, cols))
+            hp, ldh = h.data_ptr(), cols
+        else:
+            if h.dtype != residual.dtype:
+                raise TypeError("h must have the residual's dtype")
+            hp, ldh, _ = _matrix(h, "h", _FLOAT, rows, cols, d)
     elif h is not None:
         raise ValueError("h goes with a residual")
     codes = scales = y = rstd = None
     if mx8:
-        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-        a.codes, a.ld_codes, a.scales, a.ld_scales = codes.data_ptr(), cols, scales.data_ptr(), cols // 32
+        codes = x.new_empty((rows, cols), dtype=torch.uint8)
+        scales = x.new_empty((rows, cols // 32), dtype=torch.uint8)
+        cp, sp = codes.data_ptr(), scales.data_ptr()
     if bf16:
-        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-        a.y, a.ld_y = y.data_ptr(), cols
+        y = x.new_empty((rows, cols), dtype=torch.bfloat16)
+        yp = y.data_ptr()
     if save_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        a.rstd = rstd.data_ptr()
-    _check(lib().adahop_rmsnorm(ctypes.byref(a), _stream(dev)))
+        rstd = x.new_empty(rows, dtype=torch.float32)
+        tp = rstd.data_ptr()
+    a = RmsnormArgs(rows, cols, xp, ldx, rp, ldr, gp, hp, ldh, yp, cols, cp, cols, sp, cols // 32, tp,
+                    xk, rk, gk, eps)
+    _check(lib().adahop_rmsnorm(ctypes.byref(a), _stream(x.device)))
     return RmsnormOut(h, y, codes, scales, rstd)
 
 
@@ -711,32 +716,38 @@ def adahop_linear_mx(a: Tuple[torch.Tensor, torch.Tensor], b: Tuple[torch.Tensor
     if Kb != K and Kb * 2 != K:
         raise ValueError(f"b codes: {Kb} bytes a row fit neither MXFP8 nor MXFP4 of K = {K}")
     n = N // 2 if gated else N
-    g = LinearArgs(m, N, K, *_matrix(ac, "a codes", _CODES, m, K, d)[:2],
-                   *_matrix(asc, "a scales", _SCALES, m, K // 32, d)[:2],
-                   *_matrix(bc, "b codes", _CODES, N, Kb, d)[:2],
-                   *_matrix(bsc, "b scales", _SCALES, N, K // 32, d)[:2])
-    g.b_format, g.act, g.gated = (1 if Kb == K else 0), ACT[act], 1 if gated else 0
+    fmt = 1 if Kb == K else 0
+    ap, lda, _ = _matrix(ac, "a codes", _CODES, m, K, d)
+    asp, ldas, _ = _matrix(asc, "a scales", _SCALES, m, K // 32, d)
+    bp, ldb, _ = _matrix(bc, "b codes", _CODES, N, Kb, d)
+    bsp, ldbs, _ = _matrix(bsc, "b scales", _SCALES, N, K // 32, d)
+    biasp = rp = sp = zp = None
+    bk = ldr = lds = 0
     if bias is not None:
-        g.bias, g.bias_dtype = _vector(bias, "bias", _FLOAT, N, d)
+        biasp, bk = _vector(bias, "bias", _FLOAT, N, d)
     if residual is not None:
-        g.residual, g.ld_residual, _ = _matrix(residual, "residual", _BF16, m, n, d)
+        rp, ldr, _ = _matrix(residual, "residual", _BF16, m, n, d)
     scales = z = None
     if out_dtype == "MXFP8":
         if out is not None:
             raise ValueError("out is for a bf16 output")
-        out = torch.empty((m, n), dtype=torch.uint8, device=dev)
-        scales = torch.empty((m, n // 32), dtype=torch.uint8, device=dev)
-        g.out, g.ld_out, g.out_scales, g.ld_out_scales = out.data_ptr(), n, scales.data_ptr(), n // 32
+        out = ac.new_empty((m, n), dtype=torch.uint8)
+        scales = ac.new_empty((m, n // 32), dtype=torch.uint8)
+        op, ldo, sp, lds = out.data_ptr(), n, scales.data_ptr(), n // 32
     elif out_dtype == torch.bfloat16:
         if out is None:
-            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-        g.out, g.ld_out, _ = _matrix(out, "out", _BF16, m, n, d)
+            out = ac.new_empty((m, n), dtype=torch.bfloat16)
+            op, ldo = out.data_ptr(), n
+        else:
+            op, ldo, _ = _matrix(out, "out", _BF16, m, n, d)
     else:
         raise TypeError(f"out_dtype: torch.bfloat16 or \"MXFP8\", not {out_dtype}")
     if save_z:
-        z = torch.empty((m, N), dtype=torch.bfloat16, device=dev)
-        g.z, g.ld_z = z.data_ptr(), N
-    wp, wn, ws = _scratch(lib().adahop_linear_mx_workspace_size(m, N, K, g.b_format, g.gated), ws, dev)
+        z = ac.new_empty((m, N), dtype=torch.bfloat16)
+        zp = z.data_ptr()
+    g = LinearArgs(m, N, K, ap, lda, asp, ldas, bp, ldb, bsp, ldbs, biasp, rp, ldr, op, ldo, sp, lds, zp, N,
+                   fmt, bk, ACT[act], 1 if gated else 0)
+    wp, wn, ws = _scratch(lib().adahop_linear_mx_workspace_size(m, N, K, fmt, g.gated), ws, dev)
     _check(lib().adahop_linear_mx(ctypes.byref(g), wp, wn, _stream(dev)))
     return LinearOut(out, scales, z)
 

@@ -35,7 +35,8 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // 128 T elements along K straight from memory into registers, the next run's
 // loads issued before a run's products; their sums meet in LDS, added in wave
 // order. B is read once, by the workgroup that owns its rows: bound by HBM,
-// and by the bytes in flight that the registers of all waves hold.
+// and by what a compute unit loads of A and B (about 28 GB/s): 1 x 4096 x
+// 14336, E2M1 weights 9.8 us (3.1 TB/s), E4M3 15.5 us (3.9 TB/s).
 template <bool FP4, int MT, int NF, int T>
 struct Run {
   v4i a[MT][T][2];

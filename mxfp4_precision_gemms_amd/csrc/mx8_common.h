@@ -192,7 +192,7 @@ __device__ __forceinline__ void store_group(typename Elem<F32>::type* row, int64
 // then costs its last wave a latency for each: 2050 x 8191 in 39 us instead of
 // 26). Once: nontemporal, where whole cache lines are read at once and not
 // again (reads stream at 6.9 TB/s instead of 6.1; lines read in pieces are
-// fetched again: 2050 x 8191 in 48 us).
+// fetched again: 2050 x 8191 in 48 us instead of 36).
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <bool F32>
 struct Raw8 {

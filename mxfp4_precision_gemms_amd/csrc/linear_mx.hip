@@ -247,11 +247,6 @@ double few_us(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
   return 3.5 + (cu > hbm ? cu : hbm);
 }
 
-adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t stream) {
-  if (b_fp4) return gated ? few_dispatch<true, true>(a, stream) : few_dispatch<true, false>(a, stream);
-  return gated ? few_dispatch<false, true>(a, stream) : few_dispatch<false, false>(a, stream);
-}
-
 // Rows r0 .. r0 + rows - 1 and output columns c0 .. c0 + cols - 1 (a multiple
 // of 32, and all of them for a gated layer).
 LinearArgs part_of(const LinearArgs& a, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
@@ -268,6 +263,18 @@ LinearArgs part_of(const LinearArgs& a, int64_t r0, int64_t rows, int64_t c0, in
   if (a.out_scales) p.out_scales += r0 * a.ldos + c0 / 32;
   if (a.z) p.z += r0 * a.ldz + c0;
   return p;
+}
+
+// In launches whose grid's second dimension (blocks of 16 or 32 rows) fits.
+adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t stream) {
+  constexpr int64_t kRows = int64_t{1} << 20;
+  for (int64_t r = 0; r < a.m; r += kRows) {
+    const LinearArgs p = part_of(a, r, a.m - r < kRows ? a.m - r : kRows, 0, a.n);
+    const adahop_status st = b_fp4 ? (gated ? few_dispatch<true, true>(p, stream) : few_dispatch<true, false>(p, stream))
+                                   : (gated ? few_dispatch<false, true>(p, stream) : few_dispatch<false, false>(p, stream));
+    if (st != ADAHOP_OK) return st;
+  }
+  return ADAHOP_OK;
 }
 
 }  // namespace
@@ -290,26 +297,20 @@ adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* 
     return linear_tiles_launch(a, b_fp4, gated, plan, scratch, stream);
   // Operands of 2 GB and more: in pieces that the tile kernel's offsets
   // reach. Rows 4 MB apart and gated weights of 2 GB a part go by the
-  // streaming kernel, in launches that fit its grid.
+  // streaming kernel.
   auto most = [](int64_t rows, int64_t ld) {
     if (linear_tiles_reach(rows, ld)) return rows;
-    int64_t c = ((int64_t{1} << 31) / ld - 1024) / 512 * 512;
+    const int64_t c = ((int64_t{1} << 31) / ld - 1024) / 512 * 512;
     return c > 0 && linear_tiles_reach(c, ld) ? c : int64_t{0};
   };
   const int64_t rows = most(a.m, a.lda), cols = most(a.n, a.ldb);
-  const bool tiles = rows > 0 && cols > 0 && (!gated || cols == a.n);
-  const int64_t dr = tiles ? rows : int64_t{1} << 20, dc = tiles ? cols : a.n;
-  for (int64_t r = 0; r < a.m; r += dr)
-    for (int64_t c = 0; c < a.n; c += dc) {
-      const LinearArgs p = part_of(a, r, a.m - r < dr ? a.m - r : dr, c, a.n - c < dc ? a.n - c : dc);
-      adahop_status st;
-      if (tiles) {
-        TilePlan t = linear_tile_plan(p.m, p.n, p.K, b_fp4, gated);
-        t.parts = 1;
-        st = linear_tiles_launch(p, b_fp4, gated, t, scratch, stream);
-      } else {
-        st = few_launch(p, b_fp4, gated, stream);
-      }
+  if (rows == 0 || cols == 0 || (gated && cols < a.n)) return few_launch(a, b_fp4, gated, stream);
+  for (int64_t r = 0; r < a.m; r += rows)
+    for (int64_t c = 0; c < a.n; c += cols) {
+      const LinearArgs p = part_of(a, r, a.m - r < rows ? a.m - r : rows, c, a.n - c < cols ? a.n - c : cols);
+      TilePlan t = linear_tile_plan(p.m, p.n, p.K, b_fp4, gated);
+      t.parts = 1;
+      const adahop_status st = linear_tiles_launch(p, b_fp4, gated, t, scratch, stream);
       if (st != ADAHOP_OK) return st;
     }
   return ADAHOP_OK;

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import mxfp4_precision_gemms_amd as A
-from test_gpu_linear import BF, DEV, DT, activations, check_mx8, linear_ref, rand, strided, weights
+from test_gpu_linear import (BF, DEV, DT, activations, check_mx8, decode, decode4, linear_ref, rand, strided,
+                             weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +100,67 @@ def test_tiles_deterministic():
         first = A.adahop_linear_mx(a, b).out
         for _ in range(3):
             assert torch.equal(A.adahop_linear_mx(a, b).out, first)
+
+
+# ---- operands of 2 GB and more, more rows than a grid's second dimension -------
+def codes(rows, K, seed, fmt="MXFP8"):
+    """Codes and scales of small magnitudes, made on the device."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    if fmt == "MXFP8":
+        c = torch.randint(0x20, 0x40, (rows, K), dtype=torch.uint8, device=DEV, generator=g)
+        c |= torch.randint(0, 2, (rows, K), dtype=torch.uint8, device=DEV, generator=g) << 7
+    else:
+        c = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device=DEV, generator=g)
+    return c, torch.randint(124, 130, (rows, K // 32), dtype=torch.uint8, device=DEV, generator=g)
+
+
+def values(m, fmt="MXFP8"):
+    return (decode if fmt == "MXFP8" else decode4)(*m)
+
+
+def at_rows(m, rows):
+    return m[0][rows.to(DEV)], m[1][rows.to(DEV)]
+
+
+def check_at(a, b, fmt, act="NONE", gated=False):
+    """The output at some rows and columns, the last and those around every
+    2^31 bytes among them."""
+    m, K = a[0].shape
+    N = b[0].shape[0]
+    n = N // 2 if gated else N
+    got = A.adahop_linear_mx(a, b, act=act, gated=gated).out
+
+    def some(rows, ld):
+        at = {0, 1, rows // 2, rows - 1}
+        for k in range(1, rows * ld // 2 ** 31 + 1):
+            at |= {k * 2 ** 31 // ld + d for d in (-2, -1, 0, 1)}
+        return torch.tensor(sorted(r for r in at if 0 <= r < rows))
+
+    r, c = some(m, K), some(n, b[0].shape[1])
+    cols = torch.cat((c, n + c)) if gated else c
+    z, dz, out, dout = linear_ref(values(at_rows(a, r)), values(at_rows(b, cols), fmt), None, act, gated, None)
+    err = (got[r.to(DEV)][:, c.to(DEV)].cpu().double() - out).abs()
+    assert bool((err <= dout + BF * (out.abs() + dout)).all())
+
+
+def test_far_rows_of_a():
+    check_at(codes(131500, 16384, 120), codes(64, 16384, 121), "MXFP8")
+
+
+def test_far_rows_of_b():
+    check_at(codes(70, 16384, 122), codes(132000, 16384, 123), "MXFP8")
+
+
+def test_far_rows_of_gated_b():
+    check_at(codes(40, 16384, 124), codes(264000, 16384, 125), "MXFP8", act="SILU", gated=True)
+
+
+def test_rows_far_apart():
+    """40 rows 60 MB apart (one token of each of 40 long sequences)."""
+    base, sc = codes(40, 60 << 20, 126)
+    a = (base[:, :512], sc[:, :16])
+    check_at(a, codes(96, 512, 127, "MXFP4"), "MXFP4")
+
+
+def test_many_rows():
+    check_at(codes((1 << 21) + 65, 32, 128), codes(32, 32, 129, "MXFP4"), "MXFP4")

@@ -234,7 +234,7 @@ struct LinearArgs {
 };
 // Tile kernel of a product (linear_tiles.hip) and its workspace: scale words
 // by stage, then the K parts' sums.
-enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile32 = 3 };
+enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile32 = 3 };   // 256 rows >> shape
 struct TilePlan {
   TileShape shape;
   int parts;

@@ -270,8 +270,9 @@ adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t 
   constexpr int64_t kRows = int64_t{1} << 20;
   for (int64_t r = 0; r < a.m; r += kRows) {
     const LinearArgs p = part_of(a, r, a.m - r < kRows ? a.m - r : kRows, 0, a.n);
-    const adahop_status st = b_fp4 ? (gated ? few_dispatch<true, true>(p, stream) : few_dispatch<true, false>(p, stream))
-                                   : (gated ? few_dispatch<false, true>(p, stream) : few_dispatch<false, false>(p, stream));
+    adahop_status st;
+    if (b_fp4) st = gated ? few_dispatch<true, true>(p, stream) : few_dispatch<true, false>(p, stream);
+    else st = gated ? few_dispatch<false, true>(p, stream) : few_dispatch<false, false>(p, stream);
     if (st != ADAHOP_OK) return st;
   }
   return ADAHOP_OK;

@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) linear_tile_kernel(LinearArgs
   };
   // Load q of stage k of an item into slot I. Chunks past the end of K are
   // zeros, for both operands; a stage past it must not have NaN scales.
-  auto issue = [&](auto I, auto Q, int k, uint32_t base_a, uint32_t base_b, uint32_t base_sa, uint32_t base_sb) __attribute__((always_inline)) {
+  auto issue = [&](auto I, auto Q, int k, uint32_t base_a, uint32_t base_b, uint32_t base_sa,
+                   uint32_t base_sb) __attribute__((always_inline)) {
     constexpr int q = decltype(Q)::value;
     // The scalar offset stays inside the buffers (the range check may
     // subtract it from their size).
@@ -377,7 +378,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) linear_tile_kernel(LinearArgs
   // block rows of A after the third, the last four after the sixth (at its
   // end only the next stage's first are due). Loads still in flight at each
   // wait: the 9 (E2M1: 7) of the parts issued since.
-  [[maybe_unused]] auto stay_stage = [&](auto I, int k, const Place& now, const Place& next) __attribute__((always_inline)) {
+  [[maybe_unused]] auto stay_stage = [&](auto I, int k, const Place& now,
+                                         const Place& next) __attribute__((always_inline)) {
     constexpr int at = decltype(I)::value;
     using Next = Int<1 - at>;
     auto row = [&](auto R) {
@@ -432,7 +434,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) linear_tile_kernel(LinearArgs
   // Stage in slot I: enters with its B fragments and its first two A
   // fragments read; leaves with the next stage's. Fragment i of A sits in
   // buffer (i + Off) % 4.
-  [[maybe_unused]] auto stage = [&](auto I, int k, const Place& now, const Place& next) __attribute__((always_inline)) {
+  [[maybe_unused]] auto stage = [&](auto I, int k, const Place& now,
+                                    const Place& next) __attribute__((always_inline)) {
     constexpr int slot_now = decltype(I)::value;
     using Next = Int<(slot_now + 1) % 4>;
     constexpr int Off = (FM * slot_now) % 4;
@@ -691,23 +694,25 @@ TilePlan linear_tile_plan(int64_t m, int64_t n, int64_t K, int b_fp4, int gated)
   TilePlan best{};
   best.us = 1e30;
   for (int shape = kTile256; shape <= kTile32; ++shape) {
-    const int bm = shape == kTile256 ? 256 : shape == kTile128 ? 128 : shape == kTile64 ? 64 : 32;
-    const int bn = shape == kTile256 ? 256 : 128, unit = shape == kTile256 ? 2 : 4;
-    const double kb = (bm * 128 + bn * (b_fp4 ? 64 : 128)) / 1024.0;
+    const int lm = 8 - shape, ln = shape == kTile256 ? 8 : 7;     // log2 of the tile's rows and columns
+    const int lu = shape == kTile256 ? 1 : 2;                     // and of the stages that parts are made of
+    const double kb = (double)((128 << lm) + ((b_fp4 ? 64 : 128) << ln)) / 1024;
     const double stage = shape == kTile256 ? (b_fp4 ? 1.45 : 1.55) : 0.1 + kb / 55;
     // The smaller tiles of E2M1 weights run two to a compute unit.
-    const bool two = b_fp4 && bm <= 64;
-    const int64_t tiles = ((m + bm - 1) / bm) * ((N + bn - 1) / bn), units = (nk + unit - 1) / unit;
-    for (const int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    const bool two = b_fp4 && lm <= 6;
+    const int64_t tiles = ((m + (1 << lm) - 1) >> lm) * ((N + (1 << ln) - 1) >> ln);
+    const uint32_t units = (uint32_t)((nk + (1 << lu) - 1) >> lu);
+    for (const uint32_t parts : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u}) {
       if (parts > units || (parts > 1 && tiles * parts > 2 * cus)) break;
-      const int64_t rounds = (tiles * parts + cus - 1) / cus, stages = (units + parts - 1) / parts * unit;
-      double us = 5 + (double)rounds * (double)stages * stage;
+      const double rounds = parts == 1 ? (double)((tiles + cus - 1) / cus) : tiles * parts > cus ? 2 : 1;
+      double us = 5 + rounds * (double)((units + parts - 1) / parts << lu) * stage;
       if (shape == kTile256) us += 4;
-      else us += (K % 512 ? 3 : 0) + (two ? 0 : 1.5 * (double)(rounds - 1));
+      else us += (K % 512 ? 3 : 0) + (two ? 0 : 1.5 * (rounds - 1));
       if (parts > 1) us += 3 + (double)parts * (double)m * (double)N * 8 / 4e6;
-      if (us < best.us) best = {(TileShape)shape, parts, 0, 0, us};
-      best.part_bytes = best.shape == shape && best.parts == parts && parts > 1
-                            ? (size_t)tiles * bm * bn * 4 * parts : best.part_bytes;
+      if (us < best.us) {
+        best = {(TileShape)shape, (int)parts, 0, 0, us};
+        if (parts > 1) best.part_bytes = (size_t)tiles * 4 * parts << (lm + ln);
+      }
     }
   }
   // Whole groups of 64 rows, gated 32 columns' gate and up rows, and 4 stages.

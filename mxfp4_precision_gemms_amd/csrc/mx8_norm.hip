@@ -385,12 +385,25 @@ adahop_status rmsnorm_launch(const void* x, int x_f32, const void* r, int r_f32,
                              float eps, void* h, int64_t ldh, uint16_t* y, int64_t ldy,
                              uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds, float* rstd,
                              hipStream_t stream) {
-  if (rows == 0) return ADAHOP_OK;
-  const NormArgs a = {x, r, gain, gain_f32, rows, cols, ldx, ldr, ldh, ldy, ldc, lds,
-                      eps, h, y, codes, scales, rstd};
-  if (r == nullptr) return x_f32 ? norm_dispatch<true, 0>(a, stream) : norm_dispatch<false, 0>(a, stream);
-  if (x_f32) return r_f32 ? norm_dispatch<true, 2>(a, stream) : norm_dispatch<true, 1>(a, stream);
-  return r_f32 ? norm_dispatch<false, 2>(a, stream) : norm_dispatch<false, 1>(a, stream);
+  // A launch of up to 2^22 rows: its threads stay below 2^32.
+  constexpr int64_t kRows = int64_t{1} << 22;
+  for (int64_t at = 0; at < rows; at += kRows) {
+    auto bytes = [at](const void* p, int64_t ld, int64_t size) {
+      return p == nullptr ? nullptr : const_cast<char*>(static_cast<const char*>(p)) + at * ld * size;
+    };
+    const NormArgs a = {bytes(x, ldx, x_f32 ? 4 : 2), bytes(r, ldr, r_f32 ? 4 : 2), gain, gain_f32,
+                        rows - at < kRows ? rows - at : kRows, cols, ldx, ldr, ldh, ldy, ldc, lds, eps,
+                        bytes(h, ldh, r_f32 ? 4 : 2), reinterpret_cast<uint16_t*>(bytes(y, ldy, 2)),
+                        reinterpret_cast<uint8_t*>(bytes(codes, ldc, 1)),
+                        reinterpret_cast<uint8_t*>(bytes(scales, lds, 1)),
+                        reinterpret_cast<float*>(bytes(rstd, 1, 4))};
+    adahop_status st;
+    if (r == nullptr) st = x_f32 ? norm_dispatch<true, 0>(a, stream) : norm_dispatch<false, 0>(a, stream);
+    else if (x_f32) st = r_f32 ? norm_dispatch<true, 2>(a, stream) : norm_dispatch<true, 1>(a, stream);
+    else st = r_f32 ? norm_dispatch<false, 2>(a, stream) : norm_dispatch<false, 1>(a, stream);
+    if (st != ADAHOP_OK) return st;
+  }
+  return ADAHOP_OK;
 }
 
 int rmsnorm_backward_groups(int64_t rows, int64_t cols) {

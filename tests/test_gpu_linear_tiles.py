@@ -164,3 +164,16 @@ def test_rows_far_apart():
 
 def test_many_rows():
     check_at(codes((1 << 21) + 65, 32, 128), codes(32, 32, 129, "MXFP4"), "MXFP4")
+
+
+def test_norm_many_rows():
+    """More rows than one launch takes."""
+    rows, cols = (1 << 22) + 70, 32
+    g = torch.Generator(device=DEV).manual_seed(130)
+    x, r = (torch.randn(rows, cols, device=DEV, generator=g).to(torch.bfloat16) for _ in range(2))
+    gain = torch.ones(cols, device=DEV)
+    got = A.adahop_rmsnorm(x, gain, r, bf16=True, save_rstd=True)
+    for at in (slice(0, 70), slice((1 << 22) - 70, rows)):
+        part = A.adahop_rmsnorm(x[at], gain, r[at], bf16=True, save_rstd=True)
+        for a, b in zip(got, part):
+            assert torch.equal(a[at], b)

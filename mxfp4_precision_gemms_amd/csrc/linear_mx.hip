@@ -309,7 +309,7 @@ adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* 
   for (int64_t r = 0; r < a.m; r += rows)
     for (int64_t c = 0; c < a.n; c += cols) {
       const LinearArgs p = part_of(a, r, a.m - r < rows ? a.m - r : rows, c, a.n - c < cols ? a.n - c : cols);
-      TilePlan t = linear_tile_plan(p.m, p.n, p.K, b_fp4, gated);
+      TilePlan t = plan;                     // its scratch fits every piece
       t.parts = 1;
       const adahop_status st = linear_tiles_launch(p, b_fp4, gated, t, scratch, stream);
       if (st != ADAHOP_OK) return st;

@@ -28,6 +28,7 @@ using namespace mx8;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 // ---- few rows ---------------------------------------------------------------
 // A workgroup computes 16 MT rows by 16 NB columns of the output (gated: 16 NB
@@ -47,10 +48,19 @@ struct Run {
 constexpr int kBufferFlags = 0x00020000;   // raw buffer descriptor word 3
 constexpr int kPastEnd = 0x7FFFFFF0;       // an offset past the end of every buffer here
 
-template <bool FP4, bool Gated, int MT, int NB, int WV, int T>
+// Exact: the products on bf16 matrix cores, in which both formats' scaled
+// values are exact, instead of the scaled ones. The loads bind either way (1 x
+// 2048 x 4096: EXACT_US us), and an MXFP8 output of few values, where one code
+// rounded the other way shows, is then that of exact sums. A lane's 32 elements
+// of 128 are one block, 32 g .. + 31, of both operands.
+template <bool FP4, bool Gated, bool Exact, int MT, int NB, int WV, int T>
 __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__                        // the host pass needs the launch stub alone
   constexpr int NF = Gated ? 2 * NB : NB;   // 16-row blocks of B
   constexpr int Cols = 16 * NF, Pitch = Cols + 4, KR = 128 * T;
+  // Elements from one lane group's piece of a row to the next, and from a
+  // lane's first piece of 16 to its second.
+  constexpr int Lane = Exact ? 32 : 16, Half = Exact ? 16 : 64;
   __shared__ float red[WV][MT * 16][Pitch];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -66,7 +76,7 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
   for (int i = 0; i < MT; ++i) {
     int64_t r = m0 + 16 * i + r16;
     r = r < a.m ? r : a.m - 1;
-    ac[i] = a.a_codes + r * a.lda + 16 * g;
+    ac[i] = a.a_codes + r * a.lda + Lane * g;
     as[i] = a.a_scales + r * a.ldas;
   }
   const int rows_b = (int)(a.n - n0 < 16 * NB ? a.n - n0 : 16 * NB);
@@ -79,7 +89,7 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
   int oc[NB], os[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    oc[j] = (16 * j + r16) * (int)a.ldb + 16 * g;
+    oc[j] = (16 * j + r16) * (int)a.ldb + (FP4 ? 16 : Lane) * g;
     os[j] = (16 * j + r16) * (int)a.ldbs;
   }
   v4f acc[MT][NF];
@@ -99,9 +109,9 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
 #pragma unroll
         for (int h = 0; h < (FP4 ? 1 : 2); ++h) {
           // What lies past the end of K is 0 * 2^0, for both operands.
-          const int k = k0 + 128 * t + (FP4 ? 32 * g : 64 * h + 16 * g);
+          const int k = k0 + 128 * t + (FP4 ? 32 * g : Half * h + Lane * g);
           const int off = full || k < K ? oc[j % NB] : kPastEnd;
-          const int at = FP4 ? (k0 + 128 * t) / 2 : k0 + 128 * t + 64 * h;
+          const int at = FP4 ? (k0 + 128 * t) / 2 : k0 + 128 * t + Half * h;
           r.b[j][t][h] = __builtin_bit_cast(
               v4i, __builtin_amdgcn_raw_buffer_load_b128(j < NB ? bc0 : bc1, off + (full ? at : k < K ? at : 0), 0, 0));
         }
@@ -111,8 +121,8 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
       for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int at = k0 + 128 * t + 64 * h;
-          r.a[i][t][h] = full || at + 16 * g < K ? *reinterpret_cast<const v4i*>(ac[i] + at) : zero;
+          const int at = k0 + 128 * t + Half * h;
+          r.a[i][t][h] = full || at + Lane * g < K ? *reinterpret_cast<const v4i*>(ac[i] + at) : zero;
         }
     if (full) {
 #pragma unroll
@@ -147,22 +157,75 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
       }
     }
   };
+  // A lane's 32 elements as bf16, for four instructions.
+  struct Eight {
+    v8bf v[4];
+  };
+  auto widen8 = [](const v4i& lo, const v4i& hi, uint32_t byte) {
+    const float s = mx8_scale(byte);
+    Eight e;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int x = q < 2 ? lo[2 * q + w] : hi[2 * (q - 2) + w];
+        const auto a0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, false);
+        const auto a1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, true);
+        e.v[q][4 * w] = a0[0];
+        e.v[q][4 * w + 1] = a0[1];
+        e.v[q][4 * w + 2] = a1[0];
+        e.v[q][4 * w + 3] = a1[1];
+      }
+    return e;
+  };
+  auto widen4 = [](const v4i& c, uint32_t byte) {
+    const float s = mx8_scale(byte);
+    Eight e;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t x = (uint32_t)c[q];
+      const auto a0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 0);
+      const auto a1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 1);
+      const auto a2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 2);
+      const auto a3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, s, 3);
+      e.v[q] = v8bf{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+    }
+    return e;
+  };
   auto products = [&](const R& r) {
 #pragma unroll
-    for (int t = 0; t < T; ++t)
+    for (int t = 0; t < T; ++t) {
+      if constexpr (Exact) {
+        Eight wa[MT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const v4i al = r.a[i][t][0], ah = r.a[i][t][1];
-        const v8i fa = {al[0], al[1], al[2], al[3], ah[0], ah[1], ah[2], ah[3]};
+        for (int i = 0; i < MT; ++i)
+          wa[i] = widen8(r.a[i][t][0], r.a[i][t][1], (r.sa[i][t] >> (8 * g)) & 255u);
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          const v4i lo = r.b[j][t][0], hi = FP4 ? v4i{0, 0, 0, 0} : r.b[j][t][FP4 ? 0 : 1];
-          // B first: lane l then holds row l % 16 and columns 4 (l / 16) .. +3.
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, fa, acc[i][j], FP4 ? 4 : 0, 0, 0,
-              (int)(r.sb[j][t] >> (8 * g)), 0, (int)(r.sa[i][t] >> (8 * g)));
+          const uint32_t byte = (r.sb[j][t] >> (8 * g)) & 255u;
+          const Eight wb = FP4 ? widen4(r.b[j][t][0], byte) : widen8(r.b[j][t][0], r.b[j][t][FP4 ? 0 : 1], byte);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.v[q], wa[i].v[q], acc[i][j], 0, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const v4i al = r.a[i][t][0], ah = r.a[i][t][1];
+          const v8i fa = {al[0], al[1], al[2], al[3], ah[0], ah[1], ah[2], ah[3]};
+#pragma unroll
+          for (int j = 0; j < NF; ++j) {
+            const v4i lo = r.b[j][t][0], hi = FP4 ? v4i{0, 0, 0, 0} : r.b[j][t][FP4 ? 0 : 1];
+            // B first: lane l then holds row l % 16 and columns 4 (l / 16) .. +3.
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, fa, acc[i][j], FP4 ? 4 : 0, 0, 0,
+                (int)(r.sb[j][t] >> (8 * g)), 0, (int)(r.sa[i][t] >> (8 * g)));
+          }
         }
       }
+    }
   };
   const int runs = (K + KR - 1) / KR;
   R x, y;
@@ -203,11 +266,12 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
     }
     if (m0 + row < a.m && n0 + col < a.n) epilogue8<Gated>(a, m0 + row, n0 + col, z, up);
   }
+#endif
 }
 
-template <bool FP4, bool Gated, int MT, int NB, int WV, int T>
+template <bool FP4, bool Gated, bool Exact, int MT, int NB, int WV, int T>
 void few_start(const LinearArgs& a, hipStream_t stream) {
-  linear_few_kernel<FP4, Gated, MT, NB, WV, T>
+  linear_few_kernel<FP4, Gated, Exact, MT, NB, WV, T>
       <<<dim3((unsigned)((a.n + 16 * NB - 1) / (16 * NB)), (unsigned)((a.m + 16 * MT - 1) / (16 * MT))),
          dim3(64 * WV), 0, stream>>>(a);
 }
@@ -216,16 +280,19 @@ void few_start(const LinearArgs& a, hipStream_t stream) {
 // compute unit (1 x 4096 x 14336, E2M1: 10.6 us, with 32 columns and 4 waves
 // 17.1), else 32 columns and 4 waves, which read A half as often (16 x 14336
 // gated x 4096: 21.0, with 16 columns 23.9). An MXFP8 block needs 32.
-bool few_narrow(int64_t n, bool mx8) { return !mx8 && n <= 16 * 512; }
+bool few_narrow(int64_t n) { return n <= 16 * 512; }
 
 template <bool FP4, bool Gated>
 adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
-  if (few_narrow(a.n, a.out_scales != nullptr)) {
-    if (a.m <= 16) few_start<FP4, Gated, 1, 1, 8, 2>(a, stream);
-    else few_start<FP4, Gated, 2, 1, 8, 2>(a, stream);
+  if (a.out_scales != nullptr) {
+    if (a.m <= 16) few_start<FP4, Gated, true, 1, 2, 4, 2>(a, stream);
+    else few_start<FP4, Gated, true, 2, 2, 4, 2>(a, stream);
+  } else if (few_narrow(a.n)) {
+    if (a.m <= 16) few_start<FP4, Gated, false, 1, 1, 8, 2>(a, stream);
+    else few_start<FP4, Gated, false, 2, 1, 8, 2>(a, stream);
   } else {
-    if (a.m <= 16) few_start<FP4, Gated, 1, 2, 4, 2>(a, stream);
-    else few_start<FP4, Gated, 2, 2, 4, 2>(a, stream);
+    if (a.m <= 16) few_start<FP4, Gated, false, 1, 2, 4, 2>(a, stream);
+    else few_start<FP4, Gated, false, 2, 2, 4, 2>(a, stream);
   }
   return check_launch("linear_mx");
 }
@@ -237,7 +304,7 @@ adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
 // near.
 double few_us(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
   const double kb = (double)K / 1024, b = b_fp4 ? 17.0 / 32 : 33.0 / 32, a = 33.0 / 32;
-  const bool narrow = few_narrow(n, false);
+  const bool narrow = few_narrow(n);
   const int cols = narrow ? 16 : 32;
   const double down = (double)((m + 31) / 32), rows = (double)m / down;
   const double groups = down * (double)((n + cols - 1) / cols) / (double)compute_units();
@@ -293,7 +360,10 @@ adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* 
                                hipStream_t stream) {
   if (a.m == 0) return ADAHOP_OK;
   const TilePlan plan = linear_tile_plan(a.m, a.n, a.K, b_fp4, gated);
-  if (take_few(a.m, plan, a.n, a.K, b_fp4, gated)) return few_launch(a, b_fp4, gated, stream);
+  // An MXFP8 output of few values comes from exact products (at most 32768:
+  // above, its roundings that fall the other way are an even share of it).
+  if (take_few(a.m, plan, a.n, a.K, b_fp4, gated) || (a.out_scales != nullptr && a.m * a.n <= 32768))
+    return few_launch(a, b_fp4, gated, stream);
   if (linear_tiles_reach(a.m, a.lda) && linear_tiles_reach(a.n, a.ldb))
     return linear_tiles_launch(a, b_fp4, gated, plan, scratch, stream);
   // Operands of 2 GB and more: in pieces that the tile kernel's offsets

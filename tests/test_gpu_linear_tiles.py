@@ -177,3 +177,45 @@ def test_norm_many_rows():
         part = A.adahop_rmsnorm(x[at], gain, r[at], bf16=True, save_rstd=True)
         for a, b in zip(got, part):
             assert torch.equal(a[at], b)
+
+
+# ---- MXFP8 outputs of few values ------------------------------------------------
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+@pytest.mark.parametrize("m,n,K", [(1, 32, 32), (1, 64, 4096), (5, 96, 1056), (16, 160, 544), (17, 64, 2080), (33, 96, 8192),
+                                   (100, 320, 320)])
+def test_mx8_out_of_exact_products(m, n, K, fmt):
+    """Off by the fp32 sums alone: a product of two formats' values is exact,
+    a chain has up to K / 32 + 8 + 4 additions in fp32, each of four more
+    products that the instruction adds."""
+    a, va = activations(m, K, 140)
+    b, vb = weights(n, K, fmt, 141)
+    got = A.adahop_linear_mx(a, b, out_dtype="MXFP8")
+    want = va @ vb.t()
+    check_mx8(got.out, got.scales, want, (K / 4 + 16) * 2.0 ** -24 * (va.abs() @ vb.abs().t()))
+    ga, _ = weights(2 * n, K, fmt, 142)
+    gated = A.adahop_linear_mx(a, ga, act="RELU", gated=True, out_dtype="MXFP8")
+    _, vg = ga, (decode if fmt == "MXFP8" else decode4)(*ga)
+    z, mag = va @ vg.t(), (K / 4 + 16) * 2.0 ** -24 * (va.abs() @ vg.abs().t())
+    f, up = z[:, :n].clamp(min=0), z[:, n:]
+    bound = mag[:, :n] * up.abs() + (f + mag[:, :n]) * mag[:, n:] + 2.0 ** -24 * (f * up).abs()
+    check_mx8(gated.out, gated.scales, f * up, bound)
+
+
+@pytest.mark.parametrize("mx8", [False, True])
+@pytest.mark.parametrize("m", [3, 40])
+def test_scale_byte_255(m, mx8):
+    """A block whose scale is the NaN byte is NaN whatever its codes."""
+    (ac, asc), _ = activations(m, 256, 143)
+    (bc, bsc), _ = weights(64, 256, "MXFP4", 144)
+    asc[1, 3] = 255
+    got = A.adahop_linear_mx((ac, asc), (bc, bsc), out_dtype="MXFP8" if mx8 else torch.bfloat16)
+    out = A.adahop_mx8_dequant(got.out, got.scales) if mx8 else got.out
+    want = torch.zeros(m, dtype=torch.bool)
+    want[1] = True
+    assert torch.equal(out.isnan().all(1).cpu(), want) and torch.equal(out.isnan().any(1).cpu(), want)
+    bsc[5, 2] = 255
+    asc[1, 3] = 120
+    got = A.adahop_linear_mx((ac, asc), (bc, bsc), out_dtype="MXFP8" if mx8 else torch.bfloat16)
+    out = A.adahop_mx8_dequant(got.out, got.scales) if mx8 else got.out
+    cols = out.isnan().all(0).cpu()
+    assert bool(cols[5]) and int(cols.sum()) == (32 if mx8 else 1)

@@ -570,7 +570,8 @@ typedef enum {
  * adahop_iht_quant writes them, two to a byte, rows ld_b_codes bytes apart;
  * gated: the n gate rows, then the n up rows). The products are formed on the
  * scaled matrix cores (within about 5e-5 of the result, root mean square, on
- * operands with outlier columns; see the notes in csrc/linear_mx.hip), sums
+ * operands with outlier columns; see the notes in csrc/linear_mx.hip; exactly
+ * for MXFP8 outputs of few rows or few values), sums
  * over K, bias, activation and residual in fp32, with one rounding to the
  * output: bf16 (out, ld_out elements) or, with out_scales not NULL, MXFP8
  * (out: codes, ld_out bytes; n a multiple of 32). z (bf16 [m, N], or NULL)

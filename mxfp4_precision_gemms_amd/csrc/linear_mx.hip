@@ -3,19 +3,20 @@
 // A MXFP8 [m][K], B MXFP8 or MXFP4 [N][K] (N = n, or 2 n gate and up rows),
 // out bf16 or MXFP8, z optionally kept in bf16 for the backward pass.
 //
-// Matrix cores: v_mfma_scale_f32_{16x16x128,32x32x64}_f8f6f4, E4M3 by E4M3 or
-// by E2M1, one E8M0 byte per lane and 32-element block. Lane l supplies row
-// l % R (R = 16 or 32) and, of the instruction's K = 2048 / R elements: E2M1,
-// 32 g .. 32 g + 31 (g = l / R); E4M3, 16 g .. +15 in its first 16 bytes and
-// K / 2 + 16 g .. +15 in the others. Its scale byte is that of elements
-// 32 g .. 32 g + 31 for both. Checked on the device against exact products.
+// Matrix cores: v_mfma_scale_f32_16x16x128_f8f6f4, E4M3 by E4M3 or by E2M1,
+// one E8M0 byte per lane and 32-element block. Lane l supplies row l % 16 and,
+// of the instruction's 128 elements (g = l / 16): E2M1, 32 g .. 32 g + 31; E4M3,
+// 16 g .. +15 in its first 16 bytes and 64 + 16 g .. +15 in the others. Its scale
+// byte is that of elements 32 g .. 32 g + 31 for both. Checked on the device
+// against exact products.
 // Accuracy: within each group of 8 products of E4M3 codes the instruction
 // truncates what lies under 2^-13 of the largest's power of two, then adds the
 // groups in fp32. Measured against exact products: 1.5e-5 of the result (root
 // mean square), 5e-5 where 1 % of A's columns are 30 times the rest, at any K.
-// bf16 products of the same values would be exact up to the fp32 sums, at half
-// the rate; an output in bf16 or E4M3 is off by 1.7e-3 or 2.6e-2 by its own
-// rounding, so the faster product is taken, and no fp32 output is offered.
+// bf16 products of the same values are exact up to the fp32 sums, at half the
+// rate; an output in bf16 or E4M3 is off by 1.7e-3 or 2.6e-2 by its own
+// rounding, so large products take the faster one, and no fp32 output is
+// offered. MXFP8 outputs of few rows or few values take bf16 products.
 // The sums over K, the bias, the activation and the residual are in fp32;
 // one rounding to the output.
 #include "adahop_internal.h"
@@ -49,10 +50,11 @@ constexpr int kBufferFlags = 0x00020000;   // raw buffer descriptor word 3
 constexpr int kPastEnd = 0x7FFFFFF0;       // an offset past the end of every buffer here
 
 // Exact: the products on bf16 matrix cores, in which both formats' scaled
-// values are exact, instead of the scaled ones. The loads bind either way (1 x
-// 2048 x 4096: EXACT_US us), and an MXFP8 output of few values, where one code
-// rounded the other way shows, is then that of exact sums. A lane's 32 elements
-// of 128 are one block, 32 g .. + 31, of both operands.
+// values are exact, instead of the scaled ones, so that an MXFP8 output of few
+// values, where one code rounded the other way shows, is that of exact sums. A
+// lane's 32 elements of 128 are one block, 32 g .. + 31, of both operands. (1 x
+// 2048 x 4096, E2M1: 6.6 us, scaled and in bf16 5.0; 1 x 14336 x 4096: 11.7
+// and 10.8.)
 template <bool FP4, bool Gated, bool Exact, int MT, int NB, int WV, int T>
 __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__                        // the host pass needs the launch stub alone
@@ -279,12 +281,23 @@ void few_start(const LinearArgs& a, hipStream_t stream) {
 // 16 columns and 8 waves a workgroup while that makes at most two for each
 // compute unit (1 x 4096 x 14336, E2M1: 10.6 us, with 32 columns and 4 waves
 // 17.1), else 32 columns and 4 waves, which read A half as often (16 x 14336
-// gated x 4096: 21.0, with 16 columns 23.9). An MXFP8 block needs 32.
+// gated x 4096: 21.0, with 16 columns 23.9). An MXFP8 block needs 32 (1 x 4096 x
+// 14336, exact: 15.7).
 bool few_narrow(int64_t n) { return n <= 16 * 512; }
 
 template <bool FP4, bool Gated>
 adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
   if (a.out_scales != nullptr) {
+    // 8 waves by the same rule (1 x 2048 x 4096, E2M1: 6.6 us, with 4 waves
+    // 7.7; 1 x 14336 x 4096: 13.3, with 4 waves 11.7); gated, whose registers
+    // do not last for 8, 4.
+    if constexpr (!Gated) {
+      if (few_narrow(a.n)) {
+        if (a.m <= 16) few_start<FP4, Gated, true, 1, 2, 8, FP4 ? 4 : 2>(a, stream);
+        else few_start<FP4, Gated, true, 2, 2, 8, 2>(a, stream);
+        return check_launch("linear_few");
+      }
+    }
     if (a.m <= 16) few_start<FP4, Gated, true, 1, 2, 4, 2>(a, stream);
     else few_start<FP4, Gated, true, 2, 2, 4, 2>(a, stream);
   } else if (few_narrow(a.n)) {
@@ -361,7 +374,8 @@ adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* 
   if (a.m == 0) return ADAHOP_OK;
   const TilePlan plan = linear_tile_plan(a.m, a.n, a.K, b_fp4, gated);
   // An MXFP8 output of few values comes from exact products (at most 32768:
-  // above, its roundings that fall the other way are an even share of it).
+  // above, its roundings that fall the other way are an even share of it). It
+  // costs time where tiles would be faster: 33 x 960 x 14336 26 us, tiles 13.
   if (take_few(a.m, plan, a.n, a.K, b_fp4, gated) || (a.out_scales != nullptr && a.m * a.n <= 32768))
     return few_launch(a, b_fp4, gated, stream);
   if (linear_tiles_reach(a.m, a.lda) && linear_tiles_reach(a.n, a.ldb))

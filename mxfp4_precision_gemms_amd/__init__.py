@@ -167,7 +167,11 @@ def _check(status: int):
 
 
 def _stream(device=None) -> int:
-    """The current stream's handle (without a Stream object: 0.1 us for 2)."""
+    """The current stream's handle (without a Stream object: 0.1 us for 2).
+    Host tensors end here at the latest: the library would launch on their
+    addresses."""
+    if device is not None and device.type != "cuda":
+        raise ValueError(f"expected a GPU device, got {device}")
     index = None if device is None else device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
@@ -180,6 +184,15 @@ def _bf16_ptr(t: torch.Tensor, name: str) -> int:
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name}: expected a 2-D tensor with unit column stride")
     return t.data_ptr()
+
+
+def _on_device(device: torch.device, **tensors):
+    """Every tensor that is given lies on `device`, a GPU."""
+    if device.type != "cuda":
+        raise ValueError(f"expected GPU tensors, got {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the other operands on {device}")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -302,6 +315,8 @@ def adahop_gemm_mx(a_codes, a_scales, b_codes, b_scales, oe: Optional[dict] = No
     A = MxOperand(a_codes.data_ptr(), a_scales.data_ptr(), m, K)
     B = MxOperand(b_codes.data_ptr(), b_scales.data_ptr(), n, b_codes.shape[1] * 2)
     dev = a_codes.device
+    _on_device(dev, a_scales=a_scales, b_codes=b_codes, b_scales=b_scales, out=out,
+               **({} if oe is None else {"oe idx": oe.get("idx"), "oe a": oe["a"][0], "oe b": oe["b"][0]}))
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=dev)
     desc = None

@@ -1,0 +1,81 @@
+"""The binding's own refusals, on the host: a stand-in takes the library's
+place and records what reaches it. No GPU, and nothing is launched."""
+import pytest
+import torch
+
+import mxfp4_precision_gemms_amd as A
+
+
+class Standin:
+    """Every entry point succeeds and is recorded; sizes asked for are 0."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+    def launched(self):
+        return [c for c in self.calls if not c.endswith("_size")]
+
+
+@pytest.fixture
+def standin(monkeypatch):
+    s = Standin()
+    monkeypatch.setattr(A, "lib", lambda: s)
+    # a process that has a GPU, whose current stream is the default one
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
+    return s
+
+
+def mx_operands(device="cpu"):
+    return [torch.zeros(s, dtype=torch.uint8, device=device) for s in ((4, 16), (4, 1), (8, 16), (8, 1))]
+
+
+def test_stream_of_a_host_device():
+    for device in ("cpu", "meta"):
+        with pytest.raises(ValueError):
+            A._stream(torch.device(device))
+
+
+def test_stream_of_a_gpu(standin):
+    assert A._stream(torch.device("cuda")) == 0 and A._stream(torch.device("cuda", 0)) == 0
+
+
+def test_gemm_mx_of_host_tensors(standin):
+    with pytest.raises(ValueError):
+        A.adahop_gemm_mx(*mx_operands())
+    assert standin.launched() == []
+
+
+class OnGpu:
+    """Says that it lies on GPU 0; as much of a tensor as the binding looks at."""
+
+    def __init__(self, t):
+        self.t, self.device = t, torch.device("cuda", 0)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("host", range(6))
+def test_gemm_mx_with_one_host_tensor(standin, host):
+    """Each operand, the output and the outlier term's tensors are looked at."""
+    t = [OnGpu(x) if i != host else x for i, x in enumerate(
+        mx_operands() + [torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)])]
+    # (the outlier term's matrices are looked at where their address is taken)
+    oe = None if host != 5 else {"route": "OE_LEFT", "k": 2, "idx": t[5], "a": (None, 1), "b": (None, 1)}
+    with pytest.raises(ValueError):
+        A.adahop_gemm_mx(*t[:4], oe=oe, out=t[4])
+    assert standin.launched() == []
+
+
+def test_gemm_mx_of_gpu_tensors(standin):
+    t = [OnGpu(x) for x in mx_operands()]
+    out = OnGpu(torch.zeros(4, 8, dtype=torch.bfloat16))
+    assert A.adahop_gemm_mx(*t, out=out) is out
+    assert standin.launched() == ["adahop_gemm_mx"]

@@ -591,9 +591,14 @@ def _size(t: torch.Tensor, name: str):
 
 
 def _scratch(need: int, ws: Optional[torch.Tensor], device):
-    if ws is None and need:
+    """(address, bytes, tensor) of the caller's workspace, or of a new one."""
+    if ws is None:
+        if not need:
+            return None, 0, None
         ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return (None, 0, ws) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size(), ws)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous and on the same device as the operands")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def adahop_mx8_quant(src: torch.Tensor, codes: Optional[torch.Tensor] = None,

@@ -7,15 +7,16 @@ import mxfp4_precision_gemms_amd as A
 
 
 class Standin:
-    """Every entry point succeeds and is recorded; sizes asked for are 0."""
+    """Every entry point succeeds and is recorded; `size` is what each size
+    that is asked for comes to."""
 
     def __init__(self):
-        self.calls = []
+        self.calls, self.size = [], 0
 
     def __getattr__(self, name):
         def call(*args):
             self.calls.append(name)
-            return 0
+            return self.size if name.endswith("_size") else 0
         return call
 
     def launched(self):
@@ -58,6 +59,9 @@ class OnGpu:
     def __init__(self, t):
         self.t, self.device = t, torch.device("cuda", 0)
 
+    def get_device(self):
+        return 0
+
     def __getattr__(self, name):
         return getattr(self.t, name)
 
@@ -79,3 +83,26 @@ def test_gemm_mx_of_gpu_tensors(standin):
     out = OnGpu(torch.zeros(4, 8, dtype=torch.bfloat16))
     assert A.adahop_gemm_mx(*t, out=out) is out
     assert standin.launched() == ["adahop_gemm_mx"]
+
+
+# ---- the caller's workspace -------------------------------------------------
+WORKSPACES = {
+    "host": lambda: torch.zeros(256, dtype=torch.uint8),
+    "one element repeated": lambda: OnGpu(torch.zeros(1, dtype=torch.uint8).expand(256)),
+    "every second element": lambda: OnGpu(torch.zeros(512, dtype=torch.uint8)[::2]),
+    "columns of a matrix": lambda: OnGpu(torch.zeros(16, 64, dtype=torch.uint8)[:, :16]),
+}
+
+
+@pytest.mark.parametrize("size", [0, 64])
+@pytest.mark.parametrize("kind", list(WORKSPACES))
+def test_workspace_refusals(standin, kind, size):
+    standin.size = size
+    a, b = ([OnGpu(torch.zeros(s, dtype=torch.uint8)) for s in ((r, 32), (r, 1))] for r in (4, 8))
+    out = OnGpu(torch.zeros(4, 8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        A.adahop_linear_mx(a, b, out=out, ws=WORKSPACES[kind]())
+    assert standin.launched() == []
+    ws = OnGpu(torch.zeros(16, 4, dtype=torch.float32))          # any type, any shape
+    assert A.adahop_linear_mx(a, b, out=out, ws=ws).out is out
+    assert standin.launched() == ["adahop_linear_mx"]

@@ -8,6 +8,7 @@
 // the scaling. Sums run in fp32 along fixed trees: results do not change from
 // run to run.
 #include "adahop_internal.h"
+#include "launch_shapes.h"
 #include "mx8_common.h"
 
 namespace adahop {
@@ -333,20 +334,20 @@ int flat_grid(int64_t groups) {
 
 template <bool XF32, int Res>
 adahop_status norm_dispatch(const NormArgs& a, hipStream_t stream) {
-  const int64_t c = a.cols;
-  // Up to 2048 columns a wave holds a row; above, 4 waves, then 16, share it:
-  // at most 4 groups of 8 columns a thread.
-#define ADAHOP_NORM(WAVES, NV)                                                                   \
-  rmsnorm_kernel<XF32, Res, WAVES, NV>                                                           \
-      <<<dim3((unsigned)(WAVES == 1 ? (a.rows + 3) / 4 : a.rows)), dim3(WAVES == 1 ? 256 : 64 * WAVES), 0, \
-         stream>>>(a)
-  if (c <= 512) ADAHOP_NORM(1, 1);
-  else if (c <= 1024) ADAHOP_NORM(1, 2);
-  else if (c <= 2048) ADAHOP_NORM(1, 4);
-  else if (c <= 4096) ADAHOP_NORM(4, 2);
-  else if (c <= 8192) ADAHOP_NORM(4, 4);
-  else if (c <= 16384) ADAHOP_NORM(16, 2);
-  else ADAHOP_NORM(16, 4);
+  const NormShape shape = norm_shape(a.cols);
+  const dim3 grid((unsigned)norm_grid(a.rows, shape.waves)), block((unsigned)norm_block(shape.waves));
+#define ADAHOP_NORM(WAVES, NV) rmsnorm_kernel<XF32, Res, WAVES, NV><<<grid, block, 0, stream>>>(a)
+  if (shape.waves == 1) {
+    if (shape.groups == 1) ADAHOP_NORM(1, 1);
+    else if (shape.groups == 2) ADAHOP_NORM(1, 2);
+    else ADAHOP_NORM(1, 4);
+  } else if (shape.waves == 4) {
+    if (shape.groups == 2) ADAHOP_NORM(4, 2);
+    else ADAHOP_NORM(4, 4);
+  } else {
+    if (shape.groups == 2) ADAHOP_NORM(16, 2);
+    else ADAHOP_NORM(16, 4);
+  }
 #undef ADAHOP_NORM
   return check_launch("rmsnorm");
 }
@@ -385,8 +386,7 @@ adahop_status rmsnorm_launch(const void* x, int x_f32, const void* r, int r_f32,
                              float eps, void* h, int64_t ldh, uint16_t* y, int64_t ldy,
                              uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds, float* rstd,
                              hipStream_t stream) {
-  // A launch of up to 2^22 rows: its threads stay below 2^32.
-  constexpr int64_t kRows = int64_t{1} << 22;
+  constexpr int64_t kRows = kNormLaunchRows;
   for (int64_t at = 0; at < rows; at += kRows) {
     auto bytes = [at](const void* p, int64_t ld, int64_t size) {
       return p == nullptr ? nullptr : const_cast<char*>(static_cast<const char*>(p)) + at * ld * size;

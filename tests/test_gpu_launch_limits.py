@@ -1,0 +1,33 @@
+"""Sizes at which one launch would have 2^32 threads or more: the calls have to
+take them in pieces. Rows and columns around the pieces' borders are compared
+with calls of their own on them."""
+import pytest
+import torch
+
+import mxfp4_precision_gemms_amd as A
+from test_gpu_linear import DEV, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def free_memory():
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_norm_wide_rows():
+    """2^22 rows of which 16 waves share each: 104 GB."""
+    rows, cols = (1 << 22) + 40, 8224
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x.copy_(rand(1, cols, seed=1, dtype=torch.bfloat16).to(DEV).expand(rows, cols))
+    borders = [slice(0, 40), slice((1 << 21) - 20, (1 << 21) + 20), slice((1 << 22) - 20, (1 << 22) + 40)]
+    for k, at in enumerate(borders):
+        x[at] = rand(at.stop - at.start, cols, seed=2 + k, dtype=torch.bfloat16).to(DEV)
+    gain = (1 + rand(cols, seed=9, std=0.2)).to(DEV)
+    got = A.adahop_rmsnorm(x, gain, save_rstd=True)
+    for at in borders:
+        part = A.adahop_rmsnorm(x[at], gain, save_rstd=True)
+        for a, b in zip((got.codes, got.scales, got.rstd), (part.codes, part.scales, part.rstd)):
+            assert torch.equal(a[at], b)

@@ -23,4 +23,9 @@ constexpr int norm_block(int waves) { return waves == 1 ? 256 : 64 * waves; }
 // Rows of a launch: 2^31 threads where 16 waves share a row.
 constexpr int64_t kNormLaunchRows = int64_t{1} << 21;
 
+// Column sums over workgroups' parts: 16 columns a workgroup.
+constexpr int kReduceBlock = 1024;
+constexpr int64_t reduce_grid(int64_t cols) { return (cols + 15) / 16; }
+constexpr int64_t kReduceLaunchCols = int64_t{1} << 24;   // 2^30 threads
+
 }  // namespace adahop

@@ -240,19 +240,19 @@ __global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
   }
 }
 
-// out[c] = sum over p of partial[p][c]: a workgroup takes 16 columns, its 64
-// groups of 16 lanes every 64th part; their sums are added in pairs, in a
-// fixed tree. (4.9 us for 1024 x 2048, most of it latency.)
-__global__ void __launch_bounds__(1024) column_reduce_kernel(const float* __restrict__ partial,
-                                                             int parts, int64_t cols,
-                                                             float* __restrict__ out) {
+// out[c] = sum over p of partial[p][c], rows of partial `ld` apart: a workgroup
+// takes 16 columns, its 64 groups of 16 lanes every 64th part; their sums are
+// added in pairs, in a fixed tree. (4.9 us for 1024 x 2048, most of it latency.)
+__global__ void __launch_bounds__(kReduceBlock) column_reduce_kernel(const float* __restrict__ partial,
+                                                                     int parts, int64_t cols, int64_t ld,
+                                                                     float* __restrict__ out) {
   __shared__ float red[64][17];
   const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int64_t c = (int64_t)blockIdx.x * 16 + lane;
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 8
-    for (int p = group; p < parts; p += 64) s += partial[(int64_t)p * cols + c];
+    for (int p = group; p < parts; p += 64) s += partial[(int64_t)p * ld + c];
   }
   red[group][lane] = s;
 #pragma unroll
@@ -438,9 +438,14 @@ adahop_status rmsnorm_backward_launch(const void* dy, int dy_f32, const void* h,
 
 adahop_status column_reduce_launch(const float* partial, int parts, int64_t cols, float* out,
                                    hipStream_t stream) {
-  column_reduce_kernel<<<dim3((unsigned)((cols + 15) / 16)), dim3(1024), 0, stream>>>(partial, parts,
-                                                                                      cols, out);
-  return check_launch("column_reduce");
+  for (int64_t c = 0; c < cols; c += kReduceLaunchCols) {
+    const int64_t n = cols - c < kReduceLaunchCols ? cols - c : kReduceLaunchCols;
+    column_reduce_kernel<<<dim3((unsigned)reduce_grid(n)), dim3(kReduceBlock), 0, stream>>>(partial + c, parts, n,
+                                                                                          cols, out + c);
+    const adahop_status st = check_launch("column_reduce");
+    if (st != ADAHOP_OK) return st;
+  }
+  return ADAHOP_OK;
 }
 
 adahop_status mx8_quant_launch(const void* src, int f32, int64_t rows, int64_t cols, int64_t ld,

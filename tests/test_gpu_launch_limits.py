@@ -1,6 +1,6 @@
 """Sizes at which one launch would have 2^32 threads or more: the calls have to
 take them in pieces. Rows and columns around the pieces' borders are compared
-with calls of their own on them."""
+with calls of their own on them, or with the definition."""
 import pytest
 import torch
 
@@ -31,3 +31,22 @@ def test_norm_wide_rows():
         part = A.adahop_rmsnorm(x[at], gain, save_rstd=True)
         for a, b in zip((got.codes, got.scales, got.rstd), (part.codes, part.scales, part.rstd)):
             assert torch.equal(a[at], b)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_column_sums_of_many_columns(gated):
+    """Bias gradients of 2^26 columns and more."""
+    m, N = 3, (1 << 26) + 80
+    n = N // 2 if gated else N
+    g = torch.Generator(device=DEV).manual_seed(3)
+    z = torch.randn(m, N, device=DEV, generator=g).to(torch.bfloat16)
+    dout = torch.randn(m, n, device=DEV, generator=g)
+    dz, dbias = A.adahop_act_backward(dout, z, act="RELU", gated=gated, bias_grad=True)
+    zf = z.float()
+    want = dout * (zf[:, :n] > 0)
+    if gated:
+        want = torch.cat((want * zf[:, n:], dout * zf[:, :n].clamp(min=0)), 1)
+    assert torch.equal(dz, want.to(torch.bfloat16))
+    # two additions, each within 2^-24 of sums below sum |dz|
+    tol = 2.0 ** -23 * want.abs().sum(0)
+    assert bool(((dbias - want.double().sum(0)).abs() <= tol).all())

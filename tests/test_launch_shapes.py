@@ -39,3 +39,10 @@ def test_norm_launches(tmp_path):
         assert block in (256, 64 * waves) and block <= 1024
         assert grid * block < 2 ** 32, c
         assert 64 * waves * groups * 8 >= c and groups <= 4
+
+
+def test_column_sum_launches(tmp_path):
+    (grid, block, cols), = numbers(tmp_path, [
+        'printf("%lld %d %lld\\n", (long long)reduce_grid(kReduceLaunchCols), kReduceBlock,',
+        '(long long)kReduceLaunchCols);'])
+    assert grid * block < 2 ** 32 and grid * 16 >= cols

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "../../include/adahop.h"
+#include "linear_plan.h"
 
 namespace adahop {
 
@@ -232,16 +233,7 @@ struct LinearArgs {
   uint16_t* z;               // bf16 [m][N] or null
   int64_t ldz;
 };
-// Tile kernel of a product (linear_tiles.hip) and its workspace: scale words
-// by stage, then the K parts' sums.
-enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile32 = 3 };   // 256 rows >> shape
-struct TilePlan {
-  TileShape shape;
-  int parts;
-  size_t scale_bytes, part_bytes;
-  double us;                 // estimate
-};
-TilePlan linear_tile_plan(int64_t m, int64_t n, int64_t K, int b_fp4, int gated);
+
 // Whether the rows of a matrix, a tile's rows past its end included, lie
 // within the 31-bit offsets that the tile kernel uses.
 bool linear_tiles_reach(int64_t rows, int64_t ld);

@@ -278,13 +278,6 @@ void few_start(const LinearArgs& a, hipStream_t stream) {
          dim3(64 * WV), 0, stream>>>(a);
 }
 
-// 16 columns and 8 waves a workgroup while that makes at most two for each
-// compute unit (1 x 4096 x 14336, E2M1: 10.6 us, with 32 columns and 4 waves
-// 17.1), else 32 columns and 4 waves, which read A half as often (16 x 14336
-// gated x 4096: 21.0, with 16 columns 23.9). An MXFP8 block needs 32 (1 x 4096 x
-// 14336, exact: 15.7).
-bool few_narrow(int64_t n) { return n <= 16 * 512; }
-
 template <bool FP4, bool Gated>
 adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
   if (a.out_scales != nullptr) {
@@ -310,23 +303,6 @@ adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
   return check_launch("linear_mx");
 }
 
-// Estimate in microseconds, as linear_tile_plan's: a launch 3.5, all of B at
-// 5 TB/s, and what a compute unit reads of A and B (again for every 32 rows)
-// at 28 KB / us (32 columns a workgroup 20). It takes no workspace, so it does
-// not look at the output's type: the two differ little where the choice lies
-// near.
-double few_us(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
-  const double kb = (double)K / 1024, b = b_fp4 ? 17.0 / 32 : 33.0 / 32, a = 33.0 / 32;
-  const bool narrow = few_narrow(n);
-  const int cols = narrow ? 16 : 32;
-  const double down = (double)((m + 31) / 32), rows = (double)m / down;
-  const double groups = down * (double)((n + cols - 1) / cols) / (double)compute_units();
-  const double group_kb = kb * (cols * (gated ? 2 : 1) * b + rows * a);
-  const double cu = (groups < 1 ? 1 : groups) * group_kb / (narrow ? 28 : 20);
-  const double hbm = (double)n * (gated ? 2 : 1) * kb * b / 4883;
-  return 3.5 + (cu > hbm ? cu : hbm);
-}
-
 // Rows r0 .. r0 + rows - 1 and output columns c0 .. c0 + cols - 1 (a multiple
 // of 32, and all of them for a gated layer).
 LinearArgs part_of(const LinearArgs& a, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
@@ -345,38 +321,38 @@ LinearArgs part_of(const LinearArgs& a, int64_t r0, int64_t rows, int64_t c0, in
   return p;
 }
 
-// In launches whose grid's second dimension (blocks of 16 or 32 rows) fits.
+// In launches whose grid fits: its second dimension (blocks of 16 or 32 rows)
+// and, in its first, the threads.
 adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t stream) {
   constexpr int64_t kRows = int64_t{1} << 20;
-  for (int64_t r = 0; r < a.m; r += kRows) {
-    const LinearArgs p = part_of(a, r, a.m - r < kRows ? a.m - r : kRows, 0, a.n);
-    adahop_status st;
-    if (b_fp4) st = gated ? few_dispatch<true, true>(p, stream) : few_dispatch<true, false>(p, stream);
-    else st = gated ? few_dispatch<false, true>(p, stream) : few_dispatch<false, false>(p, stream);
-    if (st != ADAHOP_OK) return st;
-  }
+  const int64_t cols = gated ? a.n : kFewLaunchCols;
+  for (int64_t r = 0; r < a.m; r += kRows)
+    for (int64_t c = 0; c < a.n; c += cols) {
+      const LinearArgs p = part_of(a, r, a.m - r < kRows ? a.m - r : kRows, c, a.n - c < cols ? a.n - c : cols);
+      adahop_status st;
+      if (b_fp4) st = gated ? few_dispatch<true, true>(p, stream) : few_dispatch<true, false>(p, stream);
+      else st = gated ? few_dispatch<false, true>(p, stream) : few_dispatch<false, false>(p, stream);
+      if (st != ADAHOP_OK) return st;
+    }
   return ADAHOP_OK;
 }
 
 }  // namespace
 
-bool take_few(int64_t m, const TilePlan& p, int64_t n, int64_t K, int b_fp4, int gated) {
-  return few_us(m, n, K, b_fp4, gated) <= p.us;
-}
-
 size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
-  const TilePlan p = linear_tile_plan(m, n, K, b_fp4, gated);
-  return take_few(m, p, n, K, b_fp4, gated) ? 0 : p.scale_bytes + p.part_bytes;
+  const TilePlan p = linear_tile_plan(m, n, K, b_fp4, gated, compute_units());
+  return take_few(m, p, n, K, b_fp4, gated, compute_units()) ? 0 : p.scale_bytes + p.part_bytes;
 }
 
 adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* scratch, size_t,
                                hipStream_t stream) {
   if (a.m == 0) return ADAHOP_OK;
-  const TilePlan plan = linear_tile_plan(a.m, a.n, a.K, b_fp4, gated);
+  const int64_t cus = compute_units();
+  const TilePlan plan = linear_tile_plan(a.m, a.n, a.K, b_fp4, gated, cus);
   // An MXFP8 output of few values comes from exact products (at most 32768:
   // above, its roundings that fall the other way are an even share of it). It
   // costs time where tiles would be faster: 33 x 960 x 14336 26 us, tiles 13.
-  if (take_few(a.m, plan, a.n, a.K, b_fp4, gated) || (a.out_scales != nullptr && a.m * a.n <= 32768))
+  if (take_few(a.m, plan, a.n, a.K, b_fp4, gated, cus) || (a.out_scales != nullptr && a.m * a.n <= 32768))
     return few_launch(a, b_fp4, gated, stream);
   if (linear_tiles_reach(a.m, a.lda) && linear_tiles_reach(a.n, a.ldb))
     return linear_tiles_launch(a, b_fp4, gated, plan, scratch, stream);

@@ -681,45 +681,6 @@ adahop_status shape_launch(const LinearArgs& a, const TilePlan& p, const TileArg
 
 bool linear_tiles_reach(int64_t rows, int64_t ld) { return extent_ok(rows, ld); }
 
-// Estimates in microseconds, from measurements on the whole device (256 CUs):
-// a launch and a tile's first loads and epilogue 5, a stage 0.1 and its bytes
-// at 55 KB / us a compute unit (32 x 128 tiles 0.33 and 0.45, 64 x 128 0.4 and
-// 0.53, 128 x 128 0.57 and 0.65, E2M1 and E4M3 weights), of 256 x 256 tiles
-// 1.45 and 1.55 with 4 for ordering the scales; K parts 3 for the second
-// kernel and their sums written and read at 4 TB/s. On 36 cases (m = 40 ..
-// 3000, six weights) the choice was within 6 % of the fastest of all shapes
-// with 1, 2, 4 and 8 parts on 34, at worst 16 % off.
-TilePlan linear_tile_plan(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
-  const int64_t N = gated ? 2 * n : n, nk = (K + 127) / 128, cus = compute_units();
-  TilePlan best{};
-  best.us = 1e30;
-  for (int shape = kTile256; shape <= kTile32; ++shape) {
-    const int lm = 8 - shape, ln = shape == kTile256 ? 8 : 7;     // log2 of the tile's rows and columns
-    const int lu = shape == kTile256 ? 1 : 2;                     // and of the stages that parts are made of
-    const double kb = (double)((128 << lm) + ((b_fp4 ? 64 : 128) << ln)) / 1024;
-    const double stage = shape == kTile256 ? (b_fp4 ? 1.45 : 1.55) : 0.1 + kb / 55;
-    // The smaller tiles of E2M1 weights run two to a compute unit.
-    const bool two = b_fp4 && lm <= 6;
-    const int64_t tiles = ((m + (1 << lm) - 1) >> lm) * ((N + (1 << ln) - 1) >> ln);
-    const uint32_t units = (uint32_t)((nk + (1 << lu) - 1) >> lu);
-    for (const uint32_t parts : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u}) {
-      if (parts > units || (parts > 1 && tiles * parts > 2 * cus)) break;
-      const double rounds = parts == 1 ? (double)((tiles + cus - 1) / cus) : tiles * parts > cus ? 2 : 1;
-      double us = 5 + rounds * (double)((units + parts - 1) / parts << lu) * stage;
-      if (shape == kTile256) us += 4;
-      else us += (K % 512 ? 3 : 0) + (two ? 0 : 1.5 * (rounds - 1));
-      if (parts > 1) us += 3 + (double)parts * (double)m * (double)N * 8 / 4e6;
-      if (us < best.us) {
-        best = {(TileShape)shape, (int)parts, 0, 0, us};
-        if (parts > 1) best.part_bytes = (size_t)tiles * 4 * parts << (lm + ln);
-      }
-    }
-  }
-  // Whole groups of 64 rows, gated 32 columns' gate and up rows, and 4 stages.
-  best.scale_bytes = (size_t)((nk + 3) / 4 * 16 * (m + N + 256));
-  return best;
-}
-
 adahop_status linear_tiles_launch(const LinearArgs& a, int b_fp4, int gated, const TilePlan& p, void* scratch,
                                   hipStream_t stream) {
   const int64_t parts = gated ? 2 : 1, N = parts * a.n, Ks = a.K / 32;

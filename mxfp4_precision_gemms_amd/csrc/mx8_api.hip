@@ -126,14 +126,14 @@ adahop_status norm_back(const adahop_rmsnorm_backward_args* a, void* ws, size_t 
 }
 
 bool valid_product(int64_t m, int64_t N, int64_t K) {
-  return m >= 0 && N >= 1 && K >= 1 && K % 32 == 0 && m < kMaxDim && N < kMaxDim && K < kMaxDim;
+  return m >= 0 && N >= 1 && K >= 1 && K % 32 == 0 && m < kMaxDim && N <= kMaxLinearN && K < kMaxDim;
 }
 
 adahop_status linear(const adahop_linear_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (a == nullptr) return invalid("linear_mx: null arguments");
   if (a->m < 0 || a->N < 1 || a->K < 1) return invalid("linear_mx: m must be >= 0, N and K >= 1");
   if (a->K % 32 != 0) return invalid("linear_mx: K is not a multiple of 32");
-  if (!valid_product(a->m, a->N, a->K)) return unsupported("linear_mx: m, N or K of 2^30 or more");
+  if (!valid_product(a->m, a->N, a->K)) return unsupported("linear_mx: m or K of 2^30 or more, or N above 2^30 - 64");
   if (!all_zero(a->reserved)) return invalid("linear_mx: reserved fields must be 0");
   if (a->b_format != ADAHOP_MX_E2M1 && a->b_format != ADAHOP_MX_E4M3)
     return invalid("linear_mx: bad b_format");

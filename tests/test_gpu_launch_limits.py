@@ -6,6 +6,7 @@ import torch
 
 import mxfp4_precision_gemms_amd as A
 from test_gpu_linear import DEV, rand
+from test_gpu_linear_tiles import check_at, codes
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,9 @@ def test_column_sums_of_many_columns(gated):
     # two additions, each within 2^-24 of sums below sum |dz|
     tol = 2.0 ** -23 * want.abs().sum(0)
     assert bool(((dbias - want.double().sum(0)).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("gated,N", [(False, (1 << 29) + 96), (True, (1 << 30) - 64)])
+def test_linear_of_many_columns(gated, N):
+    """Weights of 2^29 rows and more, 9 and 17 GB."""
+    check_at(codes(2, 32, 10), codes(N, 32, 11, "MXFP4"), "MXFP4", act="RELU" if gated else "NONE", gated=gated)

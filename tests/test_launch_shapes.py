@@ -1,5 +1,5 @@
 """The launch shapes of the norm and linear layer's kernels, computed on the
-host by the header that the kernels' launches use: no launch may have 2^32
+host by the headers that the kernels' launches use: no launch may have 2^32
 threads or more in a dimension. No GPU."""
 import os
 import shutil
@@ -16,7 +16,7 @@ def evaluate(tmp_path, lines):
     if cxx is None:
         pytest.skip("no C++ compiler")
     src, exe = tmp_path / "shapes.cpp", tmp_path / "shapes"
-    src.write_text('#include <cstdio>\n#include <initializer_list>\n#include "launch_shapes.h"\nusing namespace adahop;\nint main() {\n'
+    src.write_text('#include <cstdio>\n#include <initializer_list>\n#include "launch_shapes.h"\n#include "linear_plan.h"\nusing namespace adahop;\nint main() {\n'
                    + "\n".join(lines) + "\n}\n")
     subprocess.run([cxx, "-std=c++17", "-Wall", "-Werror", "-I" + CSRC, str(src), "-o", str(exe)], check=True)
     return subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")[:-1]
@@ -46,3 +46,25 @@ def test_column_sum_launches(tmp_path):
         'printf("%lld %d %lld\\n", (long long)reduce_grid(kReduceLaunchCols), kReduceBlock,',
         '(long long)kReduceLaunchCols);'])
     assert grid * block < 2 ** 32 and grid * 16 >= cols
+
+
+def test_few_row_launches(tmp_path):
+    """A launch of the widest piece, and of the widest gated layer, which goes
+    at once."""
+    (plain, gated, cols, most), = numbers(tmp_path, [
+        'printf("%lld %lld %lld %lld\\n", (long long)few_wide_threads(kFewLaunchCols),',
+        '(long long)few_wide_threads(kMaxLinearN / 2), (long long)kFewLaunchCols, (long long)kMaxLinearN);'])
+    assert plain < 2 ** 32 and gated < 2 ** 32
+    assert cols % 32 == 0 and most < 2 ** 30
+    assert plain >= 8 * cols and gated >= 4 * most
+
+
+@pytest.mark.parametrize("N,status", [((1 << 30) - 64, 1), ((1 << 30) - 63, 2), ((1 << 30) - 1, 2)])
+def test_widest_layer(N, status):
+    """(INVALID for ld_out, which is looked at later, and UNSUPPORTED)"""
+    import ctypes
+
+    import mxfp4_precision_gemms_amd as A
+    a = A.LinearArgs(m=4, N=N, K=96, a_codes=4096, ld_a_codes=96, a_scales=4096, ld_a_scales=3, b_codes=4096,
+                     ld_b_codes=96, b_scales=4096, ld_b_scales=3, out=4096, ld_out=64, b_format=1)
+    assert A.lib().adahop_linear_mx(ctypes.byref(a), None, 0, None) == status

@@ -93,7 +93,7 @@ class LinearArgs(ctypes.Structure):
                 ("bias", _p), ("residual", _p), ("ld_residual", _i64), ("out", _p),
                 ("ld_out", _i64), ("out_scales", _p), ("ld_out_scales", _i64), ("z", _p),
                 ("ld_z", _i64), ("b_format", _i32), ("bias_dtype", _i32), ("act", _i32),
-                ("gated", _i32), ("reserved", _i32 * 4)]
+                ("gated", _i32), ("products", _i32), ("reserved", _i32 * 3)]
 
 
 # Exported symbols and their C signatures (argtypes, restype).
@@ -552,6 +552,7 @@ def ctx_views(ctx: torch.Tensor, plan: CtxPlan) -> dict:
 # ---------------------------------------------------------------------------
 ACT = {"NONE": 0, "RELU": 1, "SILU": 2, "GELU": 3, "GELU_TANH": 4}
 MX_FORMAT = {"MXFP4": 0, "MXFP8": 1}
+PRODUCTS = {"AUTO": 0, "SCALED": 1, "EXACT": 2}
 _FLOAT = {torch.bfloat16: 0, torch.int16: 0, torch.float32: 1}
 _BF16 = {torch.bfloat16: 0, torch.int16: 0}
 _CODES = {torch.uint8: 0, torch.float8_e4m3fn: 0}
@@ -722,13 +723,15 @@ def adahop_linear_mx(a: Tuple[torch.Tensor, torch.Tensor], b: Tuple[torch.Tensor
                      bias: Optional[torch.Tensor] = None, act: str = "NONE", gated: bool = False,
                      residual: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
                      save_z: bool = False, out: Optional[torch.Tensor] = None,
-                     ws: Optional[torch.Tensor] = None) -> LinearOut:
+                     ws: Optional[torch.Tensor] = None, products: str = "AUTO") -> LinearOut:
     """act(z) + residual with z = A B^T + bias; gated: act(z[:, :n]) * z[:, n:].
 
     a: MXFP8 (codes [m, K], scales [m, K/32]); b: weights [N, K] in MXFP8, or
     in MXFP4 (codes [N, K/2], as adahop_iht_quant gives them). out_dtype:
     torch.bfloat16, or "MXFP8" for codes and scales. out (bf16) may be given,
-    the residual itself among others."""
+    the residual itself among others. products: "EXACT", "SCALED" (faster on
+    many rows; moves about one MXFP8 code in a thousand to its neighbour), or
+    "AUTO": EXACT for MXFP8 outputs of up to 32768 values, else SCALED."""
     (ac, asc), (bc, bsc) = a, b
     m, K = _size(ac, "a codes")
     N, Kb = _size(bc, "b codes")
@@ -766,7 +769,7 @@ def adahop_linear_mx(a: Tuple[torch.Tensor, torch.Tensor], b: Tuple[torch.Tensor
         z = ac.new_empty((m, N), dtype=torch.bfloat16)
         zp = z.data_ptr()
     g = LinearArgs(m, N, K, ap, lda, asp, ldas, bp, ldb, bsp, ldbs, biasp, rp, ldr, op, ldo, sp, lds, zp, N,
-                   fmt, bk, ACT[act], 1 if gated else 0)
+                   fmt, bk, ACT[act], 1 if gated else 0, PRODUCTS[products])
     wp, wn, ws = _scratch(lib().adahop_linear_mx_workspace_size(m, N, K, fmt, g.gated), ws, dev)
     _check(lib().adahop_linear_mx(ctypes.byref(g), wp, wn, _stream(dev)))
     return LinearOut(out, scales, z)

@@ -239,8 +239,9 @@ struct LinearArgs {
 bool linear_tiles_reach(int64_t rows, int64_t ld);
 adahop_status linear_tiles_launch(const LinearArgs& a, int b_fp4, int gated, const TilePlan& p, void* scratch,
                                   hipStream_t stream);
-size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated);
-adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* scratch,
-                               size_t scratch_bytes, hipStream_t stream);
+// Scaled products need scratch, exact ones none.
+size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated, bool mx8_out);
+adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, bool exact, void* scratch,
+                               hipStream_t stream);
 
 }  // namespace adahop

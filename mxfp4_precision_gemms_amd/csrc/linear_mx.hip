@@ -15,8 +15,8 @@
 // mean square), 5e-5 where 1 % of A's columns are 30 times the rest, at any K.
 // bf16 products of the same values are exact up to the fp32 sums, at half the
 // rate; an output in bf16 or E4M3 is off by 1.7e-3 or 2.6e-2 by its own
-// rounding, so large products take the faster one, and no fp32 output is
-// offered. MXFP8 outputs of few rows or few values take bf16 products.
+// rounding, so large products take the faster one unless the caller asks for
+// exact ones, and no fp32 output is offered. exact_products has the rule.
 // The sums over K, the bias, the activation and the residual are in fp32;
 // one rounding to the output.
 #include "adahop_internal.h"
@@ -50,9 +50,8 @@ constexpr int kBufferFlags = 0x00020000;   // raw buffer descriptor word 3
 constexpr int kPastEnd = 0x7FFFFFF0;       // an offset past the end of every buffer here
 
 // Exact: the products on bf16 matrix cores, in which both formats' scaled
-// values are exact, instead of the scaled ones, so that an MXFP8 output of few
-// values, where one code rounded the other way shows, is that of exact sums. A
-// lane's 32 elements of 128 are one block, 32 g .. + 31, of both operands. (1 x
+// values are exact, instead of the scaled ones, so that an MXFP8 output, where
+// one code rounded the other way shows, is that of exact sums. A lane's 32 elements of 128 are one block, 32 g .. + 31, of both operands. (1 x
 // 2048 x 4096, E2M1: 6.6 us, scaled and in bf16 5.0; 1 x 14336 x 4096: 11.7
 // and 10.8.)
 template <bool FP4, bool Gated, bool Exact, int MT, int NB, int WV, int T>
@@ -278,28 +277,29 @@ void few_start(const LinearArgs& a, hipStream_t stream) {
          dim3(64 * WV), 0, stream>>>(a);
 }
 
-template <bool FP4, bool Gated>
-adahop_status few_dispatch(const LinearArgs& a, hipStream_t stream) {
-  if (a.out_scales != nullptr) {
-    // 8 waves by the same rule (1 x 2048 x 4096, E2M1: 6.6 us, with 4 waves
-    // 7.7; 1 x 14336 x 4096: 13.3, with 4 waves 11.7); gated, whose registers
-    // do not last for 8, 4.
-    if constexpr (!Gated) {
-      if (few_narrow(a.n)) {
-        if (a.m <= 16) few_start<FP4, Gated, true, 1, 2, 8, FP4 ? 4 : 2>(a, stream);
-        else few_start<FP4, Gated, true, 2, 2, 8, 2>(a, stream);
-        return check_launch("linear_few");
-      }
+// 32 columns a workgroup: 8 waves by the same rule (1 x 2048 x 4096, E2M1,
+// exact: 6.6 us, with 4 waves 7.7; 1 x 14336 x 4096: 13.3, with 4 waves 11.7);
+// gated, whose registers do not last for 8, 4.
+template <bool FP4, bool Gated, bool Exact>
+adahop_status few_wide(const LinearArgs& a, hipStream_t stream) {
+  if constexpr (!Gated) {
+    if (few_narrow(a.n)) {
+      if (a.m <= 16) few_start<FP4, Gated, Exact, 1, 2, 8, FP4 ? 4 : 2>(a, stream);
+      else few_start<FP4, Gated, Exact, 2, 2, 8, 2>(a, stream);
+      return check_launch("linear_mx");
     }
-    if (a.m <= 16) few_start<FP4, Gated, true, 1, 2, 4, 2>(a, stream);
-    else few_start<FP4, Gated, true, 2, 2, 4, 2>(a, stream);
-  } else if (few_narrow(a.n)) {
-    if (a.m <= 16) few_start<FP4, Gated, false, 1, 1, 8, 2>(a, stream);
-    else few_start<FP4, Gated, false, 2, 1, 8, 2>(a, stream);
-  } else {
-    if (a.m <= 16) few_start<FP4, Gated, false, 1, 2, 4, 2>(a, stream);
-    else few_start<FP4, Gated, false, 2, 2, 4, 2>(a, stream);
   }
+  if (a.m <= 16) few_start<FP4, Gated, Exact, 1, 2, 4, 2>(a, stream);
+  else few_start<FP4, Gated, Exact, 2, 2, 4, 2>(a, stream);
+  return check_launch("linear_mx");
+}
+
+template <bool FP4, bool Gated>
+adahop_status few_dispatch(const LinearArgs& a, bool exact, hipStream_t stream) {
+  if (exact) return few_wide<FP4, Gated, true>(a, stream);
+  if (a.out_scales != nullptr || !few_narrow(a.n)) return few_wide<FP4, Gated, false>(a, stream);
+  if (a.m <= 16) few_start<FP4, Gated, false, 1, 1, 8, 2>(a, stream);
+  else few_start<FP4, Gated, false, 2, 1, 8, 2>(a, stream);
   return check_launch("linear_mx");
 }
 
@@ -323,15 +323,15 @@ LinearArgs part_of(const LinearArgs& a, int64_t r0, int64_t rows, int64_t c0, in
 
 // In launches whose grid fits: its second dimension (blocks of 16 or 32 rows)
 // and, in its first, the threads.
-adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t stream) {
+adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, bool exact, hipStream_t stream) {
   constexpr int64_t kRows = int64_t{1} << 20;
   const int64_t cols = gated ? a.n : kFewLaunchCols;
   for (int64_t r = 0; r < a.m; r += kRows)
     for (int64_t c = 0; c < a.n; c += cols) {
       const LinearArgs p = part_of(a, r, a.m - r < kRows ? a.m - r : kRows, c, a.n - c < cols ? a.n - c : cols);
       adahop_status st;
-      if (b_fp4) st = gated ? few_dispatch<true, true>(p, stream) : few_dispatch<true, false>(p, stream);
-      else st = gated ? few_dispatch<false, true>(p, stream) : few_dispatch<false, false>(p, stream);
+      if (b_fp4) st = gated ? few_dispatch<true, true>(p, exact, stream) : few_dispatch<true, false>(p, exact, stream);
+      else st = gated ? few_dispatch<false, true>(p, exact, stream) : few_dispatch<false, false>(p, exact, stream);
       if (st != ADAHOP_OK) return st;
     }
   return ADAHOP_OK;
@@ -339,21 +339,20 @@ adahop_status few_launch(const LinearArgs& a, int b_fp4, int gated, hipStream_t 
 
 }  // namespace
 
-size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated) {
-  const TilePlan p = linear_tile_plan(m, n, K, b_fp4, gated, compute_units());
-  return take_few(m, p, n, K, b_fp4, gated, compute_units()) ? 0 : p.scale_bytes + p.part_bytes;
+size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated, bool mx8_out) {
+  const int64_t cus = compute_units();
+  const TilePlan p = linear_tile_plan(m, n, K, b_fp4, gated, cus);
+  return take_few(m, p, n, K, b_fp4, gated, mx8_out, cus) ? 0 : p.scale_bytes + p.part_bytes;
 }
 
-adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* scratch, size_t,
+adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, bool exact, void* scratch,
                                hipStream_t stream) {
   if (a.m == 0) return ADAHOP_OK;
+  if (exact) return few_launch(a, b_fp4, gated, true, stream);
   const int64_t cus = compute_units();
   const TilePlan plan = linear_tile_plan(a.m, a.n, a.K, b_fp4, gated, cus);
-  // An MXFP8 output of few values comes from exact products (at most 32768:
-  // above, its roundings that fall the other way are an even share of it). It
-  // costs time where tiles would be faster: 33 x 960 x 14336 26 us, tiles 13.
-  if (take_few(a.m, plan, a.n, a.K, b_fp4, gated, cus) || (a.out_scales != nullptr && a.m * a.n <= 32768))
-    return few_launch(a, b_fp4, gated, stream);
+  if (take_few(a.m, plan, a.n, a.K, b_fp4, gated, a.out_scales != nullptr, cus))
+    return few_launch(a, b_fp4, gated, false, stream);
   if (linear_tiles_reach(a.m, a.lda) && linear_tiles_reach(a.n, a.ldb))
     return linear_tiles_launch(a, b_fp4, gated, plan, scratch, stream);
   // Operands of 2 GB and more: in pieces that the tile kernel's offsets
@@ -365,7 +364,7 @@ adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, void* 
     return c > 0 && linear_tiles_reach(c, ld) ? c : int64_t{0};
   };
   const int64_t rows = most(a.m, a.lda), cols = most(a.n, a.ldb);
-  if (rows == 0 || cols == 0 || (gated && cols < a.n)) return few_launch(a, b_fp4, gated, stream);
+  if (rows == 0 || cols == 0 || (gated && cols < a.n)) return few_launch(a, b_fp4, gated, false, stream);
   for (int64_t r = 0; r < a.m; r += rows)
     for (int64_t c = 0; c < a.n; c += cols) {
       const LinearArgs p = part_of(a, r, a.m - r < rows ? a.m - r : rows, c, a.n - c < cols ? a.n - c : cols);

@@ -12,6 +12,18 @@ namespace adahop {
 // make less than 2^24 groups of 32).
 constexpr int64_t kMaxLinearN = (int64_t{1} << 30) - 64;
 
+// Whether the products are formed exactly (products: adahop_products). AUTO goes
+// by the output alone, so that a caller can tell, and a device's or an
+// estimate's change moves no result. Up to 32768 MXFP8 values come mostly from
+// few rows, where loads bind and exact products cost little (microseconds exact
+// and scaled: 1 x 4096 x 14336, E2M1 15.5 and 13.8, 1 x 14336 gated x 4096 20.5
+// and 18.0, 8 x 4096 x 4096, E4M3 10.2 and 9.6); the most where few columns
+// meet a long K (32 x 960 x 14336: 26 and 10.5). Above, tiles are faster by up
+// to two times at 32 rows (14336 gated x 4096, E4M3: 47 and 29), four at 100.
+constexpr bool exact_products(int products, bool mx8_out, int64_t m, int64_t n) {
+  return products == 2 || (products == 0 && mx8_out && m * n <= 32768);
+}
+
 // Tile kernel of a product (linear_tiles.hip) and its workspace: scale words
 // by stage, then the K parts' sums.
 enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile32 = 3 };   // 256 rows >> shape
@@ -74,25 +86,27 @@ constexpr int64_t few_wide_threads(int64_t n) { return (n + 31) / 32 * 256; }
 static_assert(few_wide_threads(kFewLaunchCols) < int64_t{1} << 32 &&
               few_wide_threads(kMaxLinearN / 2) < int64_t{1} << 32, "");
 
-// Estimate in microseconds, as linear_tile_plan's: a launch 3.5, all of B at
-// 5 TB/s, and what a compute unit reads of A and B (again for every 32 rows)
-// at 28 KB / us (32 columns a workgroup 20). It takes no workspace, so it does
-// not look at the output's type: the two differ little where the choice lies
-// near.
-inline double few_us(int64_t m, int64_t n, int64_t K, int b_fp4, int gated, int64_t cus) {
+// Estimate in microseconds, as linear_tile_plan's, for scaled products: a launch
+// 3.5, all of B at 5 TB/s, and what a compute unit reads of A and B (again for
+// every 32 rows) at 28 KB / us with 8 waves (24 where workgroups of 32 columns
+// share one) and 20 with 4. On 162 cases of each type (m = 1 .. 100, nine
+// weights in both formats) the choice against the tiles was within 6 % of the
+// faster on 153 (MXFP8 out) and 158 (bf16), at worst 23 % and 26 % off.
+inline double few_us(int64_t m, int64_t n, int64_t K, int b_fp4, int gated, bool mx8_out, int64_t cus) {
   const double kb = (double)K / 1024, b = b_fp4 ? 17.0 / 32 : 33.0 / 32, a = 33.0 / 32;
-  const bool narrow = few_narrow(n);
-  const int cols = narrow ? 16 : 32;
+  const int cols = few_narrow(n) && !mx8_out ? 16 : 32;
+  const bool eight = few_narrow(n) && !(mx8_out && gated);
   const double down = (double)((m + 31) / 32), rows = (double)m / down;
   const double groups = down * (double)((n + cols - 1) / cols) / (double)cus;
   const double group_kb = kb * (cols * (gated ? 2 : 1) * b + rows * a);
-  const double cu = (groups < 1 ? 1 : groups) * group_kb / (narrow ? 28 : 20);
+  const double cu = (groups < 1 ? 1 : groups) * group_kb / (!eight ? 20 : mx8_out && groups > 1 ? 24 : 28);
   const double hbm = (double)n * (gated ? 2 : 1) * kb * b / 4883;
   return 3.5 + (cu > hbm ? cu : hbm);
 }
 
-inline bool take_few(int64_t m, const TilePlan& p, int64_t n, int64_t K, int b_fp4, int gated, int64_t cus) {
-  return few_us(m, n, K, b_fp4, gated, cus) <= p.us;
+inline bool take_few(int64_t m, const TilePlan& p, int64_t n, int64_t K, int b_fp4, int gated, bool mx8_out,
+                     int64_t cus) {
+  return few_us(m, n, K, b_fp4, gated, mx8_out, cus) <= p.us;
 }
 
 }  // namespace adahop

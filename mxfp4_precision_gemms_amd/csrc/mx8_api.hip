@@ -140,6 +140,8 @@ adahop_status linear(const adahop_linear_args* a, void* ws, size_t ws_bytes, hip
   if (a->act < ADAHOP_ACT_NONE || a->act > ADAHOP_ACT_GELU_TANH)
     return invalid("linear_mx: bad activation");
   if (a->gated != 0 && a->gated != 1) return invalid("linear_mx: gated must be 0 or 1");
+  if (a->products < ADAHOP_PRODUCTS_AUTO || a->products > ADAHOP_PRODUCTS_EXACT)
+    return invalid("linear_mx: bad products");
   if (a->gated && a->N % 2 != 0) return invalid("linear_mx: a gated layer needs an even N");
   const int64_t n = a->gated ? a->N / 2 : a->N;
   const bool fp4 = a->b_format == ADAHOP_MX_E2M1;
@@ -162,13 +164,15 @@ adahop_status linear(const adahop_linear_args* a, void* ws, size_t ws_bytes, hip
     return unsupported("linear_mx: codes of A and B must be 16-byte aligned, rows included");
   if (a->ld_b_codes >= kMaxRowBytes || a->ld_b_scales >= kMaxRowBytes)
     return unsupported("linear_mx: rows of B 32 MB or more apart");
-  ADAHOP_TRY(need_workspace(ws, ws_bytes, linear_mx_scratch_bytes(a->m, n, a->K, fp4, a->gated),
-                            "linear_mx"));
+  const bool mx8_out = a->out_scales != nullptr, exact = exact_products(a->products, mx8_out, a->m, n);
+  if (!exact)
+    ADAHOP_TRY(need_workspace(ws, ws_bytes, linear_mx_scratch_bytes(a->m, n, a->K, fp4, a->gated, mx8_out),
+                              "linear_mx"));
   const LinearArgs g = {a->a_codes, a->a_scales, a->b_codes, a->b_scales, a->ld_a_codes,
                         a->ld_a_scales, a->ld_b_codes, a->ld_b_scales, a->m, n, a->K, a->bias,
                         a->bias_dtype, a->act, a->residual, a->ld_residual, a->out, a->ld_out,
                         a->out_scales, a->ld_out_scales, a->z, a->ld_z};
-  return linear_mx_launch(g, fp4, a->gated, ws, ws_bytes, stream);
+  return linear_mx_launch(g, fp4, a->gated, exact, ws, stream);
 }
 
 size_t act_back_bytes(int64_t m, int64_t N, int32_t gated) {
@@ -238,7 +242,11 @@ adahop_status adahop_rmsnorm_backward(const adahop_rmsnorm_backward_args* args, 
 size_t adahop_linear_mx_workspace_size(int64_t m, int64_t N, int64_t K, adahop_mx_format b_format,
                                        int32_t gated) {
   if (!valid_product(m, N, K) || (gated && N % 2 != 0)) return 0;
-  return linear_mx_scratch_bytes(m, gated ? N / 2 : N, K, b_format == ADAHOP_MX_E2M1, gated);
+  // Of the two types of output, the one that needs more.
+  const int64_t n = gated ? N / 2 : N;
+  const size_t bf16 = linear_mx_scratch_bytes(m, n, K, b_format == ADAHOP_MX_E2M1, gated, false);
+  const size_t mx8 = linear_mx_scratch_bytes(m, n, K, b_format == ADAHOP_MX_E2M1, gated, true);
+  return bf16 > mx8 ? bf16 : mx8;
 }
 
 adahop_status adahop_linear_mx(const adahop_linear_args* args, void* ws, size_t ws_bytes,

@@ -68,3 +68,28 @@ def test_widest_layer(N, status):
     a = A.LinearArgs(m=4, N=N, K=96, a_codes=4096, ld_a_codes=96, a_scales=4096, ld_a_scales=3, b_codes=4096,
                      ld_b_codes=96, b_scales=4096, ld_b_scales=3, out=4096, ld_out=64, b_format=1)
     assert A.lib().adahop_linear_mx(ctypes.byref(a), None, 0, None) == status
+
+
+def test_exact_products_rule(tmp_path):
+    """AUTO is exact for MXFP8 outputs of up to 32768 values, whatever K, the
+    weights or the device; SCALED and EXACT are what they say."""
+    cases = [(1, 32768), (1, 32800), (32, 1024), (33, 1024), (100, 320), (1024, 32), (1025, 32)]
+    got = numbers(tmp_path, [
+        f'printf("%d %d %d %d %d %d\\n", (int)exact_products(0, true, {m}, {n}), (int)exact_products(0, false, {m}, {n}),'
+        f' (int)exact_products(1, true, {m}, {n}), (int)exact_products(1, false, {m}, {n}),'
+        f' (int)exact_products(2, true, {m}, {n}), (int)exact_products(2, false, {m}, {n}));' for m, n in cases])
+    for (m, n), g in zip(cases, got):
+        assert g == [int(m * n <= 32768), 0, 0, 0, 1, 1], (m, n)
+
+
+@pytest.mark.parametrize("products,status", [(-1, 1), (3, 1), (1, 3), (0, 3)])
+def test_bad_products(products, status):
+    """(1: INVALID; 3: WORKSPACE, which is looked at later)"""
+    import ctypes
+
+    import mxfp4_precision_gemms_amd as A
+    a = A.LinearArgs(m=4096, N=4096, K=96, a_codes=4096, ld_a_codes=96, a_scales=4096, ld_a_scales=3, b_codes=4096,
+                     ld_b_codes=96, b_scales=4096, ld_b_scales=3, out=4096, ld_out=4096, b_format=1,
+                     products=products)
+    assert A.lib().adahop_linear_mx_workspace_size(4096, 4096, 96, 1, 0) > 0
+    assert A.lib().adahop_linear_mx(ctypes.byref(a), None, 0, None) == status

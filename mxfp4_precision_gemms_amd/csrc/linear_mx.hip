@@ -50,10 +50,12 @@ constexpr int kBufferFlags = 0x00020000;   // raw buffer descriptor word 3
 constexpr int kPastEnd = 0x7FFFFFF0;       // an offset past the end of every buffer here
 
 // Exact: the products on bf16 matrix cores, in which both formats' scaled
-// values are exact, instead of the scaled ones, so that an MXFP8 output, where
-// one code rounded the other way shows, is that of exact sums. A lane's 32 elements of 128 are one block, 32 g .. + 31, of both operands. (1 x
-// 2048 x 4096, E2M1: 6.6 us, scaled and in bf16 5.0; 1 x 14336 x 4096: 11.7
-// and 10.8.)
+// values are exact (near the ends of E8M0's range without their scales), instead
+// of the scaled ones, so that an MXFP8 output, where one code rounded the other
+// way shows, is that of exact sums. A lane's 32 elements of 128 are one block,
+// 32 g .. + 31, of both operands. (1 x 2048 x 4096, E2M1: 6.8 us, scaled and in
+// bf16 5.0; 1 x 14336 x 4096: 11.9 and 10.8; 1.6 % of it, on average, looks for
+// far scales.)
 template <bool FP4, bool Gated, bool Exact, int MT, int NB, int WV, int T>
 __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__                        // the host pass needs the launch stub alone
@@ -150,8 +152,9 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
         const int k = k0 + 128 * t + 32 * g;
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-          r.sb[j][t] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(j < NB ? bs0 : bs1,
-                                                                     k < K ? os[j % NB] + k / 32 : kPastEnd, 0, 0)
+          r.sb[j][t] = ((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(j < NB ? bs0 : bs1,
+                                                                      k < K ? os[j % NB] + k / 32 : kPastEnd, 0, 0) |
+                        (k < K ? 0u : 127u))
                        << (8 * g);
 #pragma unroll
         for (int i = 0; i < MT; ++i) r.sa[i][t] = (k < K ? (uint32_t)as[i][k / 32] : 127u) << (8 * g);
@@ -193,17 +196,101 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
     }
     return e;
   };
+  // Scales for which bf16 holds every value of a block: a code's last bit is
+  // 2^-9 (E2M1: 2^-1), bf16's least normal number 2^-126, and 448 * 2^119 (6 *
+  // 2^125) the largest below 2^128. Byte 255 makes NaNs, and in a block of zeros,
+  // past B's rows too, any scale will do.
+  auto low = [](bool fp4) { return fp4 ? 2u : 10u; };
+  auto high = [](bool fp4) { return fp4 ? 252u : 246u; };
+  auto outside = [&](uint32_t byte, bool fp4) { return byte != 255u && (byte < low(fp4) || byte > high(fp4)); };
+  auto nonzero = [](const v4i& c, bool fp4) {
+    return ((c[0] | c[1] | c[2] | c[3]) & (fp4 ? 0x77777777 : 0x7F7F7F7F)) != 0;
+  };
+  auto byte_of = [&](uint32_t word) { return (word >> (8 * g)) & 255u; };
+  // Whether a lane of the wave has such a block in a run.
+  auto far = [&](const R& r) {
+    uint32_t low_a = 255, high_a = 0, low_b = 255, high_b = 0;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint32_t v = byte_of(r.sa[i][t]);
+        low_a = v < low_a ? v : low_a;
+        high_a = v > high_a ? v : high_a;
+      }
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        const uint32_t v = byte_of(r.sb[j][t]);
+        low_b = v < low_b ? v : low_b;
+        high_b = v > high_b ? v : high_b;
+      }
+    }
+    if (!__any(low_a < low(false) || high_a > high(false) || low_b < low(FP4) || high_b > high(FP4))) return false;
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        any |= outside(byte_of(r.sa[i][t]), false) &&
+               (nonzero(r.a[i][t][0], false) || nonzero(r.a[i][t][1], false));
+#pragma unroll
+      for (int j = 0; j < NF; ++j)
+        any |= outside(byte_of(r.sb[j][t]), FP4) &&
+               (nonzero(r.b[j][t][0], FP4) || nonzero(r.b[j][t][FP4 ? 0 : 1], FP4));
+    }
+    return __any(any) != 0;
+  };
+  // Such a run is left out, and taken in a second pass over K (in the first, its
+  // code costs the others registers: up to 26 spilled) block by block: the
+  // codes' products, without scales, and the sum times both scales, whose product
+  // may be ordinary where each is not.
+  auto far_products = [&](const R& r) {
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll 1
+      for (int block = 0; block < 4; ++block) {
+        const v4i zero = {0, 0, 0, 0};
+        const bool mine = g == block;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const Eight wa = widen8(mine ? r.a[i][t][0] : zero, mine ? r.a[i][t][1] : zero, 127u);
+          const int row = __shfl((int)byte_of(r.sa[i][t]), 16 * block + r16);
+#pragma unroll
+          for (int j = 0; j < NF; ++j) {
+            const v4i lo = mine ? r.b[j][t][0] : zero, hi = mine ? r.b[j][t][FP4 ? 0 : 1] : zero;
+            const Eight wb = FP4 ? widen4(lo, 127u) : widen8(lo, hi, 127u);
+            v4f sum = {0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.v[q], wa.v[q], sum, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int col = __shfl((int)byte_of(r.sb[j][t]), 16 * block + 4 * g + e);
+              const float v = __builtin_amdgcn_ldexpf(sum[e], row + col - 254);
+              acc[i][j][e] += row == 255 || col == 255 ? __builtin_nanf("") : v;
+            }
+          }
+        }
+      }
+  };
+  [[maybe_unused]] bool again = false;
   auto products = [&](const R& r) {
+    if constexpr (Exact) {
+      if (far(r)) {
+        again = true;
+        return;
+      }
+    }
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       if constexpr (Exact) {
         Eight wa[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          wa[i] = widen8(r.a[i][t][0], r.a[i][t][1], (r.sa[i][t] >> (8 * g)) & 255u);
+          wa[i] = widen8(r.a[i][t][0], r.a[i][t][1], byte_of(r.sa[i][t]));
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          const uint32_t byte = (r.sb[j][t] >> (8 * g)) & 255u;
+          const uint32_t byte = byte_of(r.sb[j][t]);
           const Eight wb = FP4 ? widen4(r.b[j][t][0], byte) : widen8(r.b[j][t][0], r.b[j][t][FP4 ? 0 : 1], byte);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
@@ -240,6 +327,15 @@ __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
     if (i + WV < runs) load(x, KR * (i + WV));
     products(y);
     i += WV;
+  }
+  if constexpr (Exact) {
+    if (again) {
+#pragma unroll 1
+      for (i = wave; i < runs; i += WV) {
+        load(x, KR * i);
+        if (far(x)) far_products(x);
+      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)

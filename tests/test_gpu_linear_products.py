@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import mxfp4_precision_gemms_amd as A
-from test_gpu_linear import BF, U, activations, check_mx8, rand, weights
+from test_gpu_linear import BF, U, activations, check_mx8, decode, decode4, linear_ref, rand, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,75 @@ def test_names():
     b, _ = weights(32, 64, "MXFP8", 221)
     with pytest.raises(KeyError):
         A.adahop_linear_mx(a, b, products="FAST")
+
+
+# ---- scales near the ends of E8M0 ---------------------------------------------
+def far_operands(m, n, K, fmt, seed):
+    """Codes and scales whose values lie near both ends of what the formats hold,
+    in blocks where the other operand's lie near the other end; ordinary blocks
+    and blocks of zeros (byte 0) between them."""
+    g = torch.Generator().manual_seed(seed)
+
+    def codes(rows):
+        c = torch.randint(0, 0x7F, (rows, K), dtype=torch.uint8, generator=g)
+        return c | torch.randint(0, 2, (rows, K), dtype=torch.uint8, generator=g) << 7
+
+    kind = torch.arange(K // 32) % 3
+
+    def scales(rows, first, second):
+        """Bytes of `first`, `second` and 120 .. 132 in turn, block by block."""
+        s = torch.randint(0, 13, (rows, K // 32), generator=g)
+        return torch.where(kind == 0, first(s), torch.where(kind == 1, second(s), 120 + s)).to(torch.uint8)
+
+    top = 252 if fmt == "MXFP4" else 254
+    ac, asc = codes(m), scales(m, lambda s: s, lambda s: 254 - s)
+    bsc = scales(n, lambda s: top - s, lambda s: s)
+    ac[0, :32], asc[0, 0] = 0, 0
+    ac[m - 1, 64:96], asc[m - 1, 2] = 0, 0
+    bc = codes(n) if fmt == "MXFP8" else torch.randint(0, 256, (n, K // 2), dtype=torch.uint8, generator=g)
+    bc[1, :32 if fmt == "MXFP8" else 16], bsc[1, 0] = 0, 0
+    return tuple(t.to("cuda:0") for t in (ac, asc)), tuple(t.to("cuda:0") for t in (bc, bsc))
+
+
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+@pytest.mark.parametrize("m,n,K", [(1, 64, 96), (5, 64, 1056), (20, 128, 544), (3, 9216, 288)])
+def test_far_scales(m, n, K, fmt):
+    """Products of values that fp32, or bf16, cannot hold are finite, and exact
+    with EXACT."""
+    a, b = far_operands(m, n, K, fmt, 230 + m)
+    va, vb = decode(*a), (decode if fmt == "MXFP8" else decode4)(*b)
+    want, tol = va @ vb.t(), (K / 4 + 16) * U * (va.abs() @ vb.abs().t())
+    got = A.adahop_linear_mx(a, b, out_dtype="MXFP8", products="EXACT")
+    check_mx8(got.out, got.scales, want, tol)
+    gated = A.adahop_linear_mx(a, b, act="RELU", gated=True, out_dtype="MXFP8", products="EXACT")
+    h = n // 2
+    f, up = want[:, :h].clamp(min=0), want[:, h:]
+    bound = tol[:, :h] * up.abs() + (f + tol[:, :h]) * tol[:, h:] + U * (f * up).abs()
+    check_mx8(gated.out, gated.scales, f * up, bound)
+    out = A.adahop_linear_mx(a, b, products="EXACT").out.cpu().double()
+    assert bool(((out - want).abs() <= tol + BF * (want.abs() + tol)).all())
+
+
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+def test_far_scales_non_finite(fmt):
+    """Among far scales, a NaN byte or code reaches its own row or column and no other."""
+    a, b = far_operands(6, 64, 288, fmt, 240)
+    a[1][2, 4] = 255
+    a[0][4, 33] = 0x7F
+    b[1][7, 3] = 255
+    out = A.adahop_linear_mx(a, b, products="EXACT").out.cpu()
+    want = torch.zeros(6, 64, dtype=torch.bool)
+    want[2] = want[4] = True
+    want[:, 7] = True
+    assert torch.equal(out.isnan(), want) and not bool(out[~want].isinf().any())
+
+
+@pytest.mark.parametrize("m,n", [(5, 64), (40, 320), (1200, 1600)])
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+def test_far_scales_of_scaled_products(m, n, fmt):
+    a, b = far_operands(m, n, 288, fmt, 250)
+    at = torch.tensor(sorted({0, 1, m // 2, m - 1}))
+    va, vb = decode(a[0].cpu()[at], a[1].cpu()[at]), (decode if fmt == "MXFP8" else decode4)(*b)
+    z, dz, out, dout = linear_ref(va, vb, None, "NONE", False, None)
+    got = A.adahop_linear_mx(a, b, products="SCALED").out.cpu()[at].double()
+    assert bool(((got - out).abs() <= dout + BF * (out.abs() + dout)).all())

@@ -7,6 +7,8 @@ import subprocess
 
 import pytest
 
+from linear_cases import FEW, TILES
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mxfp4_precision_gemms_amd", "csrc")
 
 
@@ -93,3 +95,35 @@ def test_bad_products(products, status):
                      products=products)
     assert A.lib().adahop_linear_mx_workspace_size(4096, 4096, 96, 1, 0) > 0
     assert A.lib().adahop_linear_mx(ctypes.byref(a), None, 0, None) == status
+
+
+def test_kernels_of_the_listed_sizes(tmp_path):
+    """Each size of linear_cases.py takes the kernel that it stands under, on a
+    device of 256 compute units: a constant that is set anew cannot leave a
+    kernel without a test of its values."""
+    listed = [(None, c) for c in FEW] + [(kind, c) for kind, cases in TILES for c in cases]
+    got = numbers(tmp_path, [
+        '{ const TilePlan p = linear_tile_plan(%d, %d, %d, %d, %d, 256);\n'
+        '  printf("%%d %%d %%d %%d\\n", (int)exact_products(0, %s, %d, %d),'
+        ' (int)take_few(%d, p, %d, %d, %d, %d, %s, 256), 256 >> p.shape, p.parts); }'
+        % (m, n, K, fmt == "MXFP4", gated, str(mx8).lower(), m, n, m, n, K, fmt == "MXFP4", gated, str(mx8).lower())
+        for _, (m, n, K, fmt, gated, mx8) in listed])
+    for (kind, c), (exact, few, rows, parts) in zip(listed, got):
+        assert not exact and few == (kind is None), (c, few, rows, parts)
+        if kind is not None:
+            assert (rows, min(parts, 2)) == kind, (c, rows, parts)
+
+
+def test_listed_sizes_reach_every_variant():
+    """Every kernel with both formats, plain and gated, and, of the smaller tiles,
+    with scales as they stand and in another order. (K parts of 128 rows with
+    scales in another order come with MXFP8 weights alone.)"""
+    for (rows, parts), cases in TILES:
+        have = {(c[3], c[4], rows < 256 and c[2] % 512 == 0) for c in cases}
+        for fmt in ("MXFP4", "MXFP8"):
+            for gated in (False, True):
+                for in_place in ((False, True) if rows < 256 else (False,)):
+                    if (rows, parts, fmt, in_place) != (128, 2, "MXFP4", False):
+                        assert (fmt, gated, in_place) in have, (rows, parts, fmt, gated, in_place)
+    wide = {(c[0] <= 16, c[1] <= 8192, c[4], c[5]) for c in FEW}
+    assert len(wide) == 16

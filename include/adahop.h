@@ -588,9 +588,10 @@ typedef enum {
  * not NULL, MXFP8 (out: codes, ld_out bytes; n a multiple of 32). z (bf16
  * [m, N], or NULL) keeps z for adahop_act_backward. residual is bf16 and may be
  * out itself.
- * Needs adahop_linear_mx_workspace_size(...) bytes of 16-byte aligned
- * workspace (0 for few rows, else the scales in another order and, where K is
- * split, the parts' sums); none with EXACT products.
+ * Needs up to adahop_linear_mx_workspace_size(...) bytes of 16-byte aligned
+ * workspace, whatever the output's type (0 for few rows, else the scales in
+ * another order and, where K is split, the parts' sums); none with EXACT
+ * products.
  * Errors: INVALID for NULL operands or out (m > 0), m < 0, N or K < 1, K not
  * a multiple of 32, leading dimensions too small, N odd with gated, n not a
  * multiple of 32 with an MXFP8 output, a bad format, dtype, activation or products,

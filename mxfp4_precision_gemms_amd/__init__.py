@@ -571,7 +571,7 @@ def _matrix(t: torch.Tensor, name: str, types: dict, rows: int, cols: int, devic
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: expected unit column stride")
-    return t.data_ptr(), (s0 if rows > 1 else max(s0, cols)), kind
+    return t.data_ptr(), (s0 if rows > 1 else cols), kind
 
 
 def _vector(t: torch.Tensor, name: str, types: dict, n: int, device: int):

@@ -11,11 +11,12 @@ class Standin:
     that is asked for comes to."""
 
     def __init__(self):
-        self.calls, self.size = [], 0
+        self.calls, self.args, self.size = [], {}, 0
 
     def __getattr__(self, name):
         def call(*args):
             self.calls.append(name)
+            self.args[name] = args
             return self.size if name.endswith("_size") else 0
         return call
 
@@ -106,3 +107,14 @@ def test_workspace_refusals(standin, kind, size):
     ws = OnGpu(torch.zeros(16, 4, dtype=torch.float32))          # any type, any shape
     assert A.adahop_linear_mx(a, b, out=out, ws=ws).out is out
     assert standin.launched() == ["adahop_linear_mx"]
+
+
+def test_one_row_has_no_leading_dimension(standin):
+    """A row of a matrix whose rows lie 104 bytes apart: the distance to the next
+    row, which there is none, is not held against it."""
+    a = [OnGpu(torch.zeros(3, 104, dtype=torch.uint8)[2:, :96]), OnGpu(torch.zeros(3, 7, dtype=torch.uint8)[2:, :3])]
+    b = [OnGpu(torch.zeros(s, dtype=torch.uint8)) for s in ((8, 96), (8, 3))]
+    out = OnGpu(torch.zeros(1, 8, dtype=torch.bfloat16))
+    assert A.adahop_linear_mx(a, b, out=out).out is out
+    got = standin.args["adahop_linear_mx"][0]._obj
+    assert (got.ld_a_codes, got.ld_a_scales, got.ld_b_codes) == (96, 3, 96)

@@ -90,3 +90,13 @@ def test_linear_workspace(m, n, K, fmt, gated, mx8):
     exact = A.adahop_linear_mx(a, b, ws=ws[:0], products="EXACT", **more)
     again = A.adahop_linear_mx(a, b, products="EXACT", **more)
     assert torch.equal(exact.out, again.out)
+
+
+def test_one_row_of_strided_operands():
+    """Rows 104 bytes apart, of which only the third starts at 16 bytes."""
+    a, _ = activations(3, 96, 11)
+    b, _ = weights(64, 96, "MXFP4", 12)
+    codes, scales = strided(a[0].cpu(), 8), strided(a[1].cpu(), 4)
+    assert codes.stride(0) == 104
+    got = A.adahop_linear_mx((codes[2:], scales[2:]), b).out
+    assert torch.equal(got, A.adahop_linear_mx((a[0][2:], a[1][2:]), b).out)

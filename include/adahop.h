@@ -620,6 +620,9 @@ typedef struct {
 
 ADAHOP_API size_t adahop_linear_mx_workspace_size(int64_t m, int64_t N, int64_t K,
                                                   adahop_mx_format b_format, int32_t gated);
+/* What one call needs of it: 0 where its output's type and products need none
+ * (and for arguments that adahop_linear_mx refuses). */
+ADAHOP_API size_t adahop_linear_mx_args_workspace_size(const adahop_linear_args* args);
 ADAHOP_API adahop_status adahop_linear_mx(const adahop_linear_args* args, void* ws,
                                           size_t ws_bytes, void* stream);
 

@@ -136,6 +136,7 @@ SIGNATURES = {
     "adahop_rmsnorm_backward_workspace_size": ([_i64, _i64], _sz),
     "adahop_rmsnorm_backward": ([ctypes.POINTER(RmsnormBackwardArgs), _p, _sz, _p], _int),
     "adahop_linear_mx_workspace_size": ([_i64, _i64, _i64, _int, _i32], _sz),
+    "adahop_linear_mx_args_workspace_size": ([ctypes.POINTER(LinearArgs)], _sz),
     "adahop_linear_mx": ([ctypes.POINTER(LinearArgs), _p, _sz, _p], _int),
     "adahop_act_backward_workspace_size": ([_i64, _i64, _i32], _sz),
     "adahop_act_backward": ([_p, _int, _i64, _p, _i64, _i64, _i64, _int, _i32, _p, _i64, _p, _p,
@@ -770,8 +771,9 @@ def adahop_linear_mx(a: Tuple[torch.Tensor, torch.Tensor], b: Tuple[torch.Tensor
         zp = z.data_ptr()
     g = LinearArgs(m, N, K, ap, lda, asp, ldas, bp, ldb, bsp, ldbs, biasp, rp, ldr, op, ldo, sp, lds, zp, N,
                    fmt, bk, ACT[act], 1 if gated else 0, PRODUCTS[products])
-    wp, wn, ws = _scratch(lib().adahop_linear_mx_workspace_size(m, N, K, fmt, g.gated), ws, dev)
-    _check(lib().adahop_linear_mx(ctypes.byref(g), wp, wn, _stream(dev)))
+    args = ctypes.byref(g)
+    wp, wn, ws = _scratch(lib().adahop_linear_mx_args_workspace_size(args), ws, dev)
+    _check(lib().adahop_linear_mx(args, wp, wn, _stream(dev)))
     return LinearOut(out, scales, z)
 
 

@@ -129,6 +129,14 @@ bool valid_product(int64_t m, int64_t N, int64_t K) {
   return m >= 0 && N >= 1 && K >= 1 && K % 32 == 0 && m < kMaxDim && N <= kMaxLinearN && K < kMaxDim;
 }
 
+// Workspace of a call whose sizes, format and products are valid.
+size_t linear_bytes(const adahop_linear_args& a) {
+  const int64_t n = a.gated ? a.N / 2 : a.N;
+  const bool mx8_out = a.out_scales != nullptr;
+  if (a.m == 0 || exact_products(a.products, mx8_out, a.m, n)) return 0;
+  return linear_mx_scratch_bytes(a.m, n, a.K, a.b_format == ADAHOP_MX_E2M1, a.gated, mx8_out);
+}
+
 adahop_status linear(const adahop_linear_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (a == nullptr) return invalid("linear_mx: null arguments");
   if (a->m < 0 || a->N < 1 || a->K < 1) return invalid("linear_mx: m must be >= 0, N and K >= 1");
@@ -164,15 +172,13 @@ adahop_status linear(const adahop_linear_args* a, void* ws, size_t ws_bytes, hip
     return unsupported("linear_mx: codes of A and B must be 16-byte aligned, rows included");
   if (a->ld_b_codes >= kMaxRowBytes || a->ld_b_scales >= kMaxRowBytes)
     return unsupported("linear_mx: rows of B 32 MB or more apart");
-  const bool mx8_out = a->out_scales != nullptr, exact = exact_products(a->products, mx8_out, a->m, n);
-  if (!exact)
-    ADAHOP_TRY(need_workspace(ws, ws_bytes, linear_mx_scratch_bytes(a->m, n, a->K, fp4, a->gated, mx8_out),
-                              "linear_mx"));
+  ADAHOP_TRY(need_workspace(ws, ws_bytes, linear_bytes(*a), "linear_mx"));
   const LinearArgs g = {a->a_codes, a->a_scales, a->b_codes, a->b_scales, a->ld_a_codes,
                         a->ld_a_scales, a->ld_b_codes, a->ld_b_scales, a->m, n, a->K, a->bias,
                         a->bias_dtype, a->act, a->residual, a->ld_residual, a->out, a->ld_out,
                         a->out_scales, a->ld_out_scales, a->z, a->ld_z};
-  return linear_mx_launch(g, fp4, a->gated, exact, ws, stream);
+  return linear_mx_launch(g, fp4, a->gated, exact_products(a->products, a->out_scales != nullptr, a->m, n), ws,
+                          stream);
 }
 
 size_t act_back_bytes(int64_t m, int64_t N, int32_t gated) {
@@ -247,6 +253,11 @@ size_t adahop_linear_mx_workspace_size(int64_t m, int64_t N, int64_t K, adahop_m
   const size_t bf16 = linear_mx_scratch_bytes(m, n, K, b_format == ADAHOP_MX_E2M1, gated, false);
   const size_t mx8 = linear_mx_scratch_bytes(m, n, K, b_format == ADAHOP_MX_E2M1, gated, true);
   return bf16 > mx8 ? bf16 : mx8;
+}
+
+size_t adahop_linear_mx_args_workspace_size(const adahop_linear_args* args) {
+  if (args == nullptr || !valid_product(args->m, args->N, args->K) || (args->gated && args->N % 2 != 0)) return 0;
+  return linear_bytes(*args);
 }
 
 adahop_status adahop_linear_mx(const adahop_linear_args* args, void* ws, size_t ws_bytes,

@@ -127,3 +127,30 @@ def test_listed_sizes_reach_every_variant():
                         assert (fmt, gated, in_place) in have, (rows, parts, fmt, gated, in_place)
     wide = {(c[0] <= 16, c[1] <= 8192, c[4], c[5]) for c in FEW}
     assert len(wide) == 16
+
+
+def test_workspace_of_a_call():
+    """The size that is asked for without a call's arguments is that of the type
+    of output which needs more; a call's own is 0 where it needs none."""
+    import ctypes
+
+    import mxfp4_precision_gemms_amd as A
+    lib = A.lib()
+
+    def own(m, N, K, fmt, gated=0, mx8=False, products=0):
+        a = A.LinearArgs(m=m, N=N, K=K, b_format=fmt, gated=gated, products=products, out_scales=4096 if mx8 else None)
+        return lib.adahop_linear_mx_args_workspace_size(ctypes.byref(a))
+
+    for c in FEW + [c for _, cases in TILES for c in cases]:
+        m, n, K, fmt, gated, mx8 = c
+        f, N = int(fmt == "MXFP8"), 2 * n if gated else n
+        both = [own(m, N, K, f, int(gated), t) for t in (False, True)]
+        # (an MXFP8 output of few values is exact, and needs none)
+        asked = lib.adahop_linear_mx_workspace_size(m, N, K, f, int(gated))
+        assert both[mx8] in (0, asked) and (both[mx8] == 0) == (c in FEW)
+        assert max(both) <= asked
+        assert own(m, N, K, f, int(gated), mx8, products=2) == 0
+    assert own(0, 64, 96, 1) == 0 and own(-1, 64, 96, 1) == 0 and own(4, 64, 80, 1) == 0 and own(4, 63, 96, 1, 1) == 0
+    assert lib.adahop_linear_mx_args_workspace_size(None) == 0
+    # bf16 from few rows of a layer whose MXFP8 output would take tiles
+    assert lib.adahop_linear_mx_workspace_size(31, 3520, 1536, 1, 1) > 0 and own(31, 3520, 1536, 1, 1) == 0

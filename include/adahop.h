@@ -503,8 +503,9 @@ ADAHOP_API adahop_status adahop_mx8_dequant(const uint8_t* codes, int64_t ld_cod
  * the stream): h = x + r rounded to r's type, written to h (which may be r
  * itself); without (residual NULL): h = x, nothing is written. Then
  *   rstd = 1 / sqrt(mean_j h_j^2 + eps),   y_j = h_j * rstd * gain_j,
- * sums in fp32. y goes to codes and scales (MXFP8) and / or to y (bf16); at
- * least one is required. rstd (fp32 [rows]) may be NULL.
+ * sums in fp32 (a row whose squares overflow it, from about 1.8e19 on, gets
+ * rstd 0). y goes to codes and scales (MXFP8) and / or to y (bf16); at least
+ * one is required. rstd (fp32 [rows]) may be NULL.
  * Errors: INVALID for missing pointers, cols < 1, rows < 0, leading dimensions
  * too small, a bad dtype, cols % 32 != 0 with an MXFP8 output, eps negative or
  * not finite, reserved not 0; UNSUPPORTED for cols > 32768 or more than
@@ -567,8 +568,8 @@ typedef enum {
  * lies under 2^-13 of the largest: within about 5e-5 of the result, root mean
  * square, on operands with outlier columns; a bf16 output's rounding hides
  * that, in an MXFP8 output it moves about one code in a thousand to its
- * neighbour. Both sum in fp32. EXACT reads B again for every 32 rows, SCALED
- * takes tiles. AUTO: EXACT for MXFP8 outputs of up to 32768 values (m * n),
+ * neighbour. Both sum in fp32. EXACT reads B again for every 32 rows, so it is
+ * for few rows above all; SCALED takes tiles. AUTO: EXACT for MXFP8 outputs of up to 32768 values (m * n),
  * SCALED for larger ones and for bf16. */
 typedef enum {
   ADAHOP_PRODUCTS_AUTO = 0,

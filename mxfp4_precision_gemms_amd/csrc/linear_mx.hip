@@ -38,7 +38,8 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 // loads issued before a run's products; their sums meet in LDS, added in wave
 // order. B is read once, by the workgroup that owns its rows: bound by HBM,
 // and by what a compute unit loads of A and B (about 28 GB/s): 1 x 4096 x
-// 14336, E2M1 weights 9.8 us (3.1 TB/s), E4M3 15.5 us (3.9 TB/s).
+// 14336, E2M1 weights 10.6 us (2.9 TB/s; 9.4 from the last-level cache), E4M3
+// 15.7 us (3.9 TB/s).
 template <bool FP4, int MT, int NF, int T>
 struct Run {
   v4i a[MT][T][2];
@@ -53,9 +54,9 @@ constexpr int kPastEnd = 0x7FFFFFF0;       // an offset past the end of every bu
 // values are exact (near the ends of E8M0's range without their scales), instead
 // of the scaled ones, so that an MXFP8 output, where one code rounded the other
 // way shows, is that of exact sums. A lane's 32 elements of 128 are one block,
-// 32 g .. + 31, of both operands. (1 x 2048 x 4096, E2M1: 6.8 us, scaled and in
-// bf16 5.0; 1 x 14336 x 4096: 11.9 and 10.8; 1.6 % of it, on average, looks for
-// far scales.)
+// 32 g .. + 31, of both operands. (1 x 2048 x 4096, E2M1: 6.8 us, scaled 6.0, in
+// bf16 5.1; 1 x 14336 x 4096: 11.8, 11.1 and 10.8; 1.6 % of it, on average, looks
+// for far scales.)
 template <bool FP4, bool Gated, bool Exact, int MT, int NB, int WV, int T>
 __global__ void __launch_bounds__(64 * WV, 1) linear_few_kernel(LinearArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__                        // the host pass needs the launch stub alone

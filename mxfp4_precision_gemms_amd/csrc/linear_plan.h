@@ -16,10 +16,11 @@ constexpr int64_t kMaxLinearN = (int64_t{1} << 30) - 64;
 // by the output alone, so that a caller can tell, and a device's or an
 // estimate's change moves no result. Up to 32768 MXFP8 values come mostly from
 // few rows, where loads bind and exact products cost little (microseconds exact
-// and scaled: 1 x 4096 x 14336, E2M1 15.5 and 13.8, 1 x 14336 gated x 4096 20.5
-// and 18.0, 8 x 4096 x 4096, E4M3 10.2 and 9.6); the most where few columns
-// meet a long K (32 x 960 x 14336: 26 and 10.5). Above, tiles are faster by up
-// to two times at 32 rows (14336 gated x 4096, E4M3: 47 and 29), four at 100.
+// and scaled: 1 x 4096 x 14336, E2M1 16.0 and 13.7, 1 x 14336 gated x 4096 20.7
+// and 16.9, 8 x 4096 x 4096, E4M3 10.4 and 9.6); the most where few columns
+// meet a long K (32 x 960 x 14336: 26.0 and 10.4). Above, tiles are faster by
+// 1.6 times at 32 rows and 4 at 100 (14336 gated x 4096, E4M3: 45 and 28, 130
+// and 33), 11 at 4096 rows (4096 x 4096, E4M3: 733 and 65).
 constexpr bool exact_products(int products, bool mx8_out, int64_t m, int64_t n) {
   return products == 2 || (products == 0 && mx8_out && m * n <= 32768);
 }
@@ -41,7 +42,7 @@ struct TilePlan {
 // 1.45 and 1.55 with 4 for ordering the scales; K parts 3 for the second
 // kernel and their sums written and read at 4 TB/s. On 36 cases (m = 40 ..
 // 3000, six weights) the choice was within 6 % of the fastest of all shapes
-// with 1, 2, 4 and 8 parts on 34, at worst 16 % off.
+// and parts on 33, at worst 16 % off.
 inline TilePlan linear_tile_plan(int64_t m, int64_t n, int64_t K, int b_fp4, int gated, int64_t cus) {
   const int64_t N = gated ? 2 * n : n, nk = (K + 127) / 128;
   TilePlan best{};
@@ -77,7 +78,7 @@ inline TilePlan linear_tile_plan(int64_t m, int64_t n, int64_t K, int b_fp4, int
 // compute unit (1 x 4096 x 14336, E2M1: 10.6 us, with 32 columns and 4 waves
 // 17.1), else 32 columns and 4 waves, which read A half as often (16 x 14336
 // gated x 4096: 21.0, with 16 columns 23.9). An MXFP8 block needs 32 (1 x 4096 x
-// 14336, exact: 15.7).
+// 14336: 13.7, exact 16.0).
 constexpr bool few_narrow(int64_t n) { return n <= 16 * 512; }
 // Output columns of a launch of more than those: with 256 threads for 32
 // columns, 2^31 threads. (A gated layer's go at once.)
@@ -91,7 +92,7 @@ static_assert(few_wide_threads(kFewLaunchCols) < int64_t{1} << 32 &&
 // every 32 rows) at 28 KB / us with 8 waves (24 where workgroups of 32 columns
 // share one) and 20 with 4. On 162 cases of each type (m = 1 .. 100, nine
 // weights in both formats) the choice against the tiles was within 6 % of the
-// faster on 153 (MXFP8 out) and 158 (bf16), at worst 23 % and 26 % off.
+// faster on 154 (MXFP8 out) and 158 (bf16), at worst 24 % and 27 % off.
 inline double few_us(int64_t m, int64_t n, int64_t K, int b_fp4, int gated, bool mx8_out, int64_t cus) {
   const double kb = (double)K / 1024, b = b_fp4 ? 17.0 / 32 : 33.0 / 32, a = 33.0 / 32;
   const int cols = few_narrow(n) && !mx8_out ? 16 : 32;

@@ -408,7 +408,7 @@ adahop_status rmsnorm_launch(const void* x, int x_f32, const void* r, int r_f32,
 
 int rmsnorm_backward_groups(int64_t rows, int64_t cols) {
   // 4096 waves, 16 a compute unit; each workgroup leaves one row of partial
-  // sums (8 MB in all).
+  // sums (8 MB in all up to 8192 columns, 32 MB at 32768).
   const int waves = norm_back_waves(cols);
   const int64_t need = waves == 1 ? (rows + 3) / 4 : rows, most = waves == 1 ? 1024 : 4096 / waves;
   return (int)(need < 1 ? 1 : need < most ? need : most);

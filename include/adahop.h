@@ -597,9 +597,9 @@ typedef enum {
  * a multiple of 32, leading dimensions too small, N odd with gated, n not a
  * multiple of 32 with an MXFP8 output, a bad format, dtype, activation or products,
  * reserved not 0; UNSUPPORTED for codes of A or B that are not 16-byte
- * aligned or whose leading dimension is not a multiple of 16, for m or K of
- * 2^30 and more, N above 2^30 - 64, and for leading dimensions of B's codes or
- * scales of 2^25 bytes and more; WORKSPACE. */
+ * aligned or whose leading dimension is not a multiple of 16, for m, N or K of
+ * 2^30 and more, a gated layer's N above 2^30 - 64, and for leading dimensions
+ * of B's codes or scales of 2^25 bytes and more; WORKSPACE. */
 typedef struct {
   int64_t m, N, K;
   const uint8_t* a_codes; int64_t ld_a_codes;

@@ -374,7 +374,7 @@ void few_start(const LinearArgs& a, hipStream_t stream) {
          dim3(64 * WV), 0, stream>>>(a);
 }
 
-// 32 columns a workgroup: 8 waves by the same rule (1 x 2048 x 4096, E2M1,
+// 32 columns a workgroup: 8 waves by few_narrow too (1 x 2048 x 4096, E2M1,
 // exact: 6.6 us, with 4 waves 7.7; 1 x 14336 x 4096: 13.3, with 4 waves 11.7);
 // gated, whose registers do not last for 8, 4.
 template <bool FP4, bool Gated, bool Exact>

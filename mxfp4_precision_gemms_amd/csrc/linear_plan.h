@@ -8,9 +8,9 @@
 
 namespace adahop {
 
-// Rows of B (less than 2^30, and so few that a gated layer's output columns
-// make less than 2^24 groups of 32).
-constexpr int64_t kMaxLinearN = (int64_t{1} << 30) - 64;
+// Rows of a gated layer's B: its output columns make less than 2^24 groups of 32,
+// whose launch it takes at once.
+constexpr int64_t kMaxGatedN = (int64_t{1} << 30) - 64;
 
 // Whether the products are formed exactly (products: adahop_products). AUTO goes
 // by the output alone, so that a caller can tell, and a device's or an
@@ -85,7 +85,7 @@ constexpr bool few_narrow(int64_t n) { return n <= 16 * 512; }
 constexpr int64_t kFewLaunchCols = int64_t{1} << 28;
 constexpr int64_t few_wide_threads(int64_t n) { return (n + 31) / 32 * 256; }
 static_assert(few_wide_threads(kFewLaunchCols) < int64_t{1} << 32 &&
-              few_wide_threads(kMaxLinearN / 2) < int64_t{1} << 32, "");
+              few_wide_threads(kMaxGatedN / 2) < int64_t{1} << 32, "");
 
 // Estimate in microseconds, as linear_tile_plan's, for scaled products: a launch
 // 3.5, all of B at 5 TB/s, and what a compute unit reads of A and B (again for

@@ -125,8 +125,9 @@ adahop_status norm_back(const adahop_rmsnorm_backward_args* a, void* ws, size_t 
                                  a->dx, a->dgain, static_cast<float*>(ws), stream);
 }
 
-bool valid_product(int64_t m, int64_t N, int64_t K) {
-  return m >= 0 && N >= 1 && K >= 1 && K % 32 == 0 && m < kMaxDim && N <= kMaxLinearN && K < kMaxDim;
+bool valid_product(int64_t m, int64_t N, int64_t K, int32_t gated) {
+  return m >= 0 && N >= 1 && K >= 1 && K % 32 == 0 && m < kMaxDim && K < kMaxDim &&
+         (gated ? N <= kMaxGatedN : N < kMaxDim);
 }
 
 // Workspace of a call whose sizes, format and products are valid.
@@ -141,7 +142,8 @@ adahop_status linear(const adahop_linear_args* a, void* ws, size_t ws_bytes, hip
   if (a == nullptr) return invalid("linear_mx: null arguments");
   if (a->m < 0 || a->N < 1 || a->K < 1) return invalid("linear_mx: m must be >= 0, N and K >= 1");
   if (a->K % 32 != 0) return invalid("linear_mx: K is not a multiple of 32");
-  if (!valid_product(a->m, a->N, a->K)) return unsupported("linear_mx: m or K of 2^30 or more, or N above 2^30 - 64");
+  if (!valid_product(a->m, a->N, a->K, a->gated))
+    return unsupported("linear_mx: m, N or K of 2^30 or more, or a gated layer's N above 2^30 - 64");
   if (!all_zero(a->reserved)) return invalid("linear_mx: reserved fields must be 0");
   if (a->b_format != ADAHOP_MX_E2M1 && a->b_format != ADAHOP_MX_E4M3)
     return invalid("linear_mx: bad b_format");
@@ -247,7 +249,7 @@ adahop_status adahop_rmsnorm_backward(const adahop_rmsnorm_backward_args* args, 
 
 size_t adahop_linear_mx_workspace_size(int64_t m, int64_t N, int64_t K, adahop_mx_format b_format,
                                        int32_t gated) {
-  if (!valid_product(m, N, K) || (gated && N % 2 != 0)) return 0;
+  if (!valid_product(m, N, K, gated) || (gated && N % 2 != 0)) return 0;
   // Of the two types of output, the one that needs more.
   const int64_t n = gated ? N / 2 : N;
   const size_t bf16 = linear_mx_scratch_bytes(m, n, K, b_format == ADAHOP_MX_E2M1, gated, false);
@@ -256,7 +258,8 @@ size_t adahop_linear_mx_workspace_size(int64_t m, int64_t N, int64_t K, adahop_m
 }
 
 size_t adahop_linear_mx_args_workspace_size(const adahop_linear_args* args) {
-  if (args == nullptr || !valid_product(args->m, args->N, args->K) || (args->gated && args->N % 2 != 0)) return 0;
+  if (args == nullptr || !valid_product(args->m, args->N, args->K, args->gated)) return 0;
+  if (args->gated && args->N % 2 != 0) return 0;
   return linear_bytes(*args);
 }
 

@@ -18,8 +18,8 @@ def evaluate(tmp_path, lines):
     if cxx is None:
         pytest.skip("no C++ compiler")
     src, exe = tmp_path / "shapes.cpp", tmp_path / "shapes"
-    src.write_text('#include <cstdio>\n#include <initializer_list>\n#include "launch_shapes.h"\n#include "linear_plan.h"\nusing namespace adahop;\nint main() {\n'
-                   + "\n".join(lines) + "\n}\n")
+    head = [f"#include {h}" for h in ("<cstdio>", "<initializer_list>", '"launch_shapes.h"', '"linear_plan.h"')]
+    src.write_text("\n".join([*head, "using namespace adahop;", "int main() {", *lines, "}", ""]))
     subprocess.run([cxx, "-std=c++17", "-Wall", "-Werror", "-I" + CSRC, str(src), "-o", str(exe)], check=True)
     return subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")[:-1]
 
@@ -55,20 +55,21 @@ def test_few_row_launches(tmp_path):
     at once."""
     (plain, gated, cols, most), = numbers(tmp_path, [
         'printf("%lld %lld %lld %lld\\n", (long long)few_wide_threads(kFewLaunchCols),',
-        '(long long)few_wide_threads(kMaxLinearN / 2), (long long)kFewLaunchCols, (long long)kMaxLinearN);'])
+        '(long long)few_wide_threads(kMaxGatedN / 2), (long long)kFewLaunchCols, (long long)kMaxGatedN);'])
     assert plain < 2 ** 32 and gated < 2 ** 32
     assert cols % 32 == 0 and most < 2 ** 30
     assert plain >= 8 * cols and gated >= 4 * most
 
 
-@pytest.mark.parametrize("N,status", [((1 << 30) - 64, 1), ((1 << 30) - 63, 2), ((1 << 30) - 1, 2)])
-def test_widest_layer(N, status):
+@pytest.mark.parametrize("N,gated,status", [((1 << 30) - 1, 0, 1), (1 << 30, 0, 2), ((1 << 30) - 64, 1, 1),
+                                            ((1 << 30) - 62, 1, 2), ((1 << 30) - 2, 1, 2)])
+def test_widest_layer(N, gated, status):
     """(INVALID for ld_out, which is looked at later, and UNSUPPORTED)"""
     import ctypes
 
     import mxfp4_precision_gemms_amd as A
     a = A.LinearArgs(m=4, N=N, K=96, a_codes=4096, ld_a_codes=96, a_scales=4096, ld_a_scales=3, b_codes=4096,
-                     ld_b_codes=96, b_scales=4096, ld_b_scales=3, out=4096, ld_out=64, b_format=1)
+                     ld_b_codes=96, b_scales=4096, ld_b_scales=3, out=4096, ld_out=64, b_format=1, gated=gated)
     assert A.lib().adahop_linear_mx(ctypes.byref(a), None, 0, None) == status
 
 

@@ -646,6 +646,78 @@ ADAHOP_API adahop_status adahop_act_backward(const void* dout, adahop_out_dtype 
                                              uint16_t* dz, int64_t ld_dz, float* dbias, void* ws,
                                              size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Softmax cross entropy over a vocabulary, from hidden states h [T, D] and the
+ * output layer's weights w [V, D], without keeping the logits:
+ *   z = scale * h * w^T                                      [T, V]
+ *   lse_t = log(sum_v exp(z_tv)),   loss_t = lse_t - z_t,y(t)
+ * A target outside 0 .. V - 1 leaves its row out: loss 0; its lse is written.
+ * Products of bf16 values are exact, sums, exponentials and logits fp32.
+ * Infinities and NaNs propagate (a row of -inf has lse -inf).
+ * Needs adahop_xent_workspace_size(rows, vocab) bytes of 16-byte aligned
+ * workspace (32 bytes a row for every 256 entries of the vocabulary).
+ * Errors: INVALID for rows < 0, vocab or dim < 1, NULL h, w, targets, loss or
+ * lse (rows > 0), leading dimensions below dim, a bad target_dtype, a scale that
+ * is not finite, reserved not 0; UNSUPPORTED for dim or a leading dimension of
+ * h or w that is not a multiple of 8, h or w not 16-byte aligned, rows 8 MB or
+ * more apart, rows or vocab of 2^30 and more, or rows * vocab of 2^46 and
+ * more; WORKSPACE. */
+typedef enum { ADAHOP_INDEX_I32 = 0, ADAHOP_INDEX_I64 = 1 } adahop_index_dtype;
+
+typedef struct {
+  int64_t rows, vocab, dim;                      /* T, V, D */
+  const uint16_t* h; int64_t ld_h;               /* bf16 [T, D] */
+  const uint16_t* w; int64_t ld_w;               /* bf16 [V, D] */
+  const void* targets;                           /* [T] */
+  float* loss;                                   /* [T] */
+  float* lse;                                    /* [T] */
+  float scale;
+  int32_t target_dtype;                          /* adahop_index_dtype */
+  int32_t reserved[4];
+} adahop_xent_args;
+
+ADAHOP_API size_t adahop_xent_workspace_size(int64_t rows, int64_t vocab);
+ADAHOP_API adahop_status adahop_xent(const adahop_xent_args* args, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* Its gradient, from dloss (fp32 [T], the gradient of each row's loss) and, if
+ * not NULL, dlse (fp32 [T], that of each row's lse, as a penalty on the
+ * normalizer gives it), with the lse that adahop_xent returned:
+ *   g_tv = scale * ((dloss_t + dlse_t) * exp(z_tv - lse_t) - dloss_t * [v = y(t)])
+ *   dh = g * w   [T, D],      dw = g^T * h   [V, D]
+ * dloss of a row that is left out does not count; its dlse does. dh and dw are
+ * bf16 or fp32; either may be NULL. The logits are formed again, `piece` entries
+ * of the vocabulary at a time (0: as many as keep g within 1 GiB; rounded up to a
+ * multiple of 256, at most 2^21); g of a piece is held in bf16, sums are fp32,
+ * dh and dw are rounded once. Needs
+ * adahop_xent_backward_args_workspace_size(args) bytes of 16-byte aligned
+ * workspace (0 for arguments that the call refuses): 2 * rows * piece for g, dh
+ * in fp32 where there are several pieces, and the parts of products split over
+ * their sums.
+ * Errors: as adahop_xent, and INVALID for NULL lse or dloss (rows > 0), dh and dw
+ * both NULL (rows > 0), ld_dh or ld_dw below dim, a bad dtype, piece < 0; UNSUPPORTED for
+ * rows * dim of 2^46 and more. */
+typedef struct {
+  int64_t rows, vocab, dim;
+  const uint16_t* h; int64_t ld_h;
+  const uint16_t* w; int64_t ld_w;
+  const void* targets;
+  const float* lse;
+  const float* dloss;
+  const float* dlse;                             /* NULL: none */
+  void* dh; int64_t ld_dh;                       /* NULL: not wanted */
+  void* dw; int64_t ld_dw;
+  int64_t piece;
+  float scale;
+  int32_t target_dtype;
+  int32_t dh_dtype, dw_dtype;                    /* adahop_out_dtype */
+  int32_t reserved[4];
+} adahop_xent_backward_args;
+
+ADAHOP_API size_t adahop_xent_backward_args_workspace_size(const adahop_xent_backward_args* args);
+ADAHOP_API adahop_status adahop_xent_backward(const adahop_xent_backward_args* args, void* ws,
+                                              size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

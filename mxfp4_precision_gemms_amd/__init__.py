@@ -96,6 +96,20 @@ class LinearArgs(ctypes.Structure):
                 ("gated", _i32), ("products", _i32), ("reserved", _i32 * 3)]
 
 
+class XentArgs(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("vocab", _i64), ("dim", _i64), ("h", _p), ("ld_h", _i64),
+                ("w", _p), ("ld_w", _i64), ("targets", _p), ("loss", _p), ("lse", _p),
+                ("scale", ctypes.c_float), ("target_dtype", _i32), ("reserved", _i32 * 4)]
+
+
+class XentBackwardArgs(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("vocab", _i64), ("dim", _i64), ("h", _p), ("ld_h", _i64),
+                ("w", _p), ("ld_w", _i64), ("targets", _p), ("lse", _p), ("dloss", _p), ("dlse", _p),
+                ("dh", _p), ("ld_dh", _i64), ("dw", _p), ("ld_dw", _i64), ("piece", _i64),
+                ("scale", ctypes.c_float), ("target_dtype", _i32), ("dh_dtype", _i32),
+                ("dw_dtype", _i32), ("reserved", _i32 * 4)]
+
+
 # Exported symbols and their C signatures (argtypes, restype).
 SIGNATURES = {
     "adahop_status_string": ([_int], ctypes.c_char_p),
@@ -141,6 +155,10 @@ SIGNATURES = {
     "adahop_act_backward_workspace_size": ([_i64, _i64, _i32], _sz),
     "adahop_act_backward": ([_p, _int, _i64, _p, _i64, _i64, _i64, _int, _i32, _p, _i64, _p, _p,
                              _sz, _p], _int),
+    "adahop_xent_workspace_size": ([_i64, _i64], _sz),
+    "adahop_xent": ([ctypes.POINTER(XentArgs), _p, _sz, _p], _int),
+    "adahop_xent_backward_args_workspace_size": ([ctypes.POINTER(XentBackwardArgs)], _sz),
+    "adahop_xent_backward": ([ctypes.POINTER(XentBackwardArgs), _p, _sz, _p], _int),
 }
 
 _lib = None
@@ -798,3 +816,67 @@ def adahop_act_backward(dout: torch.Tensor, z: torch.Tensor, act: str = "NONE", 
     _check(lib().adahop_act_backward(gp, gk, ldg, zp, ldz, m, N, ACT[act], int(gated), op, ldo, bp, wp,
                                      wn, _stream(dev)))
     return dz, dbias
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy over a vocabulary
+# ---------------------------------------------------------------------------
+_INDEX = {torch.int32: 0, torch.int64: 1}
+_F32 = {torch.float32: 1}
+
+
+class XentOut(NamedTuple):
+    loss: torch.Tensor               # fp32 [T]
+    lse: torch.Tensor                # fp32 [T]: log of the sum of the logits' exponentials
+
+
+def adahop_xent(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, scale: float = 1.0,
+                ws: Optional[torch.Tensor] = None) -> XentOut:
+    """Softmax cross entropy of the logits scale * h w^T, which are not kept:
+    h [T, D] and w [V, D] in bf16, targets [T] in int64 or int32 (one outside
+    0 .. V - 1 leaves its row out: loss 0)."""
+    T, D = _size(h, "h")
+    V, _ = _size(w, "w")
+    dev, d = h.device, h.get_device()
+    hp, ldh, _ = _matrix(h, "h", _BF16, T, D, d)
+    wp, ldw, _ = _matrix(w, "w", _BF16, V, D, d)
+    tp, tk = _vector(targets, "targets", _INDEX, T, d)
+    loss, lse = torch.empty((2, T), dtype=torch.float32, device=dev)
+    a = XentArgs(T, V, D, hp, ldh, wp, ldw, tp, loss.data_ptr(), lse.data_ptr(), scale, tk)
+    wsp, wn, ws = _scratch(lib().adahop_xent_workspace_size(T, V), ws, dev)
+    _check(lib().adahop_xent(ctypes.byref(a), wsp, wn, _stream(dev)))
+    return XentOut(loss, lse)
+
+
+def adahop_xent_backward(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                         dloss: torch.Tensor, dlse: Optional[torch.Tensor] = None, scale: float = 1.0,
+                         h_grad: bool = True, w_grad: bool = True, dh_dtype=torch.bfloat16,
+                         dw_dtype=torch.bfloat16, dh: Optional[torch.Tensor] = None,
+                         dw: Optional[torch.Tensor] = None, piece: int = 0,
+                         ws: Optional[torch.Tensor] = None):
+    """(dh [T, D], dw [V, D]), None where not asked for, from the gradients of
+    each row's loss and, if given, lse (fp32 [T]). The logits are formed again,
+    `piece` entries of the vocabulary at a time (0: chosen). dh and dw may be
+    given (bf16 or fp32), else they have dh_dtype and dw_dtype."""
+    T, D = _size(h, "h")
+    V, _ = _size(w, "w")
+    dev, d = h.device, h.get_device()
+    hp, ldh, _ = _matrix(h, "h", _BF16, T, D, d)
+    wp, ldw, _ = _matrix(w, "w", _BF16, V, D, d)
+    tp, tk = _vector(targets, "targets", _INDEX, T, d)
+    lp, _ = _vector(lse, "lse", _F32, T, d)
+    gp, _ = _vector(dloss, "dloss", _F32, T, d)
+    ep = None if dlse is None else _vector(dlse, "dlse", _F32, T, d)[0]
+    a = XentBackwardArgs(T, V, D, hp, ldh, wp, ldw, tp, lp, gp, ep, None, D, None, D, piece, scale, tk)
+    if h_grad:
+        if dh is None:
+            dh = torch.empty((T, D), dtype=dh_dtype, device=dev)
+        a.dh, a.ld_dh, a.dh_dtype = _matrix(dh, "dh", _FLOAT, T, D, d)
+    if w_grad:
+        if dw is None:
+            dw = torch.empty((V, D), dtype=dw_dtype, device=dev)
+        a.dw, a.ld_dw, a.dw_dtype = _matrix(dw, "dw", _FLOAT, V, D, d)
+    args = ctypes.byref(a)
+    wsp, wn, ws = _scratch(lib().adahop_xent_backward_args_workspace_size(args), ws, dev)
+    _check(lib().adahop_xent_backward(args, wsp, wn, _stream(dev)))
+    return dh if h_grad else None, dw if w_grad else None

@@ -244,4 +244,39 @@ size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int g
 adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, bool exact, void* scratch,
                                hipStream_t stream);
 
+// ---- cross entropy over a vocabulary ----------------------------------------
+// Arguments as the public entry points', already checked; T > 0 in xent_launch.
+struct XentArgs {
+  int64_t T, V, D;
+  const uint16_t* h;
+  int64_t ldh;
+  const uint16_t* w;
+  int64_t ldw;
+  const void* targets;
+  int wide_targets;          // int64, else int32
+  float scale;
+};
+struct XentGrad {
+  const float* lse;
+  const float* dloss;
+  const float* dlse;         // or null
+  void* dh;                  // or null
+  int64_t lddh;
+  int dh_f32;
+  void* dw;                  // or null
+  int64_t lddw;
+  int dw_f32;
+};
+// Pieces of the vocabulary in the backward pass: their columns (0: chosen), a
+// multiple of 256, and how many there are.
+struct XentPieces {
+  int64_t size, count;
+};
+XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece);
+size_t xent_ws_bytes(int64_t T, int64_t V);
+adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t stream);
+size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, bool dw);
+adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t piece, void* ws,
+                                   hipStream_t stream);
+
 }  // namespace adahop

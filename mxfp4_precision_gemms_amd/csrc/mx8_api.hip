@@ -1,5 +1,5 @@
-// Host side of the norm, MXFP8 and linear-layer entry points: argument checks
-// and launches. Every check runs before the first launch; nothing allocates
+// Host side of the norm, MXFP8, linear-layer and cross-entropy entry points:
+// argument checks and launches. Every check runs before the first launch; nothing allocates
 // device memory or synchronizes.
 #include <atomic>
 #include <cmath>
@@ -188,6 +188,74 @@ size_t act_back_bytes(int64_t m, int64_t N, int32_t gated) {
   return (size_t)act_backward_groups(m, gated ? N / 2 : N) * (size_t)N * sizeof(float);
 }
 
+// ---- cross entropy ------------------------------------------------------------
+constexpr int64_t kMaxTiled = int64_t{1} << 46;     // rows * columns of a product: 2^30 tiles
+constexpr int64_t kMaxTileRow = int64_t{1} << 22;   // elements of a row of bf16 (8 MB)
+
+// m * n, both below 2^30.
+bool tiles_fit(int64_t m, int64_t n) { return m * n < kMaxTiled; }
+
+// What both calls ask of their common arguments.
+template <typename Args>
+adahop_status check_xent(const Args& a) {
+  if (a.rows < 0 || a.vocab < 1 || a.dim < 1) return invalid("xent: rows must be >= 0, vocab and dim >= 1");
+  if (a.rows >= kMaxDim || a.vocab >= kMaxDim) return unsupported("xent: rows or vocab of 2^30 or more");
+  if (!tiles_fit(a.rows, a.vocab)) return unsupported("xent: rows * vocab of 2^46 or more");
+  if (!all_zero(a.reserved)) return invalid("xent: reserved fields must be 0");
+  if (a.target_dtype != ADAHOP_INDEX_I32 && a.target_dtype != ADAHOP_INDEX_I64)
+    return invalid("xent: bad target_dtype");
+  if (!std::isfinite(a.scale)) return invalid("xent: scale must be finite");
+  if (a.ld_h < a.dim || a.ld_w < a.dim) return invalid("xent: ld_h or ld_w below dim");
+  if (a.dim % 8 != 0 || a.ld_h % 8 != 0 || a.ld_w % 8 != 0 || !aligned16(a.h) || !aligned16(a.w))
+    return unsupported("xent: rows of h and w must be 16-byte aligned, dim a multiple of 8");
+  if (a.ld_h >= kMaxTileRow || a.ld_w >= kMaxTileRow) return unsupported("xent: rows 8 MB or more apart");
+  if (a.rows > 0 && (!a.h || !a.w || !a.targets)) return invalid("xent: null h, w or targets");
+  return ADAHOP_OK;
+}
+
+template <typename Args>
+XentArgs xent_args(const Args& a) {
+  return {a.rows, a.vocab, a.dim, a.h, a.ld_h, a.w, a.ld_w, a.targets, a.target_dtype == ADAHOP_INDEX_I64, a.scale};
+}
+
+size_t xent_bytes(int64_t rows, int64_t vocab) {
+  if (rows < 1 || vocab < 1 || rows >= kMaxDim || vocab >= kMaxDim || !tiles_fit(rows, vocab)) return 0;
+  return xent_ws_bytes(rows, vocab);
+}
+
+adahop_status xent(const adahop_xent_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (a == nullptr) return invalid("xent: null arguments");
+  ADAHOP_TRY(check_xent(*a));
+  if (a->rows == 0) return ADAHOP_OK;
+  if (!a->loss || !a->lse) return invalid("xent: null loss or lse");
+  ADAHOP_TRY(need_workspace(ws, ws_bytes, xent_bytes(a->rows, a->vocab), "xent"));
+  return xent_launch(xent_args(*a), a->loss, a->lse, ws, stream);
+}
+
+adahop_status check_xent_back(const adahop_xent_backward_args& a) {
+  ADAHOP_TRY(check_xent(a));
+  if (a.rows > 0 && !a.dh && !a.dw) return invalid("xent_backward: neither dh nor dw");
+  if (!tiles_fit(a.rows, a.dim)) return unsupported("xent_backward: rows * dim of 2^46 or more");
+  if ((a.dh && (a.ld_dh < a.dim || !valid_dtype(a.dh_dtype))) ||
+      (a.dw && (a.ld_dw < a.dim || !valid_dtype(a.dw_dtype))))
+    return invalid("xent_backward: leading dimension of dh or dw below dim, or a bad dtype");
+  if (a.piece < 0) return invalid("xent_backward: piece must be >= 0");
+  if (a.rows > 0 && (!a.lse || !a.dloss)) return invalid("xent_backward: null lse or dloss");
+  return ADAHOP_OK;
+}
+
+size_t xent_back_bytes(const adahop_xent_backward_args& a) {
+  return xent_backward_ws_bytes(a.rows, a.vocab, a.dim, a.piece, a.dh != nullptr, a.dw != nullptr);
+}
+
+adahop_status xent_back(const adahop_xent_backward_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (a == nullptr) return invalid("xent_backward: null arguments");
+  ADAHOP_TRY(check_xent_back(*a));
+  ADAHOP_TRY(need_workspace(ws, ws_bytes, xent_back_bytes(*a), "xent_backward"));
+  const XentGrad g = {a->lse, a->dloss, a->dlse, a->dh, a->ld_dh, a->dh_dtype, a->dw, a->ld_dw, a->dw_dtype};
+  return xent_backward_launch(xent_args(*a), g, a->piece, ws, stream);
+}
+
 }  // namespace
 
 int64_t compute_units() {
@@ -291,6 +359,29 @@ adahop_status adahop_act_backward(const void* dout, adahop_out_dtype dout_dtype,
     return act_backward_launch(dout, dout_dtype, z, act, gated, m, n, ld_dout, ld_z, dz, ld_dz, dbias,
                                static_cast<float*>(ws), static_cast<hipStream_t>(stream));
   });
+}
+
+size_t adahop_xent_workspace_size(int64_t rows, int64_t vocab) { return xent_bytes(rows, vocab); }
+
+adahop_status adahop_xent(const adahop_xent_args* args, void* ws, size_t ws_bytes, void* stream) {
+  return entry([&] { return xent(args, ws, ws_bytes, static_cast<hipStream_t>(stream)); });
+}
+
+size_t adahop_xent_backward_args_workspace_size(const adahop_xent_backward_args* args) {
+  size_t bytes = 0;
+  const adahop_status st = entry([&]() -> adahop_status {
+    if (args == nullptr) return ADAHOP_ERR_INVALID;
+    ADAHOP_TRY(check_xent_back(*args));
+    bytes = xent_back_bytes(*args);
+    return ADAHOP_OK;
+  });
+  set_error("");
+  return st == ADAHOP_OK ? bytes : 0;
+}
+
+adahop_status adahop_xent_backward(const adahop_xent_backward_args* args, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  return entry([&] { return xent_back(args, ws, ws_bytes, static_cast<hipStream_t>(stream)); });
 }
 
 }  // extern "C"

@@ -1,0 +1,425 @@
+// Softmax cross entropy over a vocabulary, from hidden states h [T, D] and output
+// weights w [V, D] in bf16, without the logits; and its gradient (gfx950).
+//
+//   z = scale h w^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,y(t)
+//   g_tv = scale ((dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = y(t)])
+//   dh = g w,  dw = g^T h
+//
+// Forward: one product in 256 x 256 tiles (bf16_tiles.h) whose epilogue leaves,
+// for each row and 64 columns, their maximum and the sum of their exponentials
+// under it, and the target's logit; a second kernel joins them in a fixed order.
+// Backward: the vocabulary in pieces; for each the logits again, whose epilogue
+// writes g of the piece in bf16, and the two products of g. g is rounded to
+// bf16 (at most 2^-8 of each element, no sum is formed in it) since only
+// then its products run on the bf16 matrix cores; everything else is fp32. dh is
+// added up over the pieces in fp32 and rounded once.
+//
+// Bound by the matrix cores: 2 T V D operations forward, 6 T V D backward.
+#include "bf16_tiles.h"
+
+namespace adahop {
+namespace {
+
+using namespace tiles;
+using mx8::f32_to_bf16;
+using mx8::f32x2_to_bf16x2;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinusInf = -__builtin_inff();
+
+// exp(x - max) with max replaced by 0 where it is no number to subtract, so
+// that a row of -inf sums to 0 and one with +inf to +inf.
+__device__ __forceinline__ float shift_of(float max) {
+  return __builtin_fabsf(max) < __builtin_inff() ? max : 0.0f;
+}
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(kLog2e * x); }
+
+struct Targets {
+  const void* p;
+  int wide;                  // int64, else int32
+  __device__ __forceinline__ int64_t at(int64_t row) const {
+    return wide ? static_cast<const int64_t*>(p)[row] : (int64_t)static_cast<const int32_t*>(p)[row];
+  }
+};
+
+// ---- epilogues ----------------------------------------------------------------
+// A product as it stands: to bf16 or fp32, on top of `prev` if given. n is a
+// multiple of 8, so 4 columns are inside or outside together.
+struct StoreEpi {
+  void* out;
+  int64_t ld;
+  int f32;
+  const float* prev;         // [m][ld_prev], or null
+  int64_t ld_prev;
+  template <bool Wide>
+  __device__ __forceinline__ void store(v4f (&acc)[8][4], const Spot& at, int64_t m, int64_t n) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = at.row0 + 16 * i;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int step = (Wide ? 4 : 16) * j;
+        if (at.to != nullptr) {
+          *reinterpret_cast<v4f*>(at.to + (at.lrow + 16 * i) * kTile + at.lcol + step) = acc[i][j];
+          continue;
+        }
+        const int64_t c = at.col0 + step;
+        if (r >= m || c >= n) continue;
+        v4f v = acc[i][j];
+        if (prev != nullptr) {
+          v4f p;
+          __builtin_memcpy(&p, prev + r * ld_prev + c, 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += p[e];
+        }
+        if (f32) {
+          __builtin_memcpy(static_cast<float*>(out) + r * ld + c, &v, 16);
+        } else {
+          const mx8::u32x2 w = {f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3])};
+          __builtin_memcpy(static_cast<uint16_t*>(out) + r * ld + c, &w, 8);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+// The logits' maximum and sum over the wave's 64 columns of each row, and the
+// target's logit.
+struct StatsEpi {
+  float scale;
+  Targets y;
+  float2* part;              // [tile column][wave column][T]
+  float* said;               // [T]: the target's logit
+  template <bool Wide>
+  __device__ __forceinline__ void store(v4f (&acc)[8][4], const Spot& at, int64_t m, int64_t n) const {
+    static_assert(Wide, "");
+    float2* to = part + ((int64_t)at.tn * 4 + at.wn) * m;
+    const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = at.row0 + 16 * i;
+      float z[16], top = kMinusInf;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        z[e] = e < inside ? scale * acc[i][e / 4][e % 4] : kMinusInf;
+        top = __builtin_fmaxf(top, z[e]);
+      }
+      top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+      const float by = shift_of(top);
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum += exp_of(z[e] - by);
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (r < m) {
+        if ((threadIdx.x & 48) == 0) to[r] = float2{top, sum};
+        const int64_t d = y.at(r) - at.col0;
+        if (d >= 0 && d < inside) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (d == e) said[r] = z[e];
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+// The gradient of a piece's logits, columns v0 .. of the vocabulary; a tile's
+// columns past the piece's end are written as zeros.
+struct GradEpi {
+  float scale;
+  Targets y;
+  const float* lse;
+  const float* dloss;
+  const float* dlse;         // or null
+  int64_t v0, vocab;
+  uint16_t* g;
+  int64_t ld;
+  template <bool Wide>
+  __device__ __forceinline__ void store(v4f (&acc)[8][4], const Spot& at, int64_t m, int64_t n) const {
+    static_assert(Wide, "");
+    const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = at.row0 + 16 * i;
+      if (r < m) {
+        const float less = lse[r];
+        const int64_t t = y.at(r);
+        const float own = t >= 0 && t < vocab ? dloss[r] : 0.0f;
+        const float all = scale * (dlse == nullptr ? own : own + dlse[r]);
+        const int64_t d = t - v0 - at.col0;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          v[e] = all * exp_of(__builtin_fmaf(acc[i][e / 4][e % 4], scale, -less));
+          if (e >= inside) v[e] = 0.0f;
+        }
+        if (d >= 0 && d < inside) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (d == e) v[e] -= scale * own;
+        }
+        mx8::u32x4 w[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+        mx8::u32x4* to = reinterpret_cast<mx8::u32x4*>(g + r * ld + at.col0);
+        to[0] = w[0];
+        to[1] = w[1];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+// ---- joining ------------------------------------------------------------------
+// lse and loss of a row from its parts' maxima and sums: 16 rows a workgroup,
+// 16 lanes a row, lane l taking parts l, l + 16, ...; then the lanes in pairs.
+struct FinishArgs {
+  const float2* part;
+  const float* said;
+  Targets y;
+  int64_t rows, vocab;
+  int64_t parts;
+  float* loss;
+  float* lse;
+};
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float top = __builtin_fmaxf(a.x, b.x), by = shift_of(top);
+  // A part of -inf alone holds a sum of 0 (or a NaN): no shift applies to it.
+  auto shifted = [&](float2 p) { return p.x == kMinusInf ? p.y : p.y * exp_of(shift_of(p.x) - by); };
+  return float2{top, shifted(a) + shifted(b)};
+}
+__global__ void __launch_bounds__(256) xent_finish_kernel(FinishArgs a) {
+  __shared__ float2 red[16][17];
+  const int row = threadIdx.x & 15, lane = threadIdx.x >> 4;
+  const int64_t r = (int64_t)blockIdx.x * 16 + row;
+  float2 s = {kMinusInf, 0.0f};
+  if (r < a.rows) {
+#pragma unroll 8
+    for (int64_t p = lane; p < a.parts; p += 16) s = join(s, a.part[p * a.rows + r]);
+  }
+  red[lane][row] = s;
+#pragma unroll
+  for (int half = 8; half >= 1; half /= 2) {
+    __syncthreads();
+    if (lane < half) red[lane][row] = join(red[lane][row], red[lane + half][row]);
+  }
+  if (lane == 0 && r < a.rows) {
+    s = red[0][row];
+    const float lse = shift_of(s.x) + logf(s.y);
+    const int64_t t = a.y.at(r);
+    a.lse[r] = lse;
+    a.loss[r] = t >= 0 && t < a.vocab ? lse - a.said[r] : 0.0f;
+  }
+}
+
+// Adds the parts of the split tiles in order and stores them. Workgroup b takes
+// rows 16 (b % 16) .. +15 of split tile b / 16.
+__global__ void __launch_bounds__(256) tile_join_kernel(TileArgs t, StoreEpi epi) {
+  const int tile = blockIdx.x >> 4, band = blockIdx.x & 15;
+  int tm, tn;
+  tile_at(t.full + tile, t.tiles_m, t.tiles_n, &tm, &tn);
+  const int lc = 4 * (threadIdx.x & 63);
+  const int64_t c = (int64_t)tn * kTile + lc;
+  const float* first = t.split_ws + (int64_t)tile * t.parts * (kTile * kTile);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int lr = 16 * band + (threadIdx.x >> 6) + 4 * i;
+    const int64_t r = (int64_t)tm * kTile + lr;
+    if (r >= t.m || c >= t.n) continue;
+    v4f v = *reinterpret_cast<const v4f*>(first + lr * kTile + lc);
+    for (int p = 1; p < t.parts; ++p) {
+      const v4f b = *reinterpret_cast<const v4f*>(first + (int64_t)p * (kTile * kTile) + lr * kTile + lc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += b[e];
+    }
+    if (epi.prev != nullptr) {
+      v4f b;
+      __builtin_memcpy(&b, epi.prev + r * epi.ld_prev + c, 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += b[e];
+    }
+    if (epi.f32) {
+      __builtin_memcpy(static_cast<float*>(epi.out) + r * epi.ld + c, &v, 16);
+    } else {
+      const mx8::u32x2 w = {f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3])};
+      __builtin_memcpy(static_cast<uint16_t*>(epi.out) + r * epi.ld + c, &w, 8);
+    }
+  }
+}
+
+// ---- host ---------------------------------------------------------------------
+int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
+int64_t units_of(int64_t K) { return (K + 2 * kStageK - 1) / (2 * kStageK); }
+
+// The last round of tiles split along K where it leaves half of the compute
+// units or more without one (a part: at least 4 pairs of stages).
+struct Split {
+  int64_t full, split;
+  int parts;
+};
+Split split_of(int64_t m, int64_t n, int64_t K) {
+  const int64_t all = tiles_of(m) * tiles_of(n), cus = compute_units(), rem = all % cus;
+  int64_t parts = rem > 0 ? cus / rem : 1;
+  if (parts > units_of(K) / 4) parts = units_of(K) / 4;
+  if (parts > 32) parts = 32;
+  if (parts < 2) return {all, 0, 1};
+  return {all - rem, rem, (int)parts};
+}
+size_t split_bytes(int64_t m, int64_t n, int64_t K) {
+  const Split s = split_of(m, n, K);
+  return s.split ? (size_t)s.split * s.parts * kTile * kTile * sizeof(float) : 0;
+}
+
+TileArgs tile_args(Operand a, Operand b, int64_t m, int64_t n, int64_t K) {
+  TileArgs t{};
+  t.a = a;
+  t.b = b;
+  t.m = m;
+  t.n = n;
+  t.K = K;
+  t.tiles_m = (int)tiles_of(m);
+  t.tiles_n = (int)tiles_of(n);
+  t.units = (int)units_of(K);
+  t.full = t.tiles_m * t.tiles_n;
+  t.parts = 1;
+  return t;
+}
+dim3 tile_grid(const TileArgs& t) {
+  const int64_t items = (int64_t)t.full + (int64_t)t.split * t.parts, cus = compute_units();
+  return dim3((unsigned)(items < cus ? items : cus));
+}
+
+// One product of the gradient: whole tiles, split ones, and their join.
+template <Kind AK>
+adahop_status product(Operand a, Operand b, int64_t m, int64_t n, int64_t K, const StoreEpi& epi, float* ws,
+                      hipStream_t stream) {
+  TileArgs t = tile_args(a, b, m, n, K);
+  const Split s = split_of(m, n, K);
+  t.full = (int)s.full;
+  t.split = (int)s.split;
+  t.parts = s.parts;
+  t.split_ws = ws;
+  bf16_tile_kernel<AK, kAcross, StoreEpi><<<tile_grid(t), dim3(kThreads), 0, stream>>>(t, epi);
+  adahop_status st = check_launch("xent_backward product");
+  if (st != ADAHOP_OK || t.split == 0) return st;
+  tile_join_kernel<<<dim3((unsigned)(16 * t.split)), dim3(256), 0, stream>>>(t, epi);
+  return check_launch("xent_backward join");
+}
+
+Operand along(const uint16_t* p, int64_t ld) { return {reinterpret_cast<const uint8_t*>(p), 2 * ld}; }
+
+}  // namespace
+
+size_t xent_ws_bytes(int64_t T, int64_t V) {
+  return align_up(sizeof(float2) * (size_t)tiles_of(V) * 4 * (size_t)T, kAlign) + sizeof(float) * (size_t)T;
+}
+
+adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t stream) {
+  const Targets y = {a.targets, a.wide_targets};
+  float2* part = static_cast<float2*>(ws);
+  float* said = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                         align_up(sizeof(float2) * (size_t)tiles_of(a.V) * 4 * (size_t)a.T, kAlign));
+  const TileArgs t = tile_args(along(a.h, a.ldh), along(a.w, a.ldw), a.T, a.V, a.D);
+  const StatsEpi epi = {a.scale, y, part, said};
+  bf16_tile_kernel<kAlong, kAlong, StatsEpi><<<tile_grid(t), dim3(kThreads), 0, stream>>>(t, epi);
+  const adahop_status st = check_launch("xent");
+  if (st != ADAHOP_OK) return st;
+  const FinishArgs f = {part, said, y, a.T, a.V, tiles_of(a.V) * 4, loss, lse};
+  xent_finish_kernel<<<dim3((unsigned)((a.T + 15) / 16)), dim3(256), 0, stream>>>(f);
+  return check_launch("xent_finish");
+}
+
+// ---- backward -------------------------------------------------------------------
+XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece) {
+  const int64_t all = tiles_of(V) * kTile;
+  if (piece == 0) {
+    // g of a piece within 1 GiB, in pieces of about the same size.
+    piece = (int64_t{1} << 29) / (T > 0 ? T : 1) / kTile * kTile;
+    if (piece < kTile) piece = kTile;
+    if (piece > all) piece = all;
+    const int64_t count = (all + piece - 1) / piece;
+    piece = tiles_of((all + count - 1) / count) * kTile;
+  }
+  // A row of g stays within the tiles' reach.
+  if (piece > kMaxRowBytes / 4) piece = kMaxRowBytes / 4;
+  piece = tiles_of(piece < V ? piece : V) * kTile;
+  return {piece, (V + piece - 1) / piece};
+}
+
+namespace {
+struct BackLayout {
+  XentPieces p;
+  size_t off_sum, off_split, bytes;
+};
+BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, bool dw) {
+  BackLayout l{};
+  l.p = xent_pieces(T, V, piece);
+  size_t at = align_up(2 * (size_t)T * (size_t)l.p.size, kAlign);
+  l.off_sum = at;
+  if (dh && l.p.count > 1) at += align_up(4 * (size_t)T * (size_t)D, kAlign);
+  l.off_split = at;
+  const int64_t last = V - (l.p.count - 1) * l.p.size;
+  size_t split = 0;
+  for (const int64_t n : {l.p.size < V ? l.p.size : V, last}) {
+    const size_t s = dh ? split_bytes(T, D, n) : 0, u = dw ? split_bytes(n, D, T) : 0;
+    split = split > s ? split : s;
+    split = split > u ? split : u;
+  }
+  l.bytes = at + split;
+  return l;
+}
+
+__global__ void __launch_bounds__(256) zero_rows_kernel(void* out, int64_t rows, int64_t cols, int64_t ld, int f32) {
+  const int64_t n = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cols, c = i - r * cols;
+    if (f32) static_cast<float*>(out)[r * ld + c] = 0.0f;
+    else static_cast<uint16_t*>(out)[r * ld + c] = 0;
+  }
+}
+}  // namespace
+
+size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, bool dw) {
+  return T == 0 ? 0 : back_layout(T, V, D, piece, dh, dw).bytes;
+}
+
+adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t piece, void* ws,
+                                   hipStream_t stream) {
+  if (a.T == 0) {
+    if (b.dw == nullptr) return ADAHOP_OK;
+    zero_rows_kernel<<<dim3(2048), dim3(256), 0, stream>>>(b.dw, a.V, a.D, b.lddw, b.dw_f32);
+    return check_launch("xent_backward");
+  }
+  const BackLayout l = back_layout(a.T, a.V, a.D, piece, b.dh != nullptr, b.dw != nullptr);
+  uint16_t* g = static_cast<uint16_t*>(ws);
+  float* sum = reinterpret_cast<float*>(static_cast<char*>(ws) + l.off_sum);
+  float* split = reinterpret_cast<float*>(static_cast<char*>(ws) + l.off_split);
+  const Targets y = {a.targets, a.wide_targets};
+  for (int64_t q = 0; q < l.p.count; ++q) {
+    const int64_t v0 = q * l.p.size, n = a.V - v0 < l.p.size ? a.V - v0 : l.p.size;
+    const Operand h = along(a.h, a.ldh), w = along(a.w + v0 * a.ldw, a.ldw), og = along(g, l.p.size);
+    const TileArgs t = tile_args(h, w, a.T, n, a.D);
+    const GradEpi epi = {a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, l.p.size};
+    bf16_tile_kernel<kAlong, kAlong, GradEpi><<<tile_grid(t), dim3(kThreads), 0, stream>>>(t, epi);
+    adahop_status st = check_launch("xent_backward logits");
+    if (st != ADAHOP_OK) return st;
+    if (b.dh != nullptr) {
+      const bool last = q + 1 == l.p.count;
+      const StoreEpi to = {last ? b.dh : sum, last ? b.lddh : a.D, last ? b.dh_f32 : 1, q > 0 ? sum : nullptr, a.D};
+      st = product<kAlong>(og, w, a.T, a.D, n, to, split, stream);
+      if (st != ADAHOP_OK) return st;
+    }
+    if (b.dw != nullptr) {
+      const StoreEpi to = {static_cast<char*>(b.dw) + (b.dw_f32 ? 4 : 2) * v0 * b.lddw, b.lddw, b.dw_f32, nullptr, 0};
+      st = product<kAcross>(og, h, n, a.D, a.T, to, split, stream);
+      if (st != ADAHOP_OK) return st;
+    }
+  }
+  return ADAHOP_OK;
+}
+
+}  // namespace adahop

@@ -647,6 +647,84 @@ ADAHOP_API adahop_status adahop_act_backward(const void* dout, adahop_out_dtype 
                                              size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Gradients from activations kept in MXFP8, as adahop_mx8_quant or a layer's
+ * MXFP8 output writes them (checkpoints of 33 bytes in 32 elements). They are the
+ * gradients of the functions at the kept values.
+ *
+ * adahop_act_backward's, from z [m, N] in MXFP8 (N a multiple of 32), and, if
+ * `out` is not NULL, the layer's output made again beside it, so that it need
+ * not be kept:
+ *   out = act(z)   [m, n], n = N;   gated: act(z[:, :n]) * z[:, n:],  n = N / 2
+ * in bf16 (without the residual). dz bf16 [m, N]; dbias fp32 [N] or NULL, with
+ * adahop_act_backward_workspace_size(m, N, gated) bytes of workspace.
+ * Errors: as adahop_act_backward, and INVALID for N not a multiple of 32 (gated:
+ * n a multiple of 16 then), reserved not 0. */
+typedef struct {
+  int64_t m, N;
+  const void* dout; int64_t ld_dout;             /* [m, n] */
+  const uint8_t* z_codes; int64_t ld_z_codes;
+  const uint8_t* z_scales; int64_t ld_z_scales;
+  uint16_t* dz; int64_t ld_dz;
+  uint16_t* out; int64_t ld_out;                 /* NULL: not wanted */
+  float* dbias;                                  /* NULL: not wanted */
+  int32_t dout_dtype;                            /* adahop_out_dtype */
+  int32_t act, gated;
+  int32_t reserved[5];
+} adahop_act_backward_mx8_args;
+
+ADAHOP_API adahop_status adahop_act_backward_mx8(const adahop_act_backward_mx8_args* args, void* ws,
+                                                 size_t ws_bytes, void* stream);
+
+/* adahop_rmsnorm_backward's, from h in MXFP8 (cols a multiple of 32) and the rstd
+ * of the forward pass. dx and dh have the type dx_dtype; dx may be dh, or dy where
+ * the types agree. Workspace as adahop_rmsnorm_backward's.
+ * Errors: as adahop_rmsnorm_backward, and INVALID for cols not a multiple of 32. */
+typedef struct {
+  int64_t rows, cols;
+  const void* dy; int64_t ld_dy;
+  const uint8_t* h_codes; int64_t ld_h_codes;
+  const uint8_t* h_scales; int64_t ld_h_scales;
+  const void* gain;
+  const float* rstd;
+  const void* dh; int64_t ld_dh;                 /* NULL: none */
+  void* dx; int64_t ld_dx;
+  float* dgain;                                  /* NULL: not wanted */
+  int32_t dy_dtype, dx_dtype, gain_dtype;
+  int32_t reserved[5];
+} adahop_rmsnorm_backward_mx8_args;
+
+ADAHOP_API adahop_status adahop_rmsnorm_backward_mx8(const adahop_rmsnorm_backward_mx8_args* args,
+                                                     void* ws, size_t ws_bytes, void* stream);
+
+/* Weight gradient of a linear layer from its MXFP8 input X [T, Din] as it was
+ * kept (the A operand of adahop_linear_mx), without a bf16 copy of it:
+ *   dW [Dout, Din] = GY^T * X,   GY bf16 [T, Dout]
+ * X's values are taken in bf16 as adahop_mx8_dequant gives them (those below
+ * bf16's normal range, 2^-126, may count as 0), products are exact, sums fp32,
+ * dW (bf16 or fp32) is rounded once. T is any; T = 0 gives zeros. Needs
+ * adahop_gemm_wgrad_mx8_workspace_size(T, Din, Dout) bytes of 16-byte aligned
+ * workspace (the parts of products split along T).
+ * Errors: INVALID for T < 0, Din or Dout < 1, NULL GY, codes or scales (T > 0) or
+ * out, leading dimensions too small, Din not a multiple of 32, a bad dtype,
+ * reserved not 0; UNSUPPORTED for Dout or ld_gy that is not a multiple of 8,
+ * ld_x_codes not a multiple of 16, GY or codes not 16-byte aligned, rows 8 MB or
+ * more apart, T, Din or Dout of 2^30 and more, Din * Dout of 2^46 and more;
+ * WORKSPACE. */
+typedef struct {
+  int64_t T, Din, Dout;
+  const uint16_t* gy; int64_t ld_gy;
+  const uint8_t* x_codes; int64_t ld_x_codes;
+  const uint8_t* x_scales; int64_t ld_x_scales;
+  void* out; int64_t ld_out;
+  int32_t out_dtype;                             /* adahop_out_dtype */
+  int32_t reserved[5];
+} adahop_gemm_wgrad_mx8_args;
+
+ADAHOP_API size_t adahop_gemm_wgrad_mx8_workspace_size(int64_t T, int64_t Din, int64_t Dout);
+ADAHOP_API adahop_status adahop_gemm_wgrad_mx8(const adahop_gemm_wgrad_mx8_args* args, void* ws,
+                                               size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Softmax cross entropy over a vocabulary, from hidden states h [T, D] and the
  * output layer's weights w [V, D], without keeping the logits:
  *   z = scale * h * w^T                                      [T, V]

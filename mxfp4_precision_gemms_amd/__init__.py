@@ -96,6 +96,27 @@ class LinearArgs(ctypes.Structure):
                 ("gated", _i32), ("products", _i32), ("reserved", _i32 * 3)]
 
 
+class ActBackwardMx8Args(ctypes.Structure):
+    _fields_ = [("m", _i64), ("N", _i64), ("dout", _p), ("ld_dout", _i64),
+                ("z_codes", _p), ("ld_z_codes", _i64), ("z_scales", _p), ("ld_z_scales", _i64),
+                ("dz", _p), ("ld_dz", _i64), ("out", _p), ("ld_out", _i64), ("dbias", _p),
+                ("dout_dtype", _i32), ("act", _i32), ("gated", _i32), ("reserved", _i32 * 5)]
+
+
+class RmsnormBackwardMx8Args(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("dy", _p), ("ld_dy", _i64),
+                ("h_codes", _p), ("ld_h_codes", _i64), ("h_scales", _p), ("ld_h_scales", _i64),
+                ("gain", _p), ("rstd", _p), ("dh", _p), ("ld_dh", _i64), ("dx", _p), ("ld_dx", _i64),
+                ("dgain", _p), ("dy_dtype", _i32), ("dx_dtype", _i32), ("gain_dtype", _i32),
+                ("reserved", _i32 * 5)]
+
+
+class GemmWgradMx8Args(ctypes.Structure):
+    _fields_ = [("T", _i64), ("Din", _i64), ("Dout", _i64), ("gy", _p), ("ld_gy", _i64),
+                ("x_codes", _p), ("ld_x_codes", _i64), ("x_scales", _p), ("ld_x_scales", _i64),
+                ("out", _p), ("ld_out", _i64), ("out_dtype", _i32), ("reserved", _i32 * 5)]
+
+
 class XentArgs(ctypes.Structure):
     _fields_ = [("rows", _i64), ("vocab", _i64), ("dim", _i64), ("h", _p), ("ld_h", _i64),
                 ("w", _p), ("ld_w", _i64), ("targets", _p), ("loss", _p), ("lse", _p),
@@ -155,6 +176,10 @@ SIGNATURES = {
     "adahop_act_backward_workspace_size": ([_i64, _i64, _i32], _sz),
     "adahop_act_backward": ([_p, _int, _i64, _p, _i64, _i64, _i64, _int, _i32, _p, _i64, _p, _p,
                              _sz, _p], _int),
+    "adahop_act_backward_mx8": ([ctypes.POINTER(ActBackwardMx8Args), _p, _sz, _p], _int),
+    "adahop_rmsnorm_backward_mx8": ([ctypes.POINTER(RmsnormBackwardMx8Args), _p, _sz, _p], _int),
+    "adahop_gemm_wgrad_mx8_workspace_size": ([_i64, _i64, _i64], _sz),
+    "adahop_gemm_wgrad_mx8": ([ctypes.POINTER(GemmWgradMx8Args), _p, _sz, _p], _int),
     "adahop_xent_workspace_size": ([_i64, _i64], _sz),
     "adahop_xent": ([ctypes.POINTER(XentArgs), _p, _sz, _p], _int),
     "adahop_xent_backward_args_workspace_size": ([ctypes.POINTER(XentBackwardArgs)], _sz),
@@ -816,6 +841,98 @@ def adahop_act_backward(dout: torch.Tensor, z: torch.Tensor, act: str = "NONE", 
     _check(lib().adahop_act_backward(gp, gk, ldg, zp, ldz, m, N, ACT[act], int(gated), op, ldo, bp, wp,
                                      wn, _stream(dev)))
     return dz, dbias
+
+
+# ---------------------------------------------------------------------------
+# Gradients from activations kept in MXFP8
+# ---------------------------------------------------------------------------
+class ActBackwardMx8Out(NamedTuple):
+    dz: torch.Tensor                 # bf16 [m, N]
+    dbias: Optional[torch.Tensor]    # fp32 [N], if asked for
+    out: Optional[torch.Tensor]      # bf16 [m, n]: the layer's output, if asked for
+
+
+def adahop_act_backward_mx8(dout: torch.Tensor, z: Tuple[torch.Tensor, torch.Tensor], act: str = "NONE",
+                            gated: bool = False, bias_grad: bool = False, remake_out: bool = False,
+                            dz: Optional[torch.Tensor] = None,
+                            ws: Optional[torch.Tensor] = None) -> ActBackwardMx8Out:
+    """adahop_act_backward from z kept in MXFP8 (codes [m, N], scales
+    [m, N / 32]); remake_out: also the output act(z) [* up] at the kept z, so
+    that it need not be kept for the next layer's weight gradient."""
+    zc, zs = z
+    m, N = _size(zc, "z codes")
+    n = N // 2 if gated else N
+    dev, d = zc.device, zc.get_device()
+    gp, ldg, gk = _matrix(dout, "dout", _FLOAT, m, n, d)
+    zp, ldz, _ = _matrix(zc, "z codes", _CODES, m, N, d)
+    sp, lds, _ = _matrix(zs, "z scales", _SCALES, m, N // 32, d)
+    if dz is None:
+        dz = torch.empty((m, N), dtype=torch.bfloat16, device=dev)
+    op, ldo, _ = _matrix(dz, "dz", _BF16, m, N, d)
+    a = ActBackwardMx8Args(m, N, gp, ldg, zp, ldz, sp, lds, op, ldo, None, n, None, gk, ACT[act], int(gated))
+    out = dbias = wp = None
+    wn = 0
+    if remake_out:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        a.out = out.data_ptr()
+    if bias_grad:
+        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+        a.dbias = dbias.data_ptr()
+        wp, wn, ws = _scratch(lib().adahop_act_backward_workspace_size(m, N, int(gated)), ws, dev)
+    _check(lib().adahop_act_backward_mx8(ctypes.byref(a), wp, wn, _stream(dev)))
+    return ActBackwardMx8Out(dz, dbias, out)
+
+
+def adahop_rmsnorm_backward_mx8(dy: torch.Tensor, h: Tuple[torch.Tensor, torch.Tensor], gain: torch.Tensor,
+                                rstd: torch.Tensor, dh: Optional[torch.Tensor] = None,
+                                gain_grad: bool = True, dx_dtype=torch.bfloat16,
+                                dx: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """(dx, dgain) of adahop_rmsnorm_backward from h kept in MXFP8 (codes
+    [rows, cols], scales [rows, cols / 32]) and the forward's rstd. dx has
+    dx_dtype, or dh's type if that is given."""
+    hc, hs = h
+    rows, cols = _size(hc, "h codes")
+    dev, d = hc.device, hc.get_device()
+    yp, ldy, yk = _matrix(dy, "dy", _FLOAT, rows, cols, d)
+    hp, ldh, _ = _matrix(hc, "h codes", _CODES, rows, cols, d)
+    sp, lds, _ = _matrix(hs, "h scales", _SCALES, rows, cols // 32, d)
+    gp, gk = _vector(gain, "gain", _FLOAT, cols, d)
+    rp, _ = _vector(rstd, "rstd", {torch.float32: 1}, rows, d)
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=dx_dtype if dh is None else dh.dtype, device=dev)
+    xp, ldx, xk = _matrix(dx, "dx", _FLOAT, rows, cols, d)
+    a = RmsnormBackwardMx8Args(rows, cols, yp, ldy, hp, ldh, sp, lds, gp, rp, None, 0, xp, ldx, None, yk, xk, gk)
+    if dh is not None:
+        a.dh, a.ld_dh, ek = _matrix(dh, "dh", _FLOAT, rows, cols, d)
+        if ek != xk:
+            raise TypeError("dx must have dh's dtype")
+    dgain, wp, wn = None, None, 0
+    if gain_grad:
+        dgain = torch.empty(cols, dtype=torch.float32, device=dev)
+        a.dgain = dgain.data_ptr()
+        wp, wn, ws = _scratch(lib().adahop_rmsnorm_backward_workspace_size(rows, cols), ws, dev)
+    _check(lib().adahop_rmsnorm_backward_mx8(ctypes.byref(a), wp, wn, _stream(dev)))
+    return dx, dgain
+
+
+def adahop_gemm_wgrad_mx8(GY: torch.Tensor, x: Tuple[torch.Tensor, torch.Tensor], out_dtype=torch.bfloat16,
+                          out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dW [Dout, Din] = GY^T X of a linear layer, from GY (bf16 [T, Dout]) and
+    its input kept in MXFP8 (codes [T, Din], scales [T, Din / 32])."""
+    xc, xs = x
+    T, Dout = _size(GY, "GY")
+    _, Din = _size(xc, "x codes")
+    dev, d = GY.device, GY.get_device()
+    gp, ldg, _ = _matrix(GY, "GY", _BF16, T, Dout, d)
+    xp, ldx, _ = _matrix(xc, "x codes", _CODES, T, Din, d)
+    sp, lds, _ = _matrix(xs, "x scales", _SCALES, T, Din // 32, d)
+    if out is None:
+        out = torch.empty((Dout, Din), dtype=out_dtype, device=dev)
+    op, ldo, ok = _matrix(out, "out", _FLOAT, Dout, Din, d)
+    a = GemmWgradMx8Args(T, Din, Dout, gp, ldg, xp, ldx, sp, lds, op, ldo, ok)
+    wp, wn, ws = _scratch(lib().adahop_gemm_wgrad_mx8_workspace_size(T, Din, Dout), ws, dev)
+    _check(lib().adahop_gemm_wgrad_mx8(ctypes.byref(a), wp, wn, _stream(dev)))
+    return out
 
 
 # ---------------------------------------------------------------------------

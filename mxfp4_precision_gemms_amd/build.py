@@ -18,7 +18,7 @@ PROBE_SRC = "probe_mfma.hip"
 PROBE_LIB = os.path.join(HERE, "libadahop_probe.so")
 SOURCES = ["adahop_api.hip", "foid.hip", "iht_quant.hip", "gemm_mx.hip", "mx8_api.hip",
            "mx8_norm.hip", "mx8_act.hip", "linear_mx.hip",
-           "linear_tiles.hip", "xent.hip"]
+           "linear_tiles.hip", "bf16_products.hip", "xent.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

@@ -214,6 +214,22 @@ adahop_status act_backward_launch(const void* dout, int d_f32, const uint16_t* z
                                   int64_t m, int64_t n, int64_t lddo, int64_t ldz, uint16_t* dz,
                                   int64_t lddz, float* dbias, float* partial, hipStream_t stream);
 
+// The same from z, or h, kept in MXFP8 (leading dimensions in bytes); dx and dh
+// are of dx_f32's type, out (bf16, or null) is act(z) [* z_up] again.
+struct Mx8Matrix {
+  const uint8_t* codes;
+  int64_t ldc;
+  const uint8_t* scales;
+  int64_t lds;
+};
+adahop_status act_backward_mx8_launch(const void* dout, int d_f32, int64_t lddo, const Mx8Matrix& z, int act,
+                                      int gated, int64_t m, int64_t n, uint16_t* dz, int64_t lddz, uint16_t* out,
+                                      int64_t ldout, float* dbias, float* partial, hipStream_t stream);
+adahop_status rmsnorm_backward_mx8_launch(const void* dy, int dy_f32, int64_t lddy, const Mx8Matrix& h,
+                                          const void* gain, int gain_f32, const float* rstd, const void* dh,
+                                          int64_t lddh, int64_t rows, int64_t cols, void* dx, int dx_f32,
+                                          int64_t lddx, float* dgain, float* partial, hipStream_t stream);
+
 struct LinearArgs {
   const uint8_t* a_codes;
   const uint8_t* a_scales;
@@ -243,6 +259,39 @@ adahop_status linear_tiles_launch(const LinearArgs& a, int b_fp4, int gated, con
 size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int gated, bool mx8_out);
 adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, bool exact, void* scratch,
                                hipStream_t stream);
+
+// ---- products in 256 x 256 tiles ---------------------------------------------
+// C[i, j] = sum_k A(i, k) B(j, k) of bf16 operands, in fp32; then, on top of
+// `prev` (fp32 [m][ld_prev], or null), rounded to bf16 or stored in fp32. A lies
+// along K ([m][K]) or across it ([K][m]), B across ([K][n]), or, with A across,
+// in MXFP8 across ([K][n] codes, scales per 32 columns). Leading dimensions of
+// operands in bytes, those of bf16 multiples of 16 and below 8 MB; 16-byte
+// aligned; K of an A along it may end inside 16 bytes if what follows in them is
+// finite; n a multiple of 8 (codes: 32), m of an A across it likewise, or A's
+// rows reach to the next multiple; m, n, K below 2^30, m * n below 2^46. ws:
+// tile_product_bytes(m, n, K) bytes.
+struct TileOperand {
+  const void* p;
+  int64_t ld;
+  const uint8_t* scales;
+  int64_t ld_scales;
+  int kind;                  // tiles::Kind
+};
+struct TileOut {
+  void* p;
+  int64_t ld;
+  int f32;
+  const float* prev;
+  int64_t ld_prev;
+};
+size_t tile_product_bytes(int64_t m, int64_t n, int64_t K);
+adahop_status tile_product_launch(const TileOperand& a, const TileOperand& b, int64_t m, int64_t n, int64_t K,
+                                  const TileOut& out, float* ws, hipStream_t stream);
+
+// dW [Dout, Din] = GY^T X from X in MXFP8, checked; ws: tile_product_bytes(Dout,
+// Din, T) bytes.
+adahop_status wgrad_mx8_launch(const uint16_t* gy, int64_t ldgy, const Mx8Matrix& x, int64_t T, int64_t Din,
+                               int64_t Dout, void* out, int out_f32, int64_t ldo, float* ws, hipStream_t stream);
 
 // ---- cross entropy over a vocabulary ----------------------------------------
 // Arguments as the public entry points', already checked; T > 0 in xent_launch.

@@ -72,11 +72,14 @@ constexpr int kStageK = 64;                // K elements of a stage
 constexpr int kThreads = 512;
 constexpr int kGroupM = 4;                 // tile rows that run together on one XCD
 
-enum Kind { kAlong = 0, kAcross = 1 };
+// How an operand lies: along K, across it, or across it in MXFP8 (B alone).
+enum Kind { kAlong = 0, kAcross = 1, kCodes = 2 };
 
 struct Operand {
   const uint8_t* p;
   int64_t ld;                // bytes from a row to the next
+  const uint8_t* scales;     // kCodes: a byte per 32 columns
+  int64_t ld_scales;
 };
 
 struct TileArgs {
@@ -163,13 +166,14 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     int tm, tn, k0, k1, part, split_tile;
     const uint8_t* a;
     const uint8_t* b;
+    const uint8_t* scales;
     int a_bytes, b_bytes;
   };
   // Bytes of the 16-byte chunks that hold n elements.
   auto chunks = [](int64_t n) { return 2 * ((n + 7) & ~(int64_t)7); };
   auto place = [&](int item) {
     // Without an item: a stage past the end of any K.
-    Place p{0, 0, 1 << 28, 1 << 28, -1, 0, t.a.p, t.b.p, 0, 0};
+    Place p{0, 0, 1 << 28, 1 << 28, -1, 0, t.a.p, t.b.p, t.b.scales, 0, 0};
     if (item < 0) return p;
     int tile = item, part = -1;
     if (item >= t.full) {
@@ -202,9 +206,13 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       const int64_t rows = t.n - n0 < kTile ? t.n - n0 : kTile;
       p.b = t.b.p + n0 * t.b.ld;
       p.b_bytes = (int)((rows - 1) * t.b.ld + chunks(t.K));
-    } else {
+    } else if constexpr (BK == kAcross) {
       p.b = t.b.p + 2 * n0;
       p.b_bytes = (int)chunks(t.n - n0 < kTile ? t.n - n0 : kTile);
+    } else {
+      p.b = t.b.p + n0;
+      p.scales = t.b.scales + n0 / 32;
+      p.b_bytes = (int)(t.n - n0 < kTile ? t.n - n0 : kTile);   // a multiple of 32
     }
     return p;
   };
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   // that rows and K-rows past the ends read as 0. `left`: elements of K from
   // the stage's first.
   struct Source {
-    __amdgpu_buffer_rsrc_t a, b;
+    __amdgpu_buffer_rsrc_t a, b, scales;
     int left;
   };
   auto source_of = [&](Kind kind, const uint8_t* p, int bytes, int64_t ld, int k, int left) {
@@ -239,6 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     s.left = left;
     s.a = source_of(AK, in ? now.a : next.a, in ? now.a_bytes : next.a_bytes, t.a.ld, kk, left);
     s.b = source_of(BK, in ? now.b : next.b, in ? now.b_bytes : next.b_bytes, t.b.ld, kk, left);
+    if constexpr (BK == kCodes)
+      s.scales = source_of(BK, in ? now.scales : next.scales, (in ? now.b_bytes : next.b_bytes) / 32, t.b.ld_scales,
+                           kk, left);
     return s;
   };
   // Along K, load q of this wave fills rows 64 q + 8 wave + lane / 8 with chunks
@@ -252,7 +263,31 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   const int gb0 = ((lane & 31) >> 1) ^ ((kb & 3) + 4 * ((kb >> 3) & 1));
   const int oa = AK == kAlong ? row8 * (int)t.a.ld + 16 * ca
                               : ka * (int)t.a.ld + 256 * (ga >> 2) + 32 * (ga & 3) + 16 * (lane & 1);
-  const int ob = BK == kAlong ? row8 * (int)t.b.ld + 16 * cb : kb * (int)t.b.ld + 32 * gb0 + 16 * (lane & 1);
+  // Codes: two runs of 16 of a stage a thread, K-rows 32 u + thread / 16.
+  const int kc = threadIdx.x >> 4, gc = threadIdx.x & 15;
+  const int ob = BK == kCodes ? kc * (int)t.b.ld + 16 * gc : BK == kAlong ? row8 * (int)t.b.ld + 16 * cb : kb * (int)t.b.ld + 32 * gb0 + 16 * (lane & 1);
+  // Codes of the stage after the next but one, loaded a stage ahead of their
+  // widening into the slot that the stage before them frees.
+  v4i codes[2];
+  uint8_t scale[2];
+  const int oc = kc * 512 + 32 * (gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1)));
+  auto widen = [&](auto I) __attribute__((always_inline)) {
+    for_each<2>([&](auto U) {
+      const float by = mx8::mx8_scale(scale[U]);
+      v4i w[2];
+      for_each<4>([&](auto D) {
+        constexpr int d = decltype(D)::value;
+        const int four = codes[U][d];
+        const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)four, by, false);
+        const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)four, by, true);
+        w[d / 2][2 * (d % 2)] = __builtin_bit_cast(int, lo);
+        w[d / 2][2 * (d % 2) + 1] = __builtin_bit_cast(int, hi);
+      });
+      v4i* to = reinterpret_cast<v4i*>(wide(I).b + oc + 16384 * decltype(U)::value);
+      to[0] = w[0];
+      to[1] = w[1];
+    });
+  };
   // Across K, a row's last bytes are followed by the next row's: columns past
   // the tile's end reach only sums that are not stored.
   auto issue = [&](auto I, auto Q, const Source& s) __attribute__((always_inline)) {
@@ -263,6 +298,12 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       else v = oa + 32 * (q / 2) * (int)t.a.ld + 128 * (q % 2);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)&half(I, Int<q % 2>{}).a[1024 * (8 * (q / 2) + wave)],
                                                16, v, 0, 0, 0);
+    } else if constexpr (BK == kCodes) {
+      constexpr int u = (q - 4) / 2;
+      if constexpr (q % 2 == 0)
+        codes[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(s.b, ob + 32 * u * (int)t.b.ld, 0, 0));
+      else
+        scale[u] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, (kc + 32 * u) * (int)t.b.ld_scales + gc / 2, 0, 0);
     } else {
       constexpr int j = q - 4;
       int v;
@@ -335,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   auto stage = [&](auto I, int k, const Place& now, const Place& next) __attribute__((always_inline)) {
     using Next = Int<1 - decltype(I)::value>;
     const Source s = source(k + 2, now, next);
+    const Source sb = BK == kCodes ? source(k + 3, now, next) : s;
     read_a(I, Int<2>{}, Int<2>{});
     row(Int<0>{});
     __builtin_amdgcn_sched_barrier(0);
@@ -343,13 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     __builtin_amdgcn_sched_barrier(0);
     read_a(I, Int<3>{}, Int<3>{});
     row(Int<1>{});
-    issue(I, Int<4>{}, s);
-    issue(I, Int<5>{}, s);
+    if constexpr (BK == kCodes) widen(I);
+    issue(I, Int<4>{}, sb);
+    issue(I, Int<5>{}, sb);
     __builtin_amdgcn_sched_barrier(0);
     read_a(I, Int<0>{}, Int<4>{});
     row(Int<2>{});
-    issue(I, Int<6>{}, s);
-    issue(I, Int<7>{}, s);
+    issue(I, Int<6>{}, sb);
+    issue(I, Int<7>{}, sb);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, ReadsA));       // A 3 is read
     __builtin_amdgcn_s_barrier();
@@ -389,12 +432,20 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   for_each<2>([&](auto I) {
     const Source s = source(now.k0 + I, now, next);
     for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, s); });
+    if constexpr (BK == kCodes) widen(I);
     issue(I, Int<0>{}, s);
     issue(I, Int<2>{}, s);
     issue(I, Int<1>{}, s);
     issue(I, Int<3>{}, s);
   });
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 + Loads, 15));
+  if constexpr (BK == kCodes) {
+    const Source s = source(now.k0 + 2, now, next);
+    for_each<4>([&](auto Q) { issue(Int<0>{}, Int<4 + Q>{}, s); });
+    // Of 4, 4 and the codes' 4 loads, slot 0's first half of A has landed.
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 + Loads, 0));
+  } else {
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 + Loads, 15));
+  }
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
   read_a(Int<0>{}, Int<0>{}, Int<0>{});
@@ -428,6 +479,29 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   // No load may be in flight into LDS when the workgroup ends.
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
 #endif
+}
+
+// ---- host ---------------------------------------------------------------------
+inline int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
+inline int64_t units_of(int64_t K) { return (K + 2 * kStageK - 1) / (2 * kStageK); }
+
+inline TileArgs tile_args(Operand a, Operand b, int64_t m, int64_t n, int64_t K) {
+  TileArgs t{};
+  t.a = a;
+  t.b = b;
+  t.m = m;
+  t.n = n;
+  t.K = K;
+  t.tiles_m = (int)tiles_of(m);
+  t.tiles_n = (int)tiles_of(n);
+  t.units = (int)units_of(K);
+  t.full = t.tiles_m * t.tiles_n;
+  t.parts = 1;
+  return t;
+}
+inline dim3 tile_grid(const TileArgs& t) {
+  const int64_t items = (int64_t)t.full + (int64_t)t.split * t.parts, cus = compute_units();
+  return dim3((unsigned)(items < cus ? items : cus));
 }
 
 }  // namespace tiles

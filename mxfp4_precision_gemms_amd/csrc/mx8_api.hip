@@ -188,13 +188,89 @@ size_t act_back_bytes(int64_t m, int64_t N, int32_t gated) {
   return (size_t)act_backward_groups(m, gated ? N / 2 : N) * (size_t)N * sizeof(float);
 }
 
-// ---- cross entropy ------------------------------------------------------------
+// ---- gradients from MXFP8 -------------------------------------------------------
 constexpr int64_t kMaxTiled = int64_t{1} << 46;     // rows * columns of a product: 2^30 tiles
-constexpr int64_t kMaxTileRow = int64_t{1} << 22;   // elements of a row of bf16 (8 MB)
+constexpr int64_t kMaxTileRow = int64_t{1} << 23;   // bytes from an operand's row to the next
 
-// m * n, both below 2^30.
+// m * n, both at most 2^30.
 bool tiles_fit(int64_t m, int64_t n) { return m * n < kMaxTiled; }
 
+adahop_status act_back_mx8(const adahop_act_backward_mx8_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (a == nullptr) return invalid("act_backward_mx8: null arguments");
+  if (a->m < 0 || a->N < 1) return invalid("act_backward_mx8: m must be >= 0 and N >= 1");
+  if (a->m >= kMaxDim || a->N >= kMaxDim) return unsupported("act_backward_mx8: m or N of 2^30 or more");
+  if (!all_zero(a->reserved)) return invalid("act_backward_mx8: reserved fields must be 0");
+  if (a->act < ADAHOP_ACT_NONE || a->act > ADAHOP_ACT_GELU_TANH)
+    return invalid("act_backward_mx8: bad activation");
+  if (a->gated != 0 && a->gated != 1) return invalid("act_backward_mx8: gated must be 0 or 1");
+  if (a->N % 32 != 0) return invalid("act_backward_mx8: N is not a multiple of 32");
+  if (!valid_dtype(a->dout_dtype)) return invalid("act_backward_mx8: bad dtype");
+  const int64_t n = a->gated ? a->N / 2 : a->N;
+  if (a->ld_dout < n || a->ld_z_codes < a->N || a->ld_z_scales < a->N / 32 || a->ld_dz < a->N ||
+      (a->out != nullptr && a->ld_out < n))
+    return invalid("act_backward_mx8: leading dimension too small");
+  if (a->m > 0 && (!a->dout || !a->z_codes || !a->z_scales || !a->dz))
+    return invalid("act_backward_mx8: null dout, z or dz");
+  if (a->dbias != nullptr)
+    ADAHOP_TRY(need_workspace(ws, ws_bytes, act_back_bytes(a->m, a->N, a->gated), "act_backward_mx8"));
+  const Mx8Matrix z = {a->z_codes, a->ld_z_codes, a->z_scales, a->ld_z_scales};
+  return act_backward_mx8_launch(a->dout, a->dout_dtype, a->ld_dout, z, a->act, a->gated, a->m, n, a->dz, a->ld_dz,
+                                 a->out, a->ld_out, a->dbias, static_cast<float*>(ws), stream);
+}
+
+adahop_status norm_back_mx8(const adahop_rmsnorm_backward_mx8_args* a, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  if (a == nullptr) return invalid("rmsnorm_backward_mx8: null arguments");
+  ADAHOP_TRY(check_norm_sizes(a->rows, a->cols));
+  if (!all_zero(a->reserved)) return invalid("rmsnorm_backward_mx8: reserved fields must be 0");
+  if (a->cols % 32 != 0) return invalid("rmsnorm_backward_mx8: cols is not a multiple of 32");
+  if (!valid_dtype(a->dy_dtype) || !valid_dtype(a->dx_dtype) || !valid_dtype(a->gain_dtype))
+    return invalid("rmsnorm_backward_mx8: bad dtype");
+  if (a->ld_dy < a->cols || a->ld_h_codes < a->cols || a->ld_h_scales < a->cols / 32 || a->ld_dx < a->cols ||
+      (a->dh != nullptr && a->ld_dh < a->cols))
+    return invalid("rmsnorm_backward_mx8: leading dimension too small");
+  if (a->gain == nullptr) return invalid("rmsnorm_backward_mx8: null gain");
+  if (a->rows > 0 && (!a->dy || !a->h_codes || !a->h_scales || !a->rstd || !a->dx))
+    return invalid("rmsnorm_backward_mx8: null dy, h, rstd or dx");
+  if (a->rows == 0 && a->dgain == nullptr) return ADAHOP_OK;
+  if (a->dgain != nullptr)
+    ADAHOP_TRY(need_workspace(ws, ws_bytes, norm_back_bytes(a->rows, a->cols), "rmsnorm_backward_mx8"));
+  const Mx8Matrix h = {a->h_codes, a->ld_h_codes, a->h_scales, a->ld_h_scales};
+  return rmsnorm_backward_mx8_launch(a->dy, a->dy_dtype, a->ld_dy, h, a->gain, a->gain_dtype, a->rstd, a->dh,
+                                     a->ld_dh, a->rows, a->cols, a->dx, a->dx_dtype, a->ld_dx, a->dgain,
+                                     static_cast<float*>(ws), stream);
+}
+
+bool wgrad_mx8_fits(int64_t T, int64_t Din, int64_t Dout) {
+  return T < kMaxDim && Din < kMaxDim && Dout < kMaxDim && tiles_fit(Din, Dout);
+}
+size_t wgrad_mx8_bytes(int64_t T, int64_t Din, int64_t Dout) {
+  if (T < 0 || Din < 1 || Dout < 1 || !wgrad_mx8_fits(T, Din, Dout)) return 0;
+  return tile_product_bytes(Dout, Din, T);
+}
+
+adahop_status wgrad_mx8(const adahop_gemm_wgrad_mx8_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (a == nullptr) return invalid("gemm_wgrad_mx8: null arguments");
+  if (a->T < 0 || a->Din < 1 || a->Dout < 1) return invalid("gemm_wgrad_mx8: T must be >= 0, Din and Dout >= 1");
+  if (!wgrad_mx8_fits(a->T, a->Din, a->Dout))
+    return unsupported("gemm_wgrad_mx8: T, Din or Dout of 2^30 or more, or Din * Dout of 2^46 or more");
+  if (!all_zero(a->reserved)) return invalid("gemm_wgrad_mx8: reserved fields must be 0");
+  if (a->Din % 32 != 0) return invalid("gemm_wgrad_mx8: Din is not a multiple of 32");
+  if (!valid_dtype(a->out_dtype)) return invalid("gemm_wgrad_mx8: bad dtype");
+  if (a->ld_gy < a->Dout || a->ld_x_codes < a->Din || a->ld_x_scales < a->Din / 32 || a->ld_out < a->Din)
+    return invalid("gemm_wgrad_mx8: leading dimension too small");
+  if (!a->out || (a->T > 0 && (!a->gy || !a->x_codes || !a->x_scales)))
+    return invalid("gemm_wgrad_mx8: null GY, codes, scales or out");
+  if (a->Dout % 8 != 0 || a->ld_gy % 8 != 0 || a->ld_x_codes % 16 != 0 || !aligned16(a->gy) || !aligned16(a->x_codes))
+    return unsupported("gemm_wgrad_mx8: rows of GY and codes must be 16-byte aligned, Dout a multiple of 8");
+  if (2 * a->ld_gy >= kMaxTileRow || a->ld_x_codes >= kMaxTileRow || a->ld_x_scales >= kMaxTileRow)
+    return unsupported("gemm_wgrad_mx8: rows 8 MB or more apart");
+  ADAHOP_TRY(need_workspace(ws, ws_bytes, wgrad_mx8_bytes(a->T, a->Din, a->Dout), "gemm_wgrad_mx8"));
+  return wgrad_mx8_launch(a->gy, a->ld_gy, {a->x_codes, a->ld_x_codes, a->x_scales, a->ld_x_scales}, a->T, a->Din,
+                          a->Dout, a->out, a->out_dtype, a->ld_out, static_cast<float*>(ws), stream);
+}
+
+// ---- cross entropy ------------------------------------------------------------
 // What both calls ask of their common arguments.
 template <typename Args>
 adahop_status check_xent(const Args& a) {
@@ -208,7 +284,7 @@ adahop_status check_xent(const Args& a) {
   if (a.ld_h < a.dim || a.ld_w < a.dim) return invalid("xent: ld_h or ld_w below dim");
   if (a.dim % 8 != 0 || a.ld_h % 8 != 0 || a.ld_w % 8 != 0 || !aligned16(a.h) || !aligned16(a.w))
     return unsupported("xent: rows of h and w must be 16-byte aligned, dim a multiple of 8");
-  if (a.ld_h >= kMaxTileRow || a.ld_w >= kMaxTileRow) return unsupported("xent: rows 8 MB or more apart");
+  if (2 * a.ld_h >= kMaxTileRow || 2 * a.ld_w >= kMaxTileRow) return unsupported("xent: rows 8 MB or more apart");
   if (a.rows > 0 && (!a.h || !a.w || !a.targets)) return invalid("xent: null h, w or targets");
   return ADAHOP_OK;
 }
@@ -359,6 +435,25 @@ adahop_status adahop_act_backward(const void* dout, adahop_out_dtype dout_dtype,
     return act_backward_launch(dout, dout_dtype, z, act, gated, m, n, ld_dout, ld_z, dz, ld_dz, dbias,
                                static_cast<float*>(ws), static_cast<hipStream_t>(stream));
   });
+}
+
+adahop_status adahop_act_backward_mx8(const adahop_act_backward_mx8_args* args, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  return entry([&] { return act_back_mx8(args, ws, ws_bytes, static_cast<hipStream_t>(stream)); });
+}
+
+adahop_status adahop_rmsnorm_backward_mx8(const adahop_rmsnorm_backward_mx8_args* args, void* ws, size_t ws_bytes,
+                                          void* stream) {
+  return entry([&] { return norm_back_mx8(args, ws, ws_bytes, static_cast<hipStream_t>(stream)); });
+}
+
+size_t adahop_gemm_wgrad_mx8_workspace_size(int64_t T, int64_t Din, int64_t Dout) {
+  return wgrad_mx8_bytes(T, Din, Dout);
+}
+
+adahop_status adahop_gemm_wgrad_mx8(const adahop_gemm_wgrad_mx8_args* args, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  return entry([&] { return wgrad_mx8(args, ws, ws_bytes, static_cast<hipStream_t>(stream)); });
 }
 
 size_t adahop_xent_workspace_size(int64_t rows, int64_t vocab) { return xent_bytes(rows, vocab); }

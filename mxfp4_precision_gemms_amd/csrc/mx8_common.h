@@ -241,6 +241,22 @@ struct Raw8 {
   }
 };
 
+// Codes c .. c + 7 of an MXFP8 row and their block's scale, loaded long before
+// their use; c and cols are multiples of 8, and past the row's end the last
+// group is read. `first`: the row's first column counted from a multiple of 32.
+struct RawMx8 {
+  u32x2 w;
+  uint8_t byte;
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t first, int64_t c,
+                                       int64_t cols) {
+    const int64_t at = first + (c < cols ? c : cols - 8);
+    __builtin_memcpy(&w, codes + at, 8);
+    byte = scales[at / 32];
+  }
+  // The values, 0 past the end of the row.
+  __device__ __forceinline__ void get(float (&v)[8], int64_t c, int64_t cols) const;
+};
+
 // Whether every row of a matrix starts at a cache line.
 inline bool line_aligned(const void* p, int64_t ld, int f32) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (f32 ? 4 : 2))) & 127u) == 0;
@@ -302,6 +318,22 @@ __device__ __forceinline__ float mx8_inverse(uint32_t byte) {
 __device__ __forceinline__ float mx8_scale(uint32_t byte) {
   const uint32_t b = byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23;
   return __builtin_bit_cast(float, b);
+}
+// 8 codes' values under the scale s.
+__device__ __forceinline__ void mx8_unpack8(u32x2 w, float s, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
+    v[4 * j] = lo[0] * s;
+    v[4 * j + 1] = lo[1] * s;
+    v[4 * j + 2] = hi[0] * s;
+    v[4 * j + 3] = hi[1] * s;
+  }
+}
+__device__ __forceinline__ void RawMx8::get(float (&v)[8], int64_t c, int64_t cols) const {
+  const bool in = c < cols;
+  mx8_unpack8(in ? w : u32x2{0, 0}, in ? mx8_scale(byte) : 0.0f, v);
 }
 // Four E4M3 codes of v / 2^e, nearest even (hardware conversion; the scaled
 // magnitudes are at most 448). A block with byte 255 gets NaN codes.

@@ -7,6 +7,8 @@
 // once, with a row's values held in registers between the sum of squares and
 // the scaling. Sums run in fp32 along fixed trees: results do not change from
 // run to run.
+#include <type_traits>
+
 #include "adahop_internal.h"
 #include "launch_shapes.h"
 #include "mx8_common.h"
@@ -111,7 +113,9 @@ __global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
 // ---- backward ---------------------------------------------------------------
 struct NormBackArgs {
   const void* dy;
-  const void* h;
+  const void* h;           // or codes, rows ldh bytes apart
+  const uint8_t* scales;   // of h's codes
+  int64_t ldhs;
   const void* gain;
   int gain_f32;
   const float* rstd;
@@ -129,8 +133,9 @@ struct NormBackArgs {
 // 16 waves a compute unit fit, each with its next row's loads in flight
 // (16384 x 2048 in bf16 with dh: 45 .. 48 us, 5.6 .. 5.9 TB/s; a wave a row
 // without loads ahead 76).
-// Once: every row starts at a cache line.
-template <bool DyF32, bool HF32, bool Once, int Waves, int NV>
+// Once: every row starts at a cache line. Kept: h is kept in MXFP8, dx and dh are
+// of HF32's type.
+template <bool DyF32, bool HF32, bool Kept, bool Once, int Waves, int NV>
 __global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
     rmsnorm_backward_kernel(NormBackArgs a) {
   using TD = typename Elem<DyF32>::type;
@@ -143,19 +148,22 @@ __global__ void __launch_bounds__(Waves == 1 ? 256 : 64 * Waves)
   const int t = Waves == 1 ? threadIdx.x & 63 : threadIdx.x;
   struct Row {
     Raw8<DyF32> dy[NV];
-    Raw8<HF32> h[NV], dh[NV];
+    std::conditional_t<Kept, RawMx8, Raw8<HF32>> h[NV];
+    Raw8<HF32> dh[NV];
     float s;
   };
   const int64_t step = (int64_t)gridDim.x * RowsPer;
   auto load = [&](Row& r, int64_t row) {
     const TD* dy = static_cast<const TD*>(a.dy) + row * a.lddy;
-    const TH* h = static_cast<const TH*>(a.h) + row * a.ldh;
     r.s = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int64_t c = 8 * (int64_t)(t + k * T);
       r.dy[k].template load<Once>(dy, c, a.cols);
-      r.h[k].template load<Once>(h, c, a.cols);
+      if constexpr (Kept)
+        r.h[k].load(static_cast<const uint8_t*>(a.h) + row * a.ldh, a.scales + row * a.ldhs, 0, c, a.cols);
+      else
+        r.h[k].template load<Once>(static_cast<const TH*>(a.h) + row * a.ldh, c, a.cols);
       if (a.dh != nullptr) r.dh[k].template load<Once>(static_cast<const TH*>(a.dh) + row * a.lddh, c, a.cols);
     }
   };
@@ -312,17 +320,8 @@ __global__ void __launch_bounds__(256) mx8_dequant_kernel(Mx8Args a) {
     group_at(i, a.rows, a.cols, &r, &c);
     u32x2 w;
     __builtin_memcpy(&w, a.codes + r * a.ldc + c, 8);
-    const float s = mx8_scale(a.scales[r * a.lds + c / 32]);
     float v[8];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
-      const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
-      v[4 * j] = lo[0] * s;
-      v[4 * j + 1] = lo[1] * s;
-      v[4 * j + 2] = hi[0] * s;
-      v[4 * j + 3] = hi[1] * s;
-    }
+    mx8_unpack8(w, mx8_scale(a.scales[r * a.lds + c / 32]), v);
     Elem<F32>::store8(static_cast<TD*>(a.dst) + r * a.ldd + c, v);
   }
 }
@@ -359,11 +358,11 @@ int norm_back_waves(int64_t cols) {
   return w;
 }
 
-template <bool DyF32, bool HF32, bool Once>
+template <bool DyF32, bool HF32, bool Kept, bool Once>
 adahop_status norm_back_dispatch(const NormBackArgs& a, int grid, hipStream_t stream) {
   const int64_t c = a.cols;
 #define ADAHOP_NORM_BACK(WAVES, NV)                                                              \
-  rmsnorm_backward_kernel<DyF32, HF32, Once, WAVES, NV>                                                \
+  rmsnorm_backward_kernel<DyF32, HF32, Kept, Once, WAVES, NV>                                          \
       <<<dim3((unsigned)grid), dim3(WAVES == 1 ? 256 : 64 * WAVES), 0, stream>>>(a)
   switch (norm_back_waves(c)) {
     case 1: ADAHOP_NORM_BACK(1, 1); break;
@@ -414,26 +413,44 @@ int rmsnorm_backward_groups(int64_t rows, int64_t cols) {
   return (int)(need < 1 ? 1 : need < most ? need : most);
 }
 
+namespace {
+template <bool Kept>
+adahop_status norm_back_run(const NormBackArgs& a, int dy_f32, int h_f32, bool once, float* dgain,
+                            hipStream_t stream) {
+  const int grid = rmsnorm_backward_groups(a.rows, a.cols);
+  adahop_status st;
+#define ADAHOP_NORM_TYPES(ONCE)                                                                        \
+  (dy_f32 ? (h_f32 ? norm_back_dispatch<true, true, Kept, ONCE>(a, grid, stream)                       \
+                   : norm_back_dispatch<true, false, Kept, ONCE>(a, grid, stream))                     \
+          : (h_f32 ? norm_back_dispatch<false, true, Kept, ONCE>(a, grid, stream)                      \
+                   : norm_back_dispatch<false, false, Kept, ONCE>(a, grid, stream)))
+  st = once ? ADAHOP_NORM_TYPES(true) : ADAHOP_NORM_TYPES(false);
+#undef ADAHOP_NORM_TYPES
+  if (st != ADAHOP_OK || dgain == nullptr) return st;
+  return column_reduce_launch(a.partial, grid, a.cols, dgain, stream);
+}
+}  // namespace
+
 adahop_status rmsnorm_backward_launch(const void* dy, int dy_f32, const void* h, int h_f32,
                                       const void* gain, int gain_f32, const float* rstd,
                                       const void* dh, int64_t rows, int64_t cols, int64_t lddy,
                                       int64_t ldh, int64_t lddh, int64_t lddx, void* dx,
                                       float* dgain, float* partial, hipStream_t stream) {
-  const int grid = rmsnorm_backward_groups(rows, cols);
   const bool once = line_aligned(dy, lddy, dy_f32) && line_aligned(h, ldh, h_f32) &&
                     (dh == nullptr || line_aligned(dh, lddh, h_f32));
-  const NormBackArgs a = {dy, h, gain, gain_f32, rstd, dh, rows, cols, lddy, ldh, lddh, lddx, dx,
+  const NormBackArgs a = {dy, h, nullptr, 0, gain, gain_f32, rstd, dh, rows, cols, lddy, ldh, lddh, lddx, dx,
                           dgain != nullptr ? partial : nullptr};
-  adahop_status st;
-#define ADAHOP_NORM_TYPES(ONCE)                                                                        \
-  (dy_f32 ? (h_f32 ? norm_back_dispatch<true, true, ONCE>(a, grid, stream)                             \
-                   : norm_back_dispatch<true, false, ONCE>(a, grid, stream))                           \
-          : (h_f32 ? norm_back_dispatch<false, true, ONCE>(a, grid, stream)                            \
-                   : norm_back_dispatch<false, false, ONCE>(a, grid, stream)))
-  st = once ? ADAHOP_NORM_TYPES(true) : ADAHOP_NORM_TYPES(false);
-#undef ADAHOP_NORM_TYPES
-  if (st != ADAHOP_OK || dgain == nullptr) return st;
-  return column_reduce_launch(partial, grid, cols, dgain, stream);
+  return norm_back_run<false>(a, dy_f32, h_f32, once, dgain, stream);
+}
+
+adahop_status rmsnorm_backward_mx8_launch(const void* dy, int dy_f32, int64_t lddy, const Mx8Matrix& h,
+                                          const void* gain, int gain_f32, const float* rstd, const void* dh,
+                                          int64_t lddh, int64_t rows, int64_t cols, void* dx, int dx_f32,
+                                          int64_t lddx, float* dgain, float* partial, hipStream_t stream) {
+  const bool once = line_aligned(dy, lddy, dy_f32) && (dh == nullptr || line_aligned(dh, lddh, dx_f32));
+  const NormBackArgs a = {dy, h.codes, h.scales, h.lds, gain, gain_f32, rstd, dh, rows, cols, lddy, h.ldc, lddh,
+                          lddx, dx, dgain != nullptr ? partial : nullptr};
+  return norm_back_run<true>(a, dy_f32, dx_f32, once, dgain, stream);
 }
 
 adahop_status column_reduce_launch(const float* partial, int parts, int64_t cols, float* out,

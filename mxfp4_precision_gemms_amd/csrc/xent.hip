@@ -43,47 +43,6 @@ struct Targets {
 };
 
 // ---- epilogues ----------------------------------------------------------------
-// A product as it stands: to bf16 or fp32, on top of `prev` if given. n is a
-// multiple of 8, so 4 columns are inside or outside together.
-struct StoreEpi {
-  void* out;
-  int64_t ld;
-  int f32;
-  const float* prev;         // [m][ld_prev], or null
-  int64_t ld_prev;
-  template <bool Wide>
-  __device__ __forceinline__ void store(v4f (&acc)[8][4], const Spot& at, int64_t m, int64_t n) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = at.row0 + 16 * i;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int step = (Wide ? 4 : 16) * j;
-        if (at.to != nullptr) {
-          *reinterpret_cast<v4f*>(at.to + (at.lrow + 16 * i) * kTile + at.lcol + step) = acc[i][j];
-          continue;
-        }
-        const int64_t c = at.col0 + step;
-        if (r >= m || c >= n) continue;
-        v4f v = acc[i][j];
-        if (prev != nullptr) {
-          v4f p;
-          __builtin_memcpy(&p, prev + r * ld_prev + c, 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += p[e];
-        }
-        if (f32) {
-          __builtin_memcpy(static_cast<float*>(out) + r * ld + c, &v, 16);
-        } else {
-          const mx8::u32x2 w = {f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3])};
-          __builtin_memcpy(static_cast<uint16_t*>(out) + r * ld + c, &w, 8);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-};
-
 // The logits' maximum and sum over the wave's 64 columns of each row, and the
 // target's logit.
 struct StatsEpi {
@@ -216,101 +175,9 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(FinishArgs a) {
   }
 }
 
-// Adds the parts of the split tiles in order and stores them. Workgroup b takes
-// rows 16 (b % 16) .. +15 of split tile b / 16.
-__global__ void __launch_bounds__(256) tile_join_kernel(TileArgs t, StoreEpi epi) {
-  const int tile = blockIdx.x >> 4, band = blockIdx.x & 15;
-  int tm, tn;
-  tile_at(t.full + tile, t.tiles_m, t.tiles_n, &tm, &tn);
-  const int lc = 4 * (threadIdx.x & 63);
-  const int64_t c = (int64_t)tn * kTile + lc;
-  const float* first = t.split_ws + (int64_t)tile * t.parts * (kTile * kTile);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int lr = 16 * band + (threadIdx.x >> 6) + 4 * i;
-    const int64_t r = (int64_t)tm * kTile + lr;
-    if (r >= t.m || c >= t.n) continue;
-    v4f v = *reinterpret_cast<const v4f*>(first + lr * kTile + lc);
-    for (int p = 1; p < t.parts; ++p) {
-      const v4f b = *reinterpret_cast<const v4f*>(first + (int64_t)p * (kTile * kTile) + lr * kTile + lc);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += b[e];
-    }
-    if (epi.prev != nullptr) {
-      v4f b;
-      __builtin_memcpy(&b, epi.prev + r * epi.ld_prev + c, 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += b[e];
-    }
-    if (epi.f32) {
-      __builtin_memcpy(static_cast<float*>(epi.out) + r * epi.ld + c, &v, 16);
-    } else {
-      const mx8::u32x2 w = {f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3])};
-      __builtin_memcpy(static_cast<uint16_t*>(epi.out) + r * epi.ld + c, &w, 8);
-    }
-  }
-}
-
 // ---- host ---------------------------------------------------------------------
-int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
-int64_t units_of(int64_t K) { return (K + 2 * kStageK - 1) / (2 * kStageK); }
-
-// The last round of tiles split along K where it leaves half of the compute
-// units or more without one (a part: at least 4 pairs of stages).
-struct Split {
-  int64_t full, split;
-  int parts;
-};
-Split split_of(int64_t m, int64_t n, int64_t K) {
-  const int64_t all = tiles_of(m) * tiles_of(n), cus = compute_units(), rem = all % cus;
-  int64_t parts = rem > 0 ? cus / rem : 1;
-  if (parts > units_of(K) / 4) parts = units_of(K) / 4;
-  if (parts > 32) parts = 32;
-  if (parts < 2) return {all, 0, 1};
-  return {all - rem, rem, (int)parts};
-}
-size_t split_bytes(int64_t m, int64_t n, int64_t K) {
-  const Split s = split_of(m, n, K);
-  return s.split ? (size_t)s.split * s.parts * kTile * kTile * sizeof(float) : 0;
-}
-
-TileArgs tile_args(Operand a, Operand b, int64_t m, int64_t n, int64_t K) {
-  TileArgs t{};
-  t.a = a;
-  t.b = b;
-  t.m = m;
-  t.n = n;
-  t.K = K;
-  t.tiles_m = (int)tiles_of(m);
-  t.tiles_n = (int)tiles_of(n);
-  t.units = (int)units_of(K);
-  t.full = t.tiles_m * t.tiles_n;
-  t.parts = 1;
-  return t;
-}
-dim3 tile_grid(const TileArgs& t) {
-  const int64_t items = (int64_t)t.full + (int64_t)t.split * t.parts, cus = compute_units();
-  return dim3((unsigned)(items < cus ? items : cus));
-}
-
-// One product of the gradient: whole tiles, split ones, and their join.
-template <Kind AK>
-adahop_status product(Operand a, Operand b, int64_t m, int64_t n, int64_t K, const StoreEpi& epi, float* ws,
-                      hipStream_t stream) {
-  TileArgs t = tile_args(a, b, m, n, K);
-  const Split s = split_of(m, n, K);
-  t.full = (int)s.full;
-  t.split = (int)s.split;
-  t.parts = s.parts;
-  t.split_ws = ws;
-  bf16_tile_kernel<AK, kAcross, StoreEpi><<<tile_grid(t), dim3(kThreads), 0, stream>>>(t, epi);
-  adahop_status st = check_launch("xent_backward product");
-  if (st != ADAHOP_OK || t.split == 0) return st;
-  tile_join_kernel<<<dim3((unsigned)(16 * t.split)), dim3(256), 0, stream>>>(t, epi);
-  return check_launch("xent_backward join");
-}
-
-Operand along(const uint16_t* p, int64_t ld) { return {reinterpret_cast<const uint8_t*>(p), 2 * ld}; }
+Operand along(const uint16_t* p, int64_t ld) { return {reinterpret_cast<const uint8_t*>(p), 2 * ld, nullptr, 0}; }
+TileOperand operand(const uint16_t* p, int64_t ld, Kind kind) { return {p, 2 * ld, nullptr, 0, kind}; }
 
 }  // namespace
 
@@ -365,7 +232,7 @@ BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, 
   const int64_t last = V - (l.p.count - 1) * l.p.size;
   size_t split = 0;
   for (const int64_t n : {l.p.size < V ? l.p.size : V, last}) {
-    const size_t s = dh ? split_bytes(T, D, n) : 0, u = dw ? split_bytes(n, D, T) : 0;
+    const size_t s = dh ? tile_product_bytes(T, D, n) : 0, u = dw ? tile_product_bytes(n, D, T) : 0;
     split = split > s ? split : s;
     split = split > u ? split : u;
   }
@@ -373,14 +240,6 @@ BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, 
   return l;
 }
 
-__global__ void __launch_bounds__(256) zero_rows_kernel(void* out, int64_t rows, int64_t cols, int64_t ld, int f32) {
-  const int64_t n = rows * cols;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / cols, c = i - r * cols;
-    if (f32) static_cast<float*>(out)[r * ld + c] = 0.0f;
-    else static_cast<uint16_t*>(out)[r * ld + c] = 0;
-  }
-}
 }  // namespace
 
 size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, bool dw) {
@@ -391,8 +250,10 @@ adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t
                                    hipStream_t stream) {
   if (a.T == 0) {
     if (b.dw == nullptr) return ADAHOP_OK;
-    zero_rows_kernel<<<dim3(2048), dim3(256), 0, stream>>>(b.dw, a.V, a.D, b.lddw, b.dw_f32);
-    return check_launch("xent_backward");
+    // A product over no rows: zeros.
+    const TileOut to = {b.dw, b.lddw, b.dw_f32, nullptr, 0};
+    return tile_product_launch(operand(nullptr, 8, kAcross), operand(nullptr, 8, kAcross), a.V, a.D, 0, to, nullptr,
+                               stream);
   }
   const BackLayout l = back_layout(a.T, a.V, a.D, piece, b.dh != nullptr, b.dw != nullptr);
   uint16_t* g = static_cast<uint16_t*>(ws);
@@ -401,21 +262,23 @@ adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t
   const Targets y = {a.targets, a.wide_targets};
   for (int64_t q = 0; q < l.p.count; ++q) {
     const int64_t v0 = q * l.p.size, n = a.V - v0 < l.p.size ? a.V - v0 : l.p.size;
-    const Operand h = along(a.h, a.ldh), w = along(a.w + v0 * a.ldw, a.ldw), og = along(g, l.p.size);
-    const TileArgs t = tile_args(h, w, a.T, n, a.D);
+    const uint16_t* w = a.w + v0 * a.ldw;
+    const TileArgs t = tile_args(along(a.h, a.ldh), along(w, a.ldw), a.T, n, a.D);
     const GradEpi epi = {a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, l.p.size};
     bf16_tile_kernel<kAlong, kAlong, GradEpi><<<tile_grid(t), dim3(kThreads), 0, stream>>>(t, epi);
     adahop_status st = check_launch("xent_backward logits");
     if (st != ADAHOP_OK) return st;
     if (b.dh != nullptr) {
       const bool last = q + 1 == l.p.count;
-      const StoreEpi to = {last ? b.dh : sum, last ? b.lddh : a.D, last ? b.dh_f32 : 1, q > 0 ? sum : nullptr, a.D};
-      st = product<kAlong>(og, w, a.T, a.D, n, to, split, stream);
+      const TileOut to = {last ? b.dh : sum, last ? b.lddh : a.D, last ? b.dh_f32 : 1, q > 0 ? sum : nullptr, a.D};
+      st = tile_product_launch(operand(g, l.p.size, kAlong), operand(w, a.ldw, kAcross), a.T, a.D, n, to, split,
+                               stream);
       if (st != ADAHOP_OK) return st;
     }
     if (b.dw != nullptr) {
-      const StoreEpi to = {static_cast<char*>(b.dw) + (b.dw_f32 ? 4 : 2) * v0 * b.lddw, b.lddw, b.dw_f32, nullptr, 0};
-      st = product<kAcross>(og, h, n, a.D, a.T, to, split, stream);
+      const TileOut to = {static_cast<char*>(b.dw) + (b.dw_f32 ? 4 : 2) * v0 * b.lddw, b.lddw, b.dw_f32, nullptr, 0};
+      st = tile_product_launch(operand(g, l.p.size, kAcross), operand(a.h, a.ldh, kAcross), n, a.D, a.T, to, split,
+                               stream);
       if (st != ADAHOP_OK) return st;
     }
   }

@@ -269,7 +269,7 @@ adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, bool e
 // aligned; K of an A along it may end inside 16 bytes if what follows in them is
 // finite; n a multiple of 8 (codes: 32), m of an A across it likewise, or A's
 // rows reach to the next multiple; m, n, K below 2^30, m * n below 2^46. ws:
-// tile_product_bytes(m, n, K) bytes.
+// tile_product_bytes(...) bytes.
 struct TileOperand {
   const void* p;
   int64_t ld;
@@ -284,12 +284,13 @@ struct TileOut {
   const float* prev;
   int64_t ld_prev;
 };
-size_t tile_product_bytes(int64_t m, int64_t n, int64_t K);
+// along: whether A lies along K.
+size_t tile_product_bytes(int64_t m, int64_t n, int64_t K, bool along);
 adahop_status tile_product_launch(const TileOperand& a, const TileOperand& b, int64_t m, int64_t n, int64_t K,
                                   const TileOut& out, float* ws, hipStream_t stream);
 
 // dW [Dout, Din] = GY^T X from X in MXFP8, checked; ws: tile_product_bytes(Dout,
-// Din, T) bytes.
+// Din, T, false) bytes.
 adahop_status wgrad_mx8_launch(const uint16_t* gy, int64_t ldgy, const Mx8Matrix& x, int64_t T, int64_t Din,
                                int64_t Dout, void* out, int out_f32, int64_t ldo, float* ws, hipStream_t stream);
 

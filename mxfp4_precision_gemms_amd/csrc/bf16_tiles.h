@@ -33,6 +33,7 @@
 
 #include "adahop_internal.h"
 #include "mx8_common.h"
+#include "tile_plan.h"
 
 namespace adahop {
 namespace tiles {
@@ -67,9 +68,10 @@ constexpr int kBufferFlags = 0x00020000;   // raw buffer descriptor word 3
 constexpr int kPastEnd = 0x7FFFFFF0;
 constexpr int64_t kMaxRowBytes = int64_t{1} << 23;
 
-constexpr int kTile = 256;                 // rows and columns of a tile
+constexpr int kTile = 256;                 // rows and columns of a large tile
 constexpr int kStageK = 64;                // K elements of a stage
 constexpr int kThreads = 512;
+constexpr int kRingCols = 128;             // columns of a small tile
 constexpr int kGroupM = 4;                 // tile rows that run together on one XCD
 
 // How an operand lies: along K, across it, or across it in MXFP8 (B alone).
@@ -86,9 +88,10 @@ struct TileArgs {
   Operand a, b;
   int64_t m, n, K;
   int tiles_m, tiles_n;
+  int bm, bn;                // rows and columns of a tile
   int units;                 // pairs of stages of K
   // Items 0 .. full - 1 are whole tiles; those after them each one of `parts`
-  // parts of K of a tile, whose sums go to split_ws ([tile][part][256][256]).
+  // parts of K of a tile, whose sums go to split_ws ([tile][part][bm][bn]).
   int full, split, parts;
   float* split_ws;
 };
@@ -113,11 +116,65 @@ __device__ __forceinline__ void tile_at(int pos, int tiles_m, int tiles_n, int* 
 // row0 + 16 i, column col0 + (BK == kAlong ? 4 j : 16 j) + e.
 struct Spot {
   int64_t row0, col0;
-  int tn, wn;                // tile column, wave column
-  int part;                  // < 0: a whole tile
-  float* to;                 // of a part: its 256 x 256 sums
-  int lrow, lcol;            // row and column in the tile
+  int64_t group;             // the wave's columns start at 64 group
+  float* to;                 // a part's sums [bm][bn]; null: a whole tile
+  int lrow, lcol, bn;        // row and column in the tile
 };
+
+// Bytes of the 16-byte chunks that hold n elements.
+__device__ __forceinline__ int64_t chunks(int64_t n) { return 2 * ((n + 7) & ~(int64_t)7); }
+// A stage's rows of an operand: the descriptor starts at its first byte and ends
+// with its last, so that rows and K-rows past the ends read as 0. p: the tile's
+// first byte at k = 0; bytes: from there to the end of the tile's rows (across
+// K: of one K-row); left: elements of K from the stage's first.
+template <Kind K>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t source_of(const uint8_t* p, int bytes, int64_t ld, int k, int left) {
+  if constexpr (K == kAlong) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + (int64_t)128 * k), 0,
+                                             left > 0 ? bytes - 128 * k : 0, kBufferFlags);
+  } else {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + (int64_t)kStageK * k * ld), 0,
+                                             left > 0 ? (left - 1) * (int)ld + bytes : 0, kBufferFlags);
+  }
+}
+// Elements of K from stage k's first, at most a stage.
+__device__ __forceinline__ int left_at(int64_t K, int k) {
+  const int64_t rest = K - (int64_t)kStageK * k;
+  return (int)(rest < 0 ? 0 : rest < kStageK ? rest : kStageK);
+}
+// First byte of a tile's rows r0 .. and their extent, as source_of takes them.
+template <Kind K>
+__device__ __forceinline__ const uint8_t* tile_base(const Operand& o, int64_t r0) {
+  return K == kAlong ? o.p + r0 * o.ld : o.p + (K == kCodes ? 1 : 2) * r0;
+}
+template <Kind K>
+__device__ __forceinline__ int tile_bytes(const Operand& o, int64_t rows, int64_t depth) {
+  if constexpr (K == kAlong) return (int)((rows - 1) * o.ld + chunks(depth));
+  else return (int)(K == kCodes ? rows : chunks(rows));
+}
+// 16 K-rows' elements of a lane's column, transposed on their way from LDS: two
+// runs of four K-rows, `next` bytes apart.
+__device__ __forceinline__ v4i read_across(const uint8_t* p, int next) {
+  const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s16*)p));
+  const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s16*)(p + next)));
+  return v4i{lo[0], lo[1], hi[0], hi[1]};
+}
+// 16 codes under one scale as 16 bf16 (exact; below 2^-126 possibly 0).
+__device__ __forceinline__ void widen16(const v4i& codes, uint8_t scale, v4i* to) {
+  const float by = mx8::mx8_scale(scale);
+  v4i w[2];
+  for_each<4>([&](auto D) {
+    constexpr int d = decltype(D)::value;
+    const uint32_t four = (uint32_t)codes[d];
+    w[d / 2][2 * (d % 2)] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, by, false));
+    w[d / 2][2 * (d % 2) + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, by, true));
+  });
+  to[0] = w[0];
+  to[1] = w[1];
+}
+__device__ __forceinline__ v4f product16(const v4i& b, const v4i& a, const v4f& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, b), __builtin_bit_cast(v8bf, a), c, 0, 0, 0);
+}
 
 struct Half {
   uint8_t a[128 * 128];
@@ -159,9 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     const int cnt = items - base < G ? items - base : G;
     return (int)blockIdx.x < cnt ? base + xcd_band(blockIdx.x, cnt) : -1;
   };
-  // An item's place, all scalar. Stages k0 .. k1 - 1, an even number; a / b: the
-  // tile's first byte at k = 0, a_bytes / b_bytes: bytes from there to the end
-  // of the tile's rows (across K: of one K-row).
+  // An item's place, all scalar. Stages k0 .. k1 - 1, an even number.
   struct Place {
     int tm, tn, k0, k1, part, split_tile;
     const uint8_t* a;
@@ -169,8 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     const uint8_t* scales;
     int a_bytes, b_bytes;
   };
-  // Bytes of the 16-byte chunks that hold n elements.
-  auto chunks = [](int64_t n) { return 2 * ((n + 7) & ~(int64_t)7); };
   auto place = [&](int item) {
     // Without an item: a stage past the end of any K.
     Place p{0, 0, 1 << 28, 1 << 28, -1, 0, t.a.p, t.b.p, t.b.scales, 0, 0};
@@ -194,62 +247,32 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       p.k1 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)t.units * (p.part + 1) / t.parts));
     }
     const int64_t m0 = (int64_t)p.tm * kTile, n0 = (int64_t)p.tn * kTile;
-    if constexpr (AK == kAlong) {
-      const int64_t rows = t.m - m0 < kTile ? t.m - m0 : kTile;
-      p.a = t.a.p + m0 * t.a.ld;
-      p.a_bytes = (int)((rows - 1) * t.a.ld + chunks(t.K));
-    } else {
-      p.a = t.a.p + 2 * m0;
-      p.a_bytes = (int)chunks(t.m - m0 < kTile ? t.m - m0 : kTile);
-    }
-    if constexpr (BK == kAlong) {
-      const int64_t rows = t.n - n0 < kTile ? t.n - n0 : kTile;
-      p.b = t.b.p + n0 * t.b.ld;
-      p.b_bytes = (int)((rows - 1) * t.b.ld + chunks(t.K));
-    } else if constexpr (BK == kAcross) {
-      p.b = t.b.p + 2 * n0;
-      p.b_bytes = (int)chunks(t.n - n0 < kTile ? t.n - n0 : kTile);
-    } else {
-      p.b = t.b.p + n0;
-      p.scales = t.b.scales + n0 / 32;
-      p.b_bytes = (int)(t.n - n0 < kTile ? t.n - n0 : kTile);   // a multiple of 32
-    }
+    p.a = tile_base<AK>(t.a, m0);
+    p.b = tile_base<BK>(t.b, n0);
+    p.a_bytes = tile_bytes<AK>(t.a, t.m - m0 < kTile ? t.m - m0 : kTile, t.K);
+    p.b_bytes = tile_bytes<BK>(t.b, t.n - n0 < kTile ? t.n - n0 : kTile, t.K);
+    if constexpr (BK == kCodes) p.scales = t.b.scales + n0 / 32;
     return p;
   };
 
   // ---- loads: this wave's share of a stage ------------------------------------
-  // The descriptor starts at stage k's first byte and ends with its last, so
-  // that rows and K-rows past the ends read as 0. `left`: elements of K from
-  // the stage's first.
   struct Source {
     __amdgpu_buffer_rsrc_t a, b, scales;
     int left;
-  };
-  auto source_of = [&](Kind kind, const uint8_t* p, int bytes, int64_t ld, int k, int left) {
-    if (kind == kAlong) {
-      const int64_t at = (int64_t)128 * k;
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + at), 0,
-                                               left > 0 ? bytes - 128 * k : 0, kBufferFlags);
-    }
-    const int rows = left < kStageK ? left : kStageK;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + (int64_t)kStageK * k * ld), 0,
-                                             rows > 0 ? (rows - 1) * (int)ld + bytes : 0, kBufferFlags);
   };
   // Stage k of item `now`, or, past its last, of item `next`: the scalar
   // selects keep the stages free of branches.
   auto source = [&](int k, const Place& now, const Place& next) __attribute__((always_inline)) {
     const bool in = k < now.k1;
     const int at = in ? k : k - now.k1 + next.k0;
-    const int64_t rest = t.K - (int64_t)kStageK * at;
-    const int left = (int)(rest < 0 ? 0 : rest < kStageK ? rest : kStageK);
-    const int kk = left > 0 ? at : 0;
     Source s;
-    s.left = left;
-    s.a = source_of(AK, in ? now.a : next.a, in ? now.a_bytes : next.a_bytes, t.a.ld, kk, left);
-    s.b = source_of(BK, in ? now.b : next.b, in ? now.b_bytes : next.b_bytes, t.b.ld, kk, left);
+    s.left = left_at(t.K, at);
+    const int kk = s.left > 0 ? at : 0;
+    s.a = source_of<AK>(in ? now.a : next.a, in ? now.a_bytes : next.a_bytes, t.a.ld, kk, s.left);
+    s.b = source_of<BK>(in ? now.b : next.b, in ? now.b_bytes : next.b_bytes, t.b.ld, kk, s.left);
     if constexpr (BK == kCodes)
-      s.scales = source_of(BK, in ? now.scales : next.scales, (in ? now.b_bytes : next.b_bytes) / 32, t.b.ld_scales,
-                           kk, left);
+      s.scales = source_of<BK>(in ? now.scales : next.scales, (in ? now.b_bytes : next.b_bytes) / 32, t.b.ld_scales,
+                               kk, s.left);
     return s;
   };
   // Along K, load q of this wave fills rows 64 q + 8 wave + lane / 8 with chunks
@@ -273,19 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   const int oc = kc * 512 + 32 * (gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1)));
   auto widen = [&](auto I) __attribute__((always_inline)) {
     for_each<2>([&](auto U) {
-      const float by = mx8::mx8_scale(scale[U]);
-      v4i w[2];
-      for_each<4>([&](auto D) {
-        constexpr int d = decltype(D)::value;
-        const int four = codes[U][d];
-        const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)four, by, false);
-        const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)four, by, true);
-        w[d / 2][2 * (d % 2)] = __builtin_bit_cast(int, lo);
-        w[d / 2][2 * (d % 2) + 1] = __builtin_bit_cast(int, hi);
-      });
-      v4i* to = reinterpret_cast<v4i*>(wide(I).b + oc + 16384 * decltype(U)::value);
-      to[0] = w[0];
-      to[1] = w[1];
+      constexpr int u = decltype(U)::value;
+      widen16(codes[u], scale[u], reinterpret_cast<v4i*>(wide(I).b + oc + 16384 * u));
     });
   };
   // Across K, a row's last bytes are followed by the next row's: columns past
@@ -331,11 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   }
   v4f acc[8][4];
   v4i A[4][2], B[4][2];
-  auto tr = [](const uint8_t* p, int next) __attribute__((always_inline)) {
-    const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s16*)p));
-    const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s16*)(p + next)));
-    return v4i{lo[0], lo[1], hi[0], hi[1]};
-  };
   auto read_a = [&](auto I, auto Buf, auto R) __attribute__((always_inline)) {
     constexpr int b = decltype(Buf)::value, i = decltype(R)::value;
     const uint8_t* p = half(I, Int<i / 4>{}).a;
@@ -343,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       A[b][0] = *reinterpret_cast<const v4i*>(p + 2048 * (i % 4) + fa);
       A[b][1] = *reinterpret_cast<const v4i*>(p + 2048 * (i % 4) + (fa ^ 64));
     } else {
-      A[b][0] = tr(p + xa[i % 4], 1024);
-      A[b][1] = tr(p + xa[i % 4] + 8192, 1024);
+      A[b][0] = read_across(p + xa[i % 4], 1024);
+      A[b][1] = read_across(p + xa[i % 4] + 8192, 1024);
     }
   };
   auto read_b = [&](auto I, auto J) __attribute__((always_inline)) {
@@ -354,14 +361,13 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       B[j][0] = *reinterpret_cast<const v4i*>(p + 512 * j + fb);
       B[j][1] = *reinterpret_cast<const v4i*>(p + 512 * j + (fb ^ 64));
     } else {
-      B[j][0] = tr(p + xb[j], 2048);
-      B[j][1] = tr(p + xb[j] + 16384, 2048);
+      B[j][0] = read_across(p + xb[j], 2048);
+      B[j][1] = read_across(p + xb[j] + 16384, 2048);
     }
   };
   auto mma = [&](auto R, auto Buf, auto S, auto J) __attribute__((always_inline)) {
     constexpr int i = decltype(R)::value, b = decltype(Buf)::value, s = decltype(S)::value, j = decltype(J)::value;
-    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, B[j][s]),
-                                                        __builtin_bit_cast(v8bf, A[b][s]), acc[i][j], 0, 0, 0);
+    acc[i][j] = product16(B[j][s], A[b][s], acc[i][j]);
   };
   auto row = [&](auto R) __attribute__((always_inline)) {
     for_each<2>([&](auto S) {
@@ -462,13 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       stage(Int<1>{}, k + 1, now, next);
     }
     Spot at;
-    at.tn = now.tn;
-    at.wn = wn;
-    at.part = now.part;
     at.lrow = 128 * wm + r16;
     at.lcol = 64 * wn + (BK == kAlong ? 16 : 4) * g;
+    at.bn = kTile;
     at.row0 = (int64_t)now.tm * kTile + at.lrow;
     at.col0 = (int64_t)now.tn * kTile + at.lcol;
+    at.group = (int64_t)now.tn * (kTile / 64) + wn;
     at.to = now.part < 0 ? nullptr
                          : t.split_ws + ((int64_t)now.split_tile * t.parts + now.part) * (kTile * kTile);
     epi.template store<BK == kAlong>(acc, at, t.m, t.n);
@@ -481,27 +486,277 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
 #endif
 }
 
+// Small tiles, one a workgroup: 16 FM WM rows by 64 WN = 128 columns, for
+// products whose large tiles would leave compute units without work. K advances
+// through four LDS slots, filled four stages ahead; a stage's last two block rows
+// run while the next stage's first fragments are read and the slot is refilled.
+// Layouts as above, of a K-row across K 256 bytes.
+template <bool Across, int Rows>
+struct RingPart {
+  uint8_t v[Rows * 128];
+  static_assert(!Across || Rows == 128, "K-rows of 256 bytes");
+};
+
+template <Kind AK, Kind BK, typename Epi, int WM, int WN, int FM>
+__global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, Epi epi) {
+#ifdef __HIP_DEVICE_COMPILE__
+  constexpr int Waves = WM * WN, BM = 16 * FM * WM, BN = 64 * WN;
+  constexpr int Runs = 8 / Waves;                      // of 16 codes, a thread and stage
+  constexpr int LA = BM / 8 / Waves, LB = BK == kCodes ? 2 * Runs : BN / 8 / Waves, Loads = LA + LB;
+  static_assert(BN == kRingCols && FM >= 2 && FM % 2 == 0 && 3 * Loads < 64, "");
+  using PartA = RingPart<AK != kAlong, BM>;
+  using PartB = RingPart<BK != kAlong, BN>;
+  __shared__ __attribute__((aligned(1024))) PartA a0, a1, a2, a3;
+  __shared__ __attribute__((aligned(1024))) PartB b0, b1, b2, b3;
+  auto pa = [&](auto I) -> uint8_t* {
+    if constexpr (I == 0) return a0.v;
+    else if constexpr (I == 1) return a1.v;
+    else if constexpr (I == 2) return a2.v;
+    else return a3.v;
+  };
+  auto pb = [&](auto I) -> uint8_t* {
+    if constexpr (I == 0) return b0.v;
+    else if constexpr (I == 1) return b1.v;
+    else if constexpr (I == 2) return b2.v;
+    else return b3.v;
+  };
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int r16 = lane & 15, g = lane >> 4;
+
+  // ---- place ------------------------------------------------------------------
+  const int item = xcd_band(blockIdx.x, gridDim.x);
+  const bool split = item >= t.full;
+  const int s_ = split ? item - t.full : 0;
+  const int split_tile = s_ / t.parts, part = s_ - split_tile * t.parts;
+  int m_, n_;
+  tile_at(split ? t.full + split_tile : item, t.tiles_m, t.tiles_n, &m_, &n_);
+  const int tm = __builtin_amdgcn_readfirstlane(m_), tn = __builtin_amdgcn_readfirstlane(n_);
+  const int k0 = __builtin_amdgcn_readfirstlane(split ? 2 * (int)((int64_t)t.units * part / t.parts) : 0);
+  const int end = __builtin_amdgcn_readfirstlane(2 * (split ? (int)((int64_t)t.units * (part + 1) / t.parts) : t.units));
+  const int stages = (int)((t.K + kStageK - 1) / kStageK), k1 = end < stages ? end : stages;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const uint8_t* base_a = tile_base<AK>(t.a, m0);
+  const uint8_t* base_b = tile_base<BK>(t.b, n0);
+  const int bytes_a = tile_bytes<AK>(t.a, t.m - m0 < BM ? t.m - m0 : BM, t.K);
+  const int bytes_b = tile_bytes<BK>(t.b, t.n - n0 < BN ? t.n - n0 : BN, t.K);
+
+  // ---- loads --------------------------------------------------------------------
+  struct Source {
+    __amdgpu_buffer_rsrc_t a, b, scales;
+    int left;
+  };
+  auto source = [&](int k) __attribute__((always_inline)) {
+    Source s;
+    s.left = k < k1 ? left_at(t.K, k) : 0;
+    const int kk = s.left > 0 ? k : 0;
+    s.a = source_of<AK>(base_a, bytes_a, t.a.ld, kk, s.left);
+    s.b = source_of<BK>(base_b, bytes_b, t.b.ld, kk, s.left);
+    if constexpr (BK == kCodes)
+      s.scales = source_of<BK>(t.b.scales + n0 / 32, bytes_b / 32, t.b.ld_scales, kk, s.left);
+    return s;
+  };
+  // Load q of an operand along K: rows 8 (Waves q + wave) + lane / 8; across:
+  // K-rows 4 (Waves q + wave) + lane / 16. The XOR keys of load q are those of
+  // load 0 but for the bits that Waves q brings.
+  const int row8 = 8 * wave + (lane >> 3);
+  const int ca = (lane & 7) ^ ((row8 >> 1) & 7);
+  const int cb = (lane & 7) ^ (2 * ((row8 >> 4) & 3) + ((row8 >> 1) & 1));
+  const int k4 = 4 * wave + (lane >> 4);
+  const int gx = ((lane & 15) >> 1) ^ ((k4 & 3) + 4 * ((k4 >> 3) & 1));
+  const int oa = AK == kAlong ? row8 * (int)t.a.ld + 16 * ca : k4 * (int)t.a.ld + 16 * (lane & 1);
+  const int ob = BK == kAlong ? row8 * (int)t.b.ld : k4 * (int)t.b.ld + 16 * (lane & 1);
+  const int kc = threadIdx.x >> 3, gc = threadIdx.x & 7;     // + 8 Waves K-rows a run
+  v4i codes[Runs];
+  uint8_t scale[Runs];
+  auto widen = [&](auto I) __attribute__((always_inline)) {
+    for_each<Runs>([&](auto U) {
+      constexpr int u = decltype(U)::value;
+      const int group = gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1));
+      widen16(codes[u], scale[u], reinterpret_cast<v4i*>(pb(I) + kc * 256 + 32 * group + 2048 * Waves * u));
+    });
+  };
+  auto load_a = [&](auto I, auto Q, const Source& s) __attribute__((always_inline)) {
+    constexpr int q = decltype(Q)::value;
+    int v;
+    if constexpr (AK == kAlong) v = 8 * ca < s.left ? oa + 8 * Waves * q * (int)t.a.ld : kPastEnd;
+    else v = oa + 32 * (gx ^ (4 * ((Waves / 2 * q) & 1))) + 4 * Waves * q * (int)t.a.ld;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)(pa(I) + 1024 * (Waves * q + wave)), 16, v, 0, 0, 0);
+  };
+  auto load_b = [&](auto I, auto Q, const Source& s) __attribute__((always_inline)) {
+    constexpr int q = decltype(Q)::value;
+    if constexpr (BK == kCodes) {
+      constexpr int u = q / 2;
+      if constexpr (q % 2 == 0)
+        codes[u] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(s.b, (kc + 8 * Waves * u) * (int)t.b.ld + 16 * gc, 0, 0));
+      else
+        scale[u] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, (kc + 8 * Waves * u) * (int)t.b.ld_scales + gc / 2, 0,
+                                                       0);
+    } else {
+      int v;
+      if constexpr (BK == kAlong) {
+        const int c = cb ^ (2 * ((Waves / 2 * q) & 3));
+        v = 8 * c < s.left ? ob + 16 * c + 8 * Waves * q * (int)t.b.ld : kPastEnd;
+      } else {
+        v = ob + 32 * (gx ^ (4 * ((Waves / 2 * q) & 1))) + 4 * Waves * q * (int)t.b.ld;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.b, (lds_void*)(pb(I) + 1024 * (Waves * q + wave)), 16, v, 0, 0, 0);
+    }
+  };
+
+  // ---- fragments ------------------------------------------------------------------
+  const int q4 = r16 >> 2, sub = r16 & 3, hk = q4 + 4 * (g & 1);
+  const int fa = AK == kAlong ? (16 * FM * wm + r16) * 128 + 16 * (g ^ ((r16 >> 1) & 7)) : (8 * g + q4) * 256 + 8 * sub;
+  const int fb = BK == kAlong ? (64 * wn + 16 * q4 + sub) * 128 + 16 * (g ^ (2 * q4 + (sub >> 1)))
+                              : (8 * g + q4) * 256 + 8 * sub;
+  v4f acc[FM][4];
+  v4i A[4][2], B[4][2];
+  auto read_a = [&](auto I, auto Buf, auto R) __attribute__((always_inline)) {
+    constexpr int b = decltype(Buf)::value, i = decltype(R)::value;
+    const uint8_t* p = pa(I);
+    if constexpr (AK == kAlong) {
+      A[b][0] = *reinterpret_cast<const v4i*>(p + 2048 * i + fa);
+      A[b][1] = *reinterpret_cast<const v4i*>(p + 2048 * i + (fa ^ 64));
+    } else {
+      const int at = fa + 32 * ((FM * wm + i) ^ hk);
+      A[b][0] = read_across(p + at, 1024);
+      A[b][1] = read_across(p + at + 8192, 1024);
+    }
+  };
+  auto read_b = [&](auto I, auto J) __attribute__((always_inline)) {
+    constexpr int j = decltype(J)::value;
+    const uint8_t* p = pb(I);
+    if constexpr (BK == kAlong) {
+      B[j][0] = *reinterpret_cast<const v4i*>(p + 512 * j + fb);
+      B[j][1] = *reinterpret_cast<const v4i*>(p + 512 * j + (fb ^ 64));
+    } else {
+      const int at = fb + 32 * ((4 * wn + j) ^ hk);
+      B[j][0] = read_across(p + at, 1024);
+      B[j][1] = read_across(p + at + 8192, 1024);
+    }
+  };
+  // Stage k in slot I: enters with its B fragments and its first two A fragments
+  // read; leaves with the next stage's. Fragment i of A sits in buffer
+  // (i + Off) % 4. Codes are loaded five stages ahead, a stage before they are
+  // widened into the slot.
+  auto stage = [&](auto I, int k) __attribute__((always_inline)) {
+    constexpr int slot = decltype(I)::value;
+    using Next = Int<(slot + 1) % 4>;
+    constexpr int Off = (FM * slot) % 4;
+    const Source s = source(k + 4);
+    const Source sb = BK == kCodes ? source(k + 5) : s;
+    for_each<FM - 2>([&](auto R) {
+      constexpr int i = decltype(R)::value;
+      read_a(I, Int<(i + 2 + Off) % 4>{}, Int<i + 2>{});
+      for_each<8>([&](auto X) {
+        constexpr int x = decltype(X)::value;
+        acc[i][x % 4] = product16(B[x % 4][x / 4], A[(i + Off) % 4][x / 4], acc[i][x % 4]);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // All of this slot's reads are in; the next stage's loads of this wave have
+    // landed when only the two later stages' are in flight. The barrier
+    // publishes the next stage and frees this slot.
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * Loads, 0));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (BK == kCodes) widen(I);
+    read_a(Next{}, Int<(FM + Off) % 4>{}, Int<0>{});
+    read_a(Next{}, Int<(FM + 1 + Off) % 4>{}, Int<1>{});
+    for_each<4>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      for_each<2>([&](auto S) {
+        constexpr int x = decltype(S)::value;
+        acc[FM - 2][j] = product16(B[j][x], A[(FM - 2 + Off) % 4][x], acc[FM - 2][j]);
+        acc[FM - 1][j] = product16(B[j][x], A[(FM - 1 + Off) % 4][x], acc[FM - 1][j]);
+      });
+      read_b(Next{}, J);
+      for_each<Loads * (j + 1) / 4 - Loads * j / 4>([&](auto Q) {
+        constexpr int q = Loads * j / 4 + decltype(Q)::value;
+        if constexpr (q < LB) load_b(I, Int<q>{}, sb);
+        else load_a(I, Int<q - LB>{}, s);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+  for_each<4>([&](auto I) {
+    const Source s = source(k0 + I);
+    for_each<LB>([&](auto Q) { load_b(I, Q, s); });
+    if constexpr (BK == kCodes) widen(I);
+    for_each<LA>([&](auto Q) { load_a(I, Q, s); });
+  });
+  if constexpr (BK == kCodes) {
+    const Source s = source(k0 + 4);
+    for_each<LB>([&](auto Q) { load_b(Int<0>{}, Q, s); });
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(BK == kCodes ? LA + LB : 3 * Loads, 0));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  read_a(Int<0>{}, Int<0>{}, Int<0>{});
+  read_a(Int<0>{}, Int<1>{}, Int<1>{});
+  for_each<4>([&](auto J) { read_b(Int<0>{}, J); });
+  int k = k0;
+  for (; k + 4 <= k1; k += 4) for_each<4>([&](auto I) { stage(I, k + I); });
+  for_each<3>([&](auto I) {
+    if (k + I < k1) stage(I, k + I);
+  });
+  Spot at;
+  at.lrow = 16 * FM * wm + r16;
+  at.lcol = 64 * wn + (BK == kAlong ? 16 : 4) * g;
+  at.bn = BN;
+  at.row0 = m0 + at.lrow;
+  at.col0 = n0 + at.lcol;
+  at.group = (int64_t)tn * WN + wn;
+  at.to = !split ? nullptr : t.split_ws + ((int64_t)split_tile * t.parts + part) * (BM * BN);
+  epi.template store<BK == kAlong>(acc, at, t.m, t.n);
+  // No load may be in flight into LDS when the workgroup ends.
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+#endif
+}
+
 // ---- host ---------------------------------------------------------------------
-inline int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 inline int64_t units_of(int64_t K) { return (K + 2 * kStageK - 1) / (2 * kStageK); }
 
-inline TileArgs tile_args(Operand a, Operand b, int64_t m, int64_t n, int64_t K) {
+inline TileArgs tile_args(const ProductPlan& p, Operand a, Operand b, int64_t m, int64_t n, int64_t K) {
   TileArgs t{};
   t.a = a;
   t.b = b;
   t.m = m;
   t.n = n;
   t.K = K;
-  t.tiles_m = (int)tiles_of(m);
-  t.tiles_n = (int)tiles_of(n);
+  t.bm = tile_rows(p.shape);
+  t.bn = tile_cols(p.shape);
+  t.tiles_m = (int)((m + t.bm - 1) / t.bm);
+  t.tiles_n = (int)((n + t.bn - 1) / t.bn);
   t.units = (int)units_of(K);
-  t.full = t.tiles_m * t.tiles_n;
-  t.parts = 1;
+  t.full = (int)p.full;
+  t.split = (int)p.split;
+  t.parts = p.parts;
   return t;
 }
-inline dim3 tile_grid(const TileArgs& t) {
-  const int64_t items = (int64_t)t.full + (int64_t)t.split * t.parts, cus = compute_units();
-  return dim3((unsigned)(items < cus ? items : cus));
+
+template <Kind AK, Kind BK, typename Epi>
+void tile_launch(const ProductPlan& p, TileArgs t, const Epi& epi, hipStream_t stream) {
+  const int64_t items = p.full + p.split * p.parts, cus = compute_units();
+  if (p.shape == kTile256) {
+    // Codes are loaded three stages ahead, which has to stay within the next tile.
+    if (BK == kCodes && t.units < 2) t.units = 2;
+    bf16_tile_kernel<AK, BK, Epi><<<dim3((unsigned)(items < cus ? items : cus)), dim3(kThreads), 0, stream>>>(t, epi);
+    return;
+  }
+  const dim3 grid((unsigned)items);
+  if constexpr (AK == kAlong) {
+    if (p.shape == kTile64)
+      return (void)(bf16_ring_kernel<AK, BK, Epi, 2, 2, 2><<<grid, dim3(256), 0, stream>>>(t, epi));
+  }
+  bf16_ring_kernel<AK, BK, Epi, 4, 2, 2><<<grid, dim3(512), 0, stream>>>(t, epi);
 }
 
 }  // namespace tiles

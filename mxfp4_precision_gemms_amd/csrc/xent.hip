@@ -48,15 +48,15 @@ struct Targets {
 struct StatsEpi {
   float scale;
   Targets y;
-  float2* part;              // [tile column][wave column][T]
+  float2* part;              // [64 columns][T]
   float* said;               // [T]: the target's logit
-  template <bool Wide>
-  __device__ __forceinline__ void store(v4f (&acc)[8][4], const Spot& at, int64_t m, int64_t n) const {
+  template <bool Wide, int FM>
+  __device__ __forceinline__ void store(v4f (&acc)[FM][4], const Spot& at, int64_t m, int64_t n) const {
     static_assert(Wide, "");
-    float2* to = part + ((int64_t)at.tn * 4 + at.wn) * m;
+    float2* to = part + at.group * m;
     const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < FM; ++i) {
       const int64_t r = at.row0 + 16 * i;
       float z[16], top = kMinusInf;
 #pragma unroll
@@ -97,12 +97,12 @@ struct GradEpi {
   int64_t v0, vocab;
   uint16_t* g;
   int64_t ld;
-  template <bool Wide>
-  __device__ __forceinline__ void store(v4f (&acc)[8][4], const Spot& at, int64_t m, int64_t n) const {
+  template <bool Wide, int FM>
+  __device__ __forceinline__ void store(v4f (&acc)[FM][4], const Spot& at, int64_t m, int64_t n) const {
     static_assert(Wide, "");
     const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < FM; ++i) {
       const int64_t r = at.row0 + 16 * i;
       if (r < m) {
         const float less = lse[r];
@@ -177,43 +177,47 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(FinishArgs a) {
 
 // ---- host ---------------------------------------------------------------------
 Operand along(const uint16_t* p, int64_t ld) { return {reinterpret_cast<const uint8_t*>(p), 2 * ld, nullptr, 0}; }
+// Whole columns of 256, which every tile's columns divide.
+int64_t whole(int64_t n) { return (n + kTile - 1) / kTile * kTile; }
+// Groups of 64 columns that leave a maximum and a sum for a row.
+int64_t groups_of(int64_t V) { return whole(V) / 64; }
 TileOperand operand(const uint16_t* p, int64_t ld, Kind kind) { return {p, 2 * ld, nullptr, 0, kind}; }
 
 }  // namespace
 
 size_t xent_ws_bytes(int64_t T, int64_t V) {
-  return align_up(sizeof(float2) * (size_t)tiles_of(V) * 4 * (size_t)T, kAlign) + sizeof(float) * (size_t)T;
+  return align_up(sizeof(float2) * (size_t)groups_of(V) * (size_t)T, kAlign) + sizeof(float) * (size_t)T;
 }
 
 adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t stream) {
   const Targets y = {a.targets, a.wide_targets};
   float2* part = static_cast<float2*>(ws);
   float* said = reinterpret_cast<float*>(static_cast<char*>(ws) +
-                                         align_up(sizeof(float2) * (size_t)tiles_of(a.V) * 4 * (size_t)a.T, kAlign));
-  const TileArgs t = tile_args(along(a.h, a.ldh), along(a.w, a.ldw), a.T, a.V, a.D);
-  const StatsEpi epi = {a.scale, y, part, said};
-  bf16_tile_kernel<kAlong, kAlong, StatsEpi><<<tile_grid(t), dim3(kThreads), 0, stream>>>(t, epi);
+                                         align_up(sizeof(float2) * (size_t)groups_of(a.V) * (size_t)a.T, kAlign));
+  const ProductPlan plan = product_plan(a.T, a.V, a.D, true, false, compute_units());
+  const TileArgs t = tile_args(plan, along(a.h, a.ldh), along(a.w, a.ldw), a.T, a.V, a.D);
+  tile_launch<kAlong, kAlong>(plan, t, StatsEpi{a.scale, y, part, said}, stream);
   const adahop_status st = check_launch("xent");
   if (st != ADAHOP_OK) return st;
-  const FinishArgs f = {part, said, y, a.T, a.V, tiles_of(a.V) * 4, loss, lse};
+  const FinishArgs f = {part, said, y, a.T, a.V, (int64_t)t.tiles_n * (t.bn / 64), loss, lse};
   xent_finish_kernel<<<dim3((unsigned)((a.T + 15) / 16)), dim3(256), 0, stream>>>(f);
   return check_launch("xent_finish");
 }
 
 // ---- backward -------------------------------------------------------------------
 XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece) {
-  const int64_t all = tiles_of(V) * kTile;
+  const int64_t all = whole(V);
   if (piece == 0) {
     // g of a piece within 1 GiB, in pieces of about the same size.
     piece = (int64_t{1} << 29) / (T > 0 ? T : 1) / kTile * kTile;
     if (piece < kTile) piece = kTile;
     if (piece > all) piece = all;
     const int64_t count = (all + piece - 1) / piece;
-    piece = tiles_of((all + count - 1) / count) * kTile;
+    piece = whole((all + count - 1) / count);
   }
   // A row of g stays within the tiles' reach.
   if (piece > kMaxRowBytes / 4) piece = kMaxRowBytes / 4;
-  piece = tiles_of(piece < V ? piece : V) * kTile;
+  piece = whole(piece < V ? piece : V);
   return {piece, (V + piece - 1) / piece};
 }
 
@@ -232,7 +236,7 @@ BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, 
   const int64_t last = V - (l.p.count - 1) * l.p.size;
   size_t split = 0;
   for (const int64_t n : {l.p.size < V ? l.p.size : V, last}) {
-    const size_t s = dh ? tile_product_bytes(T, D, n) : 0, u = dw ? tile_product_bytes(n, D, T) : 0;
+    const size_t s = dh ? tile_product_bytes(T, D, n, true) : 0, u = dw ? tile_product_bytes(n, D, T, false) : 0;
     split = split > s ? split : s;
     split = split > u ? split : u;
   }
@@ -263,9 +267,9 @@ adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t
   for (int64_t q = 0; q < l.p.count; ++q) {
     const int64_t v0 = q * l.p.size, n = a.V - v0 < l.p.size ? a.V - v0 : l.p.size;
     const uint16_t* w = a.w + v0 * a.ldw;
-    const TileArgs t = tile_args(along(a.h, a.ldh), along(w, a.ldw), a.T, n, a.D);
-    const GradEpi epi = {a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, l.p.size};
-    bf16_tile_kernel<kAlong, kAlong, GradEpi><<<tile_grid(t), dim3(kThreads), 0, stream>>>(t, epi);
+    const ProductPlan plan = product_plan(a.T, n, a.D, true, false, compute_units());
+    const TileArgs t = tile_args(plan, along(a.h, a.ldh), along(w, a.ldw), a.T, n, a.D);
+    tile_launch<kAlong, kAlong>(plan, t, GradEpi{a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, l.p.size}, stream);
     adahop_status st = check_launch("xent_backward logits");
     if (st != ADAHOP_OK) return st;
     if (b.dh != nullptr) {

@@ -72,7 +72,7 @@ constexpr int kTile = 256;                 // rows and columns of a large tile
 constexpr int kStageK = 64;                // K elements of a stage
 constexpr int kThreads = 512;
 constexpr int kRingCols = 128;             // columns of a small tile
-constexpr int kGroupM = 4;                 // tile rows that run together on one XCD
+constexpr int kGroupM = 8;                 // tile rows that run together on one XCD
 
 // How an operand lies: along K, across it, or across it in MXFP8 (B alone).
 enum Kind { kAlong = 0, kAcross = 1, kCodes = 2 };
@@ -159,18 +159,14 @@ __device__ __forceinline__ v4i read_across(const uint8_t* p, int next) {
   const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s16*)(p + next)));
   return v4i{lo[0], lo[1], hi[0], hi[1]};
 }
-// 16 codes under one scale as 16 bf16 (exact; below 2^-126 possibly 0).
-__device__ __forceinline__ void widen16(const v4i& codes, uint8_t scale, v4i* to) {
-  const float by = mx8::mx8_scale(scale);
-  v4i w[2];
-  for_each<4>([&](auto D) {
-    constexpr int d = decltype(D)::value;
-    const uint32_t four = (uint32_t)codes[d];
-    w[d / 2][2 * (d % 2)] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, by, false));
-    w[d / 2][2 * (d % 2) + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, by, true));
-  });
-  to[0] = w[0];
-  to[1] = w[1];
+// 8 codes under one scale as 8 bf16 (exact; below 2^-126 possibly 0). The
+// instruction takes the scale's exponent alone, so every byte is its E8M0 value.
+__device__ __forceinline__ v4i widen8(uint32_t lo, uint32_t hi, uint8_t scale) {
+  const float by = __builtin_bit_cast(float, (uint32_t)scale << 23);
+  return v4i{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, by, false)),
+             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, by, true)),
+             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, by, false)),
+             __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, by, true))};
 }
 __device__ __forceinline__ v4f product16(const v4i& b, const v4i& a, const v4f& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, b), __builtin_bit_cast(v8bf, a), c, 0, 0, 0);
@@ -294,11 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   v4i codes[2];
   uint8_t scale[2];
   const int oc = kc * 512 + 32 * (gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1)));
-  auto widen = [&](auto I) __attribute__((always_inline)) {
-    for_each<2>([&](auto U) {
-      constexpr int u = decltype(U)::value;
-      widen16(codes[u], scale[u], reinterpret_cast<v4i*>(wide(I).b + oc + 16384 * u));
-    });
+  // Half h of run u. Of 8 threads, 4 begin with their second half, so that a
+  // write's 16-byte pieces lie 16 bytes apart over 128.
+  const int sw = (gc >> 2) & 1;
+  auto widen = [&](auto I, auto U, auto H) __attribute__((always_inline)) {
+    constexpr int u = decltype(U)::value, h = decltype(H)::value;
+    const bool last = h != sw;
+    const v4i w = widen8((uint32_t)(last ? codes[u][2] : codes[u][0]), (uint32_t)(last ? codes[u][3] : codes[u][1]), scale[u]);
+    *reinterpret_cast<v4i*>(wide(I).b + oc + 16384 * u + (last ? 16 : 0)) = w;
   };
   // Across K, a row's last bytes are followed by the next row's: columns past
   // the tile's end reach only sums that are not stored.
@@ -382,38 +381,53 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   auto stage = [&](auto I, int k, const Place& now, const Place& next) __attribute__((always_inline)) {
     using Next = Int<1 - decltype(I)::value>;
     const Source s = source(k + 2, now, next);
-    const Source sb = BK == kCodes ? source(k + 3, now, next) : s;
+    // A block row's matrix instructions with its LDS reads, `piece` of the codes'
+    // widening (one LDS write) and loads `First` .. of the stage's between them.
+    auto step = [&](auto R, auto Piece, auto First, auto Count) __attribute__((always_inline)) {
+      constexpr int r = decltype(R)::value, piece = decltype(Piece)::value, count = decltype(Count)::value;
+      row(R);
+      if constexpr (piece >= 0) widen(I, Int<piece / 2>{}, Int<piece % 2>{});
+      for_each<count>([&](auto C) { issue(I, Int<decltype(First)::value + decltype(C)::value>{}, s); });
+      for_each<8>([&](auto X) {
+        constexpr int x = decltype(X)::value;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                          // MFMA
+        if constexpr (x < ReadsA) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // DS read
+        if constexpr (piece >= 0) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);                // VALU
+        if constexpr (piece >= 0 && x == 6) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);      // DS write
+        if constexpr (x >= 4 && x - 4 < count) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // VMEM
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr bool Codes = BK == kCodes;
+    // The codes of run u, a stage further ahead, once both its halves are widened.
+    auto recode = [&](auto U) __attribute__((always_inline)) {
+      if constexpr (Codes) {
+        const Source sb = source(k + 3, now, next);
+        issue(I, Int<4 + 2 * decltype(U)::value>{}, sb);
+        issue(I, Int<5 + 2 * decltype(U)::value>{}, sb);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
     read_a(I, Int<2>{}, Int<2>{});
-    row(Int<0>{});
-    __builtin_amdgcn_sched_barrier(0);
+    step(Int<0>{}, Int<-1>{}, Int<0>{}, Int<0>{});
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));         // B and A 0 .. 2 are read
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read_a(I, Int<3>{}, Int<3>{});
-    row(Int<1>{});
-    if constexpr (BK == kCodes) widen(I);
-    issue(I, Int<4>{}, sb);
-    issue(I, Int<5>{}, sb);
-    __builtin_amdgcn_sched_barrier(0);
+    step(Int<1>{}, Int<Codes ? 0 : -1>{}, Int<4>{}, Int<Codes ? 0 : 2>{});
     read_a(I, Int<0>{}, Int<4>{});
-    row(Int<2>{});
-    issue(I, Int<6>{}, sb);
-    issue(I, Int<7>{}, sb);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, ReadsA));       // A 3 is read
+    step(Int<2>{}, Int<Codes ? 1 : -1>{}, Int<6>{}, Int<Codes ? 0 : 2>{});
+    recode(Int<0>{});
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, ReadsA + (Codes ? 1 : 0)));   // A 3 is read
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read_a(I, Int<1>{}, Int<5>{});
-    row(Int<3>{});
-    issue(I, Int<0>{}, s);
-    __builtin_amdgcn_sched_barrier(0);
+    step(Int<3>{}, Int<Codes ? 2 : -1>{}, Int<0>{}, Int<1>{});
     read_a(I, Int<2>{}, Int<6>{});
-    row(Int<4>{});
-    issue(I, Int<2>{}, s);
-    __builtin_amdgcn_sched_barrier(0);
+    step(Int<4>{}, Int<Codes ? 3 : -1>{}, Int<2>{}, Int<1>{});
+    recode(Int<1>{});
     read_a(I, Int<3>{}, Int<7>{});
-    row(Int<5>{});
-    __builtin_amdgcn_sched_barrier(0);
+    step(Int<5>{}, Int<-1>{}, Int<0>{}, Int<0>{});
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
@@ -427,6 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       read_b(Next{}, J);
       if constexpr (J == 1) issue(I, Int<1>{}, s);
       if constexpr (J == 2) issue(I, Int<3>{}, s);
+      for_each<4>([&](auto X) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (J == 0 ? 3 : 1) * (ReadsA / 2) / 2, 0);
+      });
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -435,21 +453,40 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   if (item < 0) return;
   Place now = place(item), next = place(item_at(1));
   int round = 1;
-  for_each<2>([&](auto I) {
-    const Source s = source(now.k0 + I, now, next);
-    for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, s); });
-    if constexpr (BK == kCodes) widen(I);
-    issue(I, Int<0>{}, s);
-    issue(I, Int<2>{}, s);
-    issue(I, Int<1>{}, s);
-    issue(I, Int<3>{}, s);
-  });
   if constexpr (BK == kCodes) {
-    const Source s = source(now.k0 + 2, now, next);
+    // The order of the loads after slot 0's is a stage's, so that the waits for
+    // codes are as loose here as there.
+    const Source s = source(now.k0, now, next), s1 = source(now.k0 + 1, now, next), s2 = source(now.k0 + 2, now, next);
+    auto whole = [&](auto I) __attribute__((always_inline)) {
+      for_each<4>([&](auto X) { widen(I, Int<decltype(X)::value / 2>{}, Int<decltype(X)::value % 2>{}); });
+      __builtin_amdgcn_sched_barrier(0);
+    };
     for_each<4>([&](auto Q) { issue(Int<0>{}, Int<4 + Q>{}, s); });
-    // Of 4, 4 and the codes' 4 loads, slot 0's first half of A has landed.
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 + Loads, 0));
+    for_each<4>([&](auto Q) { issue(Int<0>{}, Q, s); });
+    whole(Int<0>{});
+    for_each<4>([&](auto Q) { issue(Int<1>{}, Int<4 + Q>{}, s1); });
+    whole(Int<1>{});
+    issue(Int<0>{}, Int<4>{}, s2);
+    issue(Int<0>{}, Int<5>{}, s2);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(Int<1>{}, Int<0>{}, s1);
+    issue(Int<1>{}, Int<2>{}, s1);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(Int<0>{}, Int<6>{}, s2);
+    issue(Int<0>{}, Int<7>{}, s2);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(Int<1>{}, Int<1>{}, s1);
+    issue(Int<1>{}, Int<3>{}, s1);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
   } else {
+    for_each<2>([&](auto I) {
+      const Source s = source(now.k0 + I, now, next);
+      for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, s); });
+      issue(I, Int<0>{}, s);
+      issue(I, Int<2>{}, s);
+      issue(I, Int<1>{}, s);
+      issue(I, Int<3>{}, s);
+    });
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 + Loads, 15));
   }
   __builtin_amdgcn_s_barrier();
@@ -570,11 +607,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int kc = threadIdx.x >> 3, gc = threadIdx.x & 7;     // + 8 Waves K-rows a run
   v4i codes[Runs];
   uint8_t scale[Runs];
+  const int sw = (gc >> 2) & 1;
   auto widen = [&](auto I) __attribute__((always_inline)) {
     for_each<Runs>([&](auto U) {
       constexpr int u = decltype(U)::value;
-      const int group = gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1));
-      widen16(codes[u], scale[u], reinterpret_cast<v4i*>(pb(I) + kc * 256 + 32 * group + 2048 * Waves * u));
+      uint8_t* to = pb(I) + kc * 256 + 32 * (gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1))) + 2048 * Waves * u;
+      for_each<2>([&](auto H) {
+        const bool last = decltype(H)::value != sw;
+        *reinterpret_cast<v4i*>(to + (last ? 16 : 0)) =
+            widen8((uint32_t)(last ? codes[u][2] : codes[u][0]), (uint32_t)(last ? codes[u][3] : codes[u][1]), scale[u]);
+      });
     });
   };
   auto load_a = [&](auto I, auto Q, const Source& s) __attribute__((always_inline)) {

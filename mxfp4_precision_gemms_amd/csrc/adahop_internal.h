@@ -284,13 +284,13 @@ struct TileOut {
   const float* prev;
   int64_t ld_prev;
 };
-// along: whether A lies along K.
-size_t tile_product_bytes(int64_t m, int64_t n, int64_t K, bool along);
+// a, b: the operands' kinds.
+size_t tile_product_bytes(int64_t m, int64_t n, int64_t K, int a, int b);
 adahop_status tile_product_launch(const TileOperand& a, const TileOperand& b, int64_t m, int64_t n, int64_t K,
                                   const TileOut& out, float* ws, hipStream_t stream);
 
-// dW [Dout, Din] = GY^T X from X in MXFP8, checked; ws: tile_product_bytes(Dout,
-// Din, T, false) bytes.
+// dW [Dout, Din] = GY^T X from X in MXFP8, checked; ws: wgrad_mx8_ws_bytes bytes.
+size_t wgrad_mx8_ws_bytes(int64_t T, int64_t Din, int64_t Dout);
 adahop_status wgrad_mx8_launch(const uint16_t* gy, int64_t ldgy, const Mx8Matrix& x, int64_t T, int64_t Din,
                                int64_t Dout, void* out, int out_f32, int64_t ldo, float* ws, hipStream_t stream);
 

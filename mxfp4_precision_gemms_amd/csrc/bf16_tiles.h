@@ -74,9 +74,6 @@ constexpr int kThreads = 512;
 constexpr int kRingCols = 128;             // columns of a small tile
 constexpr int kGroupM = 8;                 // tile rows that run together on one XCD
 
-// How an operand lies: along K, across it, or across it in MXFP8 (B alone).
-enum Kind { kAlong = 0, kAcross = 1, kCodes = 2 };
-
 struct Operand {
   const uint8_t* p;
   int64_t ld;                // bytes from a row to the next
@@ -91,7 +88,8 @@ struct TileArgs {
   int bm, bn;                // rows and columns of a tile
   int units;                 // pairs of stages of K
   // Items 0 .. full - 1 are whole tiles; those after them each one of `parts`
-  // parts of K of a tile, whose sums go to split_ws ([tile][part][bm][bn]).
+  // parts of K of a tile, whose sums go to split_ws ([tile][part][bm][bn]). All
+  // tiles' first parts come first, so that what an XCD runs at once shares K-rows.
   int full, split, parts;
   float* split_ws;
 };
@@ -113,11 +111,12 @@ __device__ __forceinline__ void tile_at(int pos, int tiles_m, int tiles_n, int* 
 }
 
 // What an epilogue is told of the wave's accumulators: acc[i][j][e] is row
-// row0 + 16 i, column col0 + (BK == kAlong ? 4 j : 16 j) + e.
+// row0 + step i, column col0 + (BK == kAlong ? 4 j : 16 j) + e.
 struct Spot {
   int64_t row0, col0;
   int64_t group;             // the wave's columns start at 64 group
   float* to;                 // a part's sums [bm][bn]; null: a whole tile
+  int step;                  // from a block row to the next
   int lrow, lcol, bn;        // row and column in the tile
 };
 
@@ -172,27 +171,32 @@ __device__ __forceinline__ v4f product16(const v4i& b, const v4i& a, const v4f& 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, b), __builtin_bit_cast(v8bf, a), c, 0, 0, 0);
 }
 
+template <int Rows>
 struct Half {
-  uint8_t a[128 * 128];
+  uint8_t a[Rows * 128];
 };
 struct Wide {
   uint8_t b[256 * 128];
 };
 
-template <Kind AK, Kind BK, typename Epi>
+template <Kind AK, Kind BK, typename Epi, int FM>
 __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi epi) {
 #ifdef __HIP_DEVICE_COMPILE__                        // the host pass needs the launch stub alone
-  constexpr int Loads = 8;                           // of a wave and stage: 4 of A, 4 of B
+  // Tile rows; a wave's block rows in A's second half; loads of a wave and stage:
+  // of A (2 of the first half) and 4 of B.
+  constexpr int BM = 32 * FM, Rest = FM - 4, LA = FM / 2, Loads = LA + 4;
+  static_assert(FM == 8 || (FM == 6 && AK == kAlong), "");
   // One LDS object for each part that is filled at once: alias analysis then
   // sees that loads into one do not touch another, and adds no wait before
   // the reads.
-  __shared__ __attribute__((aligned(1024))) Half f0, f1, r0, r1;   // first and last 64 rows of a wave
+  __shared__ __attribute__((aligned(1024))) Half<128> f0, f1;           // a wave row's first 4 block rows
+  __shared__ __attribute__((aligned(1024))) Half<32 * Rest> r0, r1;     // and the others
   __shared__ __attribute__((aligned(1024))) Wide w0, w1;
-  auto half = [&](auto I, auto H) -> Half& {
-    if constexpr (I == 0 && H == 0) return f0;
-    else if constexpr (I == 0) return r0;
-    else if constexpr (H == 0) return f1;
-    else return r1;
+  auto half = [&](auto I, auto H) -> uint8_t* {
+    if constexpr (I == 0 && H == 0) return f0.a;
+    else if constexpr (I == 0) return r0.a;
+    else if constexpr (H == 0) return f1.a;
+    else return r1.a;
   };
   auto wide = [&](auto I) -> Wide& {
     if constexpr (I == 0) return w0;
@@ -227,9 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     int tile = item, part = -1;
     if (item >= t.full) {
       const int s = item - t.full;
-      p.split_tile = __builtin_amdgcn_readfirstlane(s / t.parts);
+      part = s / t.split;
+      p.split_tile = __builtin_amdgcn_readfirstlane(s - part * t.split);
       tile = t.full + p.split_tile;
-      part = s - p.split_tile * t.parts;
     }
     int m_, n_;
     tile_at(tile, t.tiles_m, t.tiles_n, &m_, &n_);
@@ -242,10 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       p.k0 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)t.units * p.part / t.parts));
       p.k1 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)t.units * (p.part + 1) / t.parts));
     }
-    const int64_t m0 = (int64_t)p.tm * kTile, n0 = (int64_t)p.tn * kTile;
+    const int64_t m0 = (int64_t)p.tm * BM, n0 = (int64_t)p.tn * kTile;
     p.a = tile_base<AK>(t.a, m0);
     p.b = tile_base<BK>(t.b, n0);
-    p.a_bytes = tile_bytes<AK>(t.a, t.m - m0 < kTile ? t.m - m0 : kTile, t.K);
+    p.a_bytes = tile_bytes<AK>(t.a, t.m - m0 < BM ? t.m - m0 : BM, t.K);
     p.b_bytes = tile_bytes<BK>(t.b, t.n - n0 < kTile ? t.n - n0 : kTile, t.K);
     if constexpr (BK == kCodes) p.scales = t.b.scales + n0 / 32;
     return p;
@@ -271,17 +275,23 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
                                kk, s.left);
     return s;
   };
-  // Along K, load q of this wave fills rows 64 q + 8 wave + lane / 8 with chunks
-  // XORed as they are read; across, K-rows (A) 32 (q / 2) + 4 wave + lane / 16 of
-  // half q % 2, (B) 16 q + 2 wave + lane / 32.
+  // Block row i of wave row wm is rows 32 i + 16 wm .. +15 of the tile, so that a
+  // tile of few rows has work for both. Along K, load q of this wave fills rows
+  // 64 q' + 8 wave + lane / 8 of B or of a half of A (loads 0 and 2 the first, 1 and
+  // 3 the other; q' = q / 2), with chunks XORed as they are read; across, K-rows
+  // (A) 32 q' + 4 wave + lane / 16 of a half, (B) 16 q + 2 wave + lane / 32.
   const int row8 = 8 * wave + (lane >> 3);
   const int ca = (lane & 7) ^ ((row8 >> 1) & 7);
   const int cb = (lane & 7) ^ (2 * ((row8 >> 4) & 3) + ((row8 >> 1) & 1));
   const int ka = 4 * wave + (lane >> 4), kb = 2 * wave + (lane >> 5);
   const int ga = ((lane & 15) >> 1) ^ ((ka & 3) + 4 * ((ka >> 3) & 1));
   const int gb0 = ((lane & 31) >> 1) ^ ((kb & 3) + 4 * ((kb >> 3) & 1));
-  const int oa = AK == kAlong ? row8 * (int)t.a.ld + 16 * ca
-                              : ka * (int)t.a.ld + 256 * (ga >> 2) + 32 * (ga & 3) + 16 * (lane & 1);
+  const int rowa = 32 * (wave >> 1) + 8 * (wave & 1) + (lane >> 3);
+  // The second half holds, of 6 block rows, two: 16 rows of each wave row.
+  const int rowr = FM == 8 ? 128 + rowa : 128 + 32 * ((wave >> 1) & 1) + 16 * (wave >> 2) + 8 * (wave & 1) + (lane >> 3);
+  const int oa = AK == kAlong ? rowa * (int)t.a.ld + 16 * ca
+                              : ka * (int)t.a.ld + 64 * (ga & 3) + 32 * (ga >> 2) + 16 * (lane & 1);
+  const int orest = rowr * (int)t.a.ld + 16 * ca;
   // Codes: two runs of 16 of a stage a thread, K-rows 32 u + thread / 16.
   const int kc = threadIdx.x >> 4, gc = threadIdx.x & 15;
   const int ob = BK == kCodes ? kc * (int)t.b.ld + 16 * gc : BK == kAlong ? row8 * (int)t.b.ld + 16 * cb : kb * (int)t.b.ld + 32 * gb0 + 16 * (lane & 1);
@@ -305,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     constexpr int q = decltype(Q)::value;
     if constexpr (q < 4) {
       int v;
-      if constexpr (AK == kAlong) v = 8 * ca < s.left ? oa + 64 * q * (int)t.a.ld : kPastEnd;
-      else v = oa + 32 * (q / 2) * (int)t.a.ld + 128 * (q % 2);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)&half(I, Int<q % 2>{}).a[1024 * (8 * (q / 2) + wave)],
+      if constexpr (AK == kAlong) v = 8 * ca < s.left ? (q % 2 == 0 ? oa : orest) + 16 * (q / 2) * (int)t.a.ld : kPastEnd;
+      else v = oa + 32 * (q / 2) * (int)t.a.ld + 256 * (q % 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)(half(I, Int<q % 2>{}) + 1024 * (8 * (q / 2) + wave)),
                                                16, v, 0, 0, 0);
     } else if constexpr (BK == kCodes) {
       constexpr int u = (q - 4) / 2;
@@ -334,23 +344,21 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
                               : (8 * g + q4) * 256 + 8 * sub;
   const int fb = BK == kAlong ? (64 * wn + 16 * q4 + sub) * 128 + 16 * (g ^ (2 * q4 + (sub >> 1)))
                               : (8 * g + q4) * 512 + 8 * sub;
-  int xa[4], xb[4];                                  // across K: the groups of the blocks
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    xa[i] = fa + 32 * ((4 * wm + i) ^ hk);
-    xb[i] = fb + 32 * ((4 * wn + i) ^ hk);
-  }
-  v4f acc[8][4];
+  // Across K: the first block's address; block i's differs in the bits of 32 i.
+  const int xa = fa + 32 * ((4 * wm) ^ hk), xb = fb + 32 * ((4 * wn) ^ hk);
+  const int fr = FM == 8 ? fa : fa - 32 * 128 * wm;  // in A's second half
+  v4f acc[FM][4];
   v4i A[4][2], B[4][2];
   auto read_a = [&](auto I, auto Buf, auto R) __attribute__((always_inline)) {
     constexpr int b = decltype(Buf)::value, i = decltype(R)::value;
-    const uint8_t* p = half(I, Int<i / 4>{}).a;
+    const uint8_t* p = half(I, Int<i / 4>{});
     if constexpr (AK == kAlong) {
-      A[b][0] = *reinterpret_cast<const v4i*>(p + 2048 * (i % 4) + fa);
-      A[b][1] = *reinterpret_cast<const v4i*>(p + 2048 * (i % 4) + (fa ^ 64));
+      const int at = i < 4 ? fa : fr;
+      A[b][0] = *reinterpret_cast<const v4i*>(p + 2048 * (i % 4) + at);
+      A[b][1] = *reinterpret_cast<const v4i*>(p + 2048 * (i % 4) + (at ^ 64));
     } else {
-      A[b][0] = read_across(p + xa[i % 4], 1024);
-      A[b][1] = read_across(p + xa[i % 4] + 8192, 1024);
+      A[b][0] = read_across(p + (xa ^ (32 * (i % 4))), 1024);
+      A[b][1] = read_across(p + (xa ^ (32 * (i % 4))) + 8192, 1024);
     }
   };
   auto read_b = [&](auto I, auto J) __attribute__((always_inline)) {
@@ -360,32 +368,30 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       B[j][0] = *reinterpret_cast<const v4i*>(p + 512 * j + fb);
       B[j][1] = *reinterpret_cast<const v4i*>(p + 512 * j + (fb ^ 64));
     } else {
-      B[j][0] = read_across(p + xb[j], 2048);
-      B[j][1] = read_across(p + xb[j] + 16384, 2048);
+      B[j][0] = read_across(p + (xb ^ (32 * j)), 2048);
+      B[j][1] = read_across(p + (xb ^ (32 * j)) + 16384, 2048);
     }
   };
   auto mma = [&](auto R, auto Buf, auto S, auto J) __attribute__((always_inline)) {
     constexpr int i = decltype(R)::value, b = decltype(Buf)::value, s = decltype(S)::value, j = decltype(J)::value;
     acc[i][j] = product16(B[j][s], A[b][s], acc[i][j]);
   };
-  auto row = [&](auto R) __attribute__((always_inline)) {
-    for_each<2>([&](auto S) {
-      for_each<4>([&](auto J) { mma(R, Int<decltype(R)::value % 4>{}, S, J); });
-    });
-  };
   constexpr int ReadsA = AK == kAlong ? 2 : 4;       // LDS reads of a block row's fragments
 
   // Stage k in slot I: enters with its B fragments and first two A fragments
-  // read; leaves with the next stage's. Loads still in flight at the first and
-  // the last wait: the 8 issued since those of the parts that are due.
+  // read; leaves with the next stage's. Fragment i of A sits in buffer
+  // (i + Off) % 4. Loads still in flight at the first and the last wait: a
+  // stage's, issued since those of the parts that are due.
   auto stage = [&](auto I, int k, const Place& now, const Place& next) __attribute__((always_inline)) {
     using Next = Int<1 - decltype(I)::value>;
+    constexpr int Off = (FM * decltype(I)::value) % 4;
+    auto read = [&](auto R) { read_a(I, Int<(decltype(R)::value + Off) % 4>{}, R); };
     const Source s = source(k + 2, now, next);
     // A block row's matrix instructions with its LDS reads, `piece` of the codes'
     // widening (one LDS write) and loads `First` .. of the stage's between them.
     auto step = [&](auto R, auto Piece, auto First, auto Count) __attribute__((always_inline)) {
       constexpr int r = decltype(R)::value, piece = decltype(Piece)::value, count = decltype(Count)::value;
-      row(R);
+      for_each<2>([&](auto S) { for_each<4>([&](auto J) { mma(R, Int<(r + Off) % 4>{}, S, J); }); });
       if constexpr (piece >= 0) widen(I, Int<piece / 2>{}, Int<piece % 2>{});
       for_each<count>([&](auto C) { issue(I, Int<decltype(First)::value + decltype(C)::value>{}, s); });
       for_each<8>([&](auto X) {
@@ -408,40 +414,46 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    read_a(I, Int<2>{}, Int<2>{});
+    read(Int<2>{});
     step(Int<0>{}, Int<-1>{}, Int<0>{}, Int<0>{});
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));         // B and A 0 .. 2 are read
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_a(I, Int<3>{}, Int<3>{});
+    read(Int<3>{});
     step(Int<1>{}, Int<Codes ? 0 : -1>{}, Int<4>{}, Int<Codes ? 0 : 2>{});
-    read_a(I, Int<0>{}, Int<4>{});
+    read(Int<4>{});
     step(Int<2>{}, Int<Codes ? 1 : -1>{}, Int<6>{}, Int<Codes ? 0 : 2>{});
     recode(Int<0>{});
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, ReadsA + (Codes ? 1 : 0)));   // A 3 is read
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_a(I, Int<1>{}, Int<5>{});
+    read(Int<5>{});
     step(Int<3>{}, Int<Codes ? 2 : -1>{}, Int<0>{}, Int<1>{});
-    read_a(I, Int<2>{}, Int<6>{});
-    step(Int<4>{}, Int<Codes ? 3 : -1>{}, Int<2>{}, Int<1>{});
-    recode(Int<1>{});
-    read_a(I, Int<3>{}, Int<7>{});
-    step(Int<5>{}, Int<-1>{}, Int<0>{}, Int<0>{});
+    if constexpr (FM == 8) {
+      read(Int<6>{});
+      step(Int<4>{}, Int<Codes ? 3 : -1>{}, Int<2>{}, Int<1>{});
+      recode(Int<1>{});
+      read(Int<7>{});
+      step(Int<5>{}, Int<-1>{}, Int<0>{}, Int<0>{});
+    } else {
+      issue(I, Int<2>{}, s);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_a(Next{}, Int<0>{}, Int<0>{});
-    read_a(Next{}, Int<1>{}, Int<1>{});
+    constexpr int X = FM - 2, Y = FM - 1;                      // the last two block rows
+    read_a(Next{}, Int<(FM + Off) % 4>{}, Int<0>{});
+    read_a(Next{}, Int<(FM + 1 + Off) % 4>{}, Int<1>{});
     for_each<4>([&](auto J) {
-      mma(Int<6>{}, Int<2>{}, Int<0>{}, J);
-      mma(Int<7>{}, Int<3>{}, Int<0>{}, J);
-      mma(Int<6>{}, Int<2>{}, Int<1>{}, J);
-      mma(Int<7>{}, Int<3>{}, Int<1>{}, J);
+      for_each<2>([&](auto S) {
+        mma(Int<X>{}, Int<(X + Off) % 4>{}, S, J);
+        mma(Int<Y>{}, Int<(Y + Off) % 4>{}, S, J);
+      });
       read_b(Next{}, J);
       if constexpr (J == 1) issue(I, Int<1>{}, s);
-      if constexpr (J == 2) issue(I, Int<3>{}, s);
-      for_each<4>([&](auto X) {
+      if constexpr (J == 2 && FM == 8) issue(I, Int<3>{}, s);
+      for_each<4>([&](auto) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, (J == 0 ? 3 : 1) * (ReadsA / 2) / 2, 0);
       });
@@ -485,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       issue(I, Int<0>{}, s);
       issue(I, Int<2>{}, s);
       issue(I, Int<1>{}, s);
-      issue(I, Int<3>{}, s);
+      if constexpr (FM == 8) issue(I, Int<3>{}, s);
     });
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 + Loads, 15));
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(Rest / 2 + Loads, 15));
   }
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
@@ -497,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
 
   while (item >= 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
     for (int k = now.k0; k < now.k1; k += 2) {
@@ -505,14 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       stage(Int<1>{}, k + 1, now, next);
     }
     Spot at;
-    at.lrow = 128 * wm + r16;
+    at.lrow = 16 * wm + r16;
     at.lcol = 64 * wn + (BK == kAlong ? 16 : 4) * g;
     at.bn = kTile;
-    at.row0 = (int64_t)now.tm * kTile + at.lrow;
+    at.step = 32;
+    at.row0 = (int64_t)now.tm * BM + at.lrow;
     at.col0 = (int64_t)now.tn * kTile + at.lcol;
     at.group = (int64_t)now.tn * (kTile / 64) + wn;
     at.to = now.part < 0 ? nullptr
-                         : t.split_ws + ((int64_t)now.split_tile * t.parts + now.part) * (kTile * kTile);
+                         : t.split_ws + ((int64_t)now.split_tile * t.parts + now.part) * (BM * kTile);
     epi.template store<BK == kAlong>(acc, at, t.m, t.n);
     item = item_at(round);
     now = next;
@@ -566,7 +579,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int item = xcd_band(blockIdx.x, gridDim.x);
   const bool split = item >= t.full;
   const int s_ = split ? item - t.full : 0;
-  const int split_tile = s_ / t.parts, part = s_ - split_tile * t.parts;
+  const int part = split ? s_ / t.split : 0, split_tile = split ? s_ - part * t.split : 0;
   int m_, n_;
   tile_at(split ? t.full + split_tile : item, t.tiles_m, t.tiles_n, &m_, &n_);
   const int tm = __builtin_amdgcn_readfirstlane(m_), tn = __builtin_amdgcn_readfirstlane(n_);
@@ -753,6 +766,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   at.lrow = 16 * FM * wm + r16;
   at.lcol = 64 * wn + (BK == kAlong ? 16 : 4) * g;
   at.bn = BN;
+  at.step = 16;
   at.row0 = m0 + at.lrow;
   at.col0 = n0 + at.lcol;
   at.group = (int64_t)tn * WN + wn;
@@ -773,8 +787,8 @@ inline TileArgs tile_args(const ProductPlan& p, Operand a, Operand b, int64_t m,
   t.m = m;
   t.n = n;
   t.K = K;
-  t.bm = tile_rows(p.shape);
-  t.bn = tile_cols(p.shape);
+  t.bm = tile_rows(p.tile);
+  t.bn = tile_cols(p.tile);
   t.tiles_m = (int)((m + t.bm - 1) / t.bm);
   t.tiles_n = (int)((n + t.bn - 1) / t.bn);
   t.units = (int)units_of(K);
@@ -787,18 +801,21 @@ inline TileArgs tile_args(const ProductPlan& p, Operand a, Operand b, int64_t m,
 template <Kind AK, Kind BK, typename Epi>
 void tile_launch(const ProductPlan& p, TileArgs t, const Epi& epi, hipStream_t stream) {
   const int64_t items = p.full + p.split * p.parts, cus = compute_units();
-  if (p.shape == kTile256) {
-    // Codes are loaded three stages ahead, which has to stay within the next tile.
-    if (BK == kCodes && t.units < 2) t.units = 2;
-    bf16_tile_kernel<AK, BK, Epi><<<dim3((unsigned)(items < cus ? items : cus)), dim3(kThreads), 0, stream>>>(t, epi);
-    return;
+  const dim3 most((unsigned)(items < cus ? items : cus)), all((unsigned)items);
+  switch (p.tile) {
+    case k256x256:
+      // Codes are loaded three stages ahead, which has to stay within the next tile.
+      if (BK == kCodes && t.units < 2) t.units = 2;
+      bf16_tile_kernel<AK, BK, Epi, 8><<<most, dim3(kThreads), 0, stream>>>(t, epi);
+      break;
+    case k192x256:
+      if constexpr (AK == kAlong) bf16_tile_kernel<AK, BK, Epi, 6><<<most, dim3(kThreads), 0, stream>>>(t, epi);
+      break;
+    case k64x128:
+      if constexpr (AK == kAlong) bf16_ring_kernel<AK, BK, Epi, 2, 2, 2><<<all, dim3(256), 0, stream>>>(t, epi);
+      break;
+    default: bf16_ring_kernel<AK, BK, Epi, 4, 2, 2><<<all, dim3(512), 0, stream>>>(t, epi);
   }
-  const dim3 grid((unsigned)items);
-  if constexpr (AK == kAlong) {
-    if (p.shape == kTile64)
-      return (void)(bf16_ring_kernel<AK, BK, Epi, 2, 2, 2><<<grid, dim3(256), 0, stream>>>(t, epi));
-  }
-  bf16_ring_kernel<AK, BK, Epi, 4, 2, 2><<<grid, dim3(512), 0, stream>>>(t, epi);
 }
 
 }  // namespace tiles

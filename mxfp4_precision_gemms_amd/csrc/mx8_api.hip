@@ -246,7 +246,7 @@ bool wgrad_mx8_fits(int64_t T, int64_t Din, int64_t Dout) {
 }
 size_t wgrad_mx8_bytes(int64_t T, int64_t Din, int64_t Dout) {
   if (T < 0 || Din < 1 || Dout < 1 || !wgrad_mx8_fits(T, Din, Dout)) return 0;
-  return tile_product_bytes(Dout, Din, T, false);
+  return wgrad_mx8_ws_bytes(T, Din, Dout);
 }
 
 adahop_status wgrad_mx8(const adahop_gemm_wgrad_mx8_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {

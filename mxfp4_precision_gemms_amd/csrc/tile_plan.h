@@ -4,43 +4,55 @@
 
 #include <cstdint>
 
-#include "linear_plan.h"
-
 namespace adahop {
 namespace tiles {
 
-// Tiles of 256 x 256, or of 128 or 64 rows by 128 columns (an operand A across K:
-// 256 or 128 rows).
-constexpr int tile_rows(TileShape s) { return 256 >> s; }
-constexpr int tile_cols(TileShape s) { return s == kTile256 ? 256 : 128; }
+// How an operand lies: along K, across it, or across it in MXFP8 (B alone).
+enum Kind { kAlong = 0, kAcross = 1, kCodes = 2 };
+
+// Rows x columns. An operand A across K takes the first and the third alone.
+enum Tile { k256x256 = 0, k192x256 = 1, k128x128 = 2, k64x128 = 3 };
+constexpr int tile_rows(Tile s) { return s == k256x256 ? 256 : s == k192x256 ? 192 : s == k128x128 ? 128 : 64; }
+constexpr int tile_cols(Tile s) { return s == k256x256 || s == k192x256 ? 256 : 128; }
 
 // Tiles 0 .. full - 1 are whole, the `split` after them are each formed in `parts`
 // parts of K.
 struct ProductPlan {
-  TileShape shape;
+  Tile tile;
   int64_t full, split;
   int parts;
   double us;                 // estimate
 };
 
-inline ProductPlan product_plan(int64_t m, int64_t n, int64_t K, bool along, bool splits, int64_t cus) {
+// Estimates in microseconds from measurements on the whole device (256 CUs): a
+// launch and a tile's first loads and epilogue 5, a stage of K as below; parts of
+// K a second launch and their sums written and read at 4.5 TB/s. The last round
+// of tiles is split where it leaves half of the compute units or more without
+// one. Up to 128 rows the small tiles alone: what binds there is B's way from
+// memory, which four slots keep busier than two (1 x 131072 x 4096: 192 us with
+// 64 x 128 tiles, 206 with 128 x 128, 260 with 256 x 256).
+inline ProductPlan product_plan(int64_t m, int64_t n, int64_t K, Kind a, Kind b, bool splits, int64_t cus) {
   ProductPlan best{};
   best.us = 1e30;
   const int64_t units = (K + 127) / 128;
-  for (const TileShape shape : {kTile256, kTile128, kTile64}) {
-    if (!along && shape > kTile128) break;
-    const int64_t bm = tile_rows(shape), bn = tile_cols(shape);
+  for (const Tile tile : {k256x256, k192x256, k128x128, k64x128}) {
+    if (a != kAlong && (tile == k192x256 || tile == k64x128)) continue;
+    if (a == kAlong && m <= 128 && tile < k128x128) continue;
+    const int64_t bm = tile_rows(tile), bn = tile_cols(tile);
     const int64_t all = ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
-    const double stage = shape == kTile256 ? 1.0 : shape == kTile128 ? 0.4 : 0.35;
+    const double stage = tile == k256x256 ? 1.1 : tile == k192x256 ? 0.86
+                         : tile == k64x128 ? 0.4 : b == kCodes ? 0.8 : a == kAcross ? 0.6 : 0.46;
     const int64_t rem = all % cus;
     int64_t parts = splits && rem > 0 ? cus / rem : 1;
     if (parts > units / 4) parts = units / 4;
     if (parts > 32) parts = 32;
-    ProductPlan p{shape, all, 0, 1, 0};
-    if (parts >= 2) p = {shape, all - rem, rem, (int)parts, 0};
+    ProductPlan p{tile, all, 0, 1, 0};
+    if (parts >= 2) p = {tile, all - rem, rem, (int)parts, 0};
     const int64_t rounds = (p.full + cus - 1) / cus;
     p.us = 5 + stage * 2 * (double)units * (double)rounds;
-    if (p.split) p.us += 5 + stage * 2 * (double)((units + p.parts - 1) / p.parts);
+    if (p.split)
+      p.us += 4 + stage * 2 * (double)((units + p.parts - 1) / p.parts) +
+              p.parts * ((double)p.split / (double)all) * (double)m * (double)n * 8 / 4.5e6;
     if (p.us < best.us) best = p;
   }
   return best;

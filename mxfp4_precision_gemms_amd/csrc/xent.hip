@@ -57,7 +57,7 @@ struct StatsEpi {
     const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int64_t r = at.row0 + 16 * i;
+      const int64_t r = at.row0 + at.step * i;
       float z[16], top = kMinusInf;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -103,7 +103,7 @@ struct GradEpi {
     const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int64_t r = at.row0 + 16 * i;
+      const int64_t r = at.row0 + at.step * i;
       if (r < m) {
         const float less = lse[r];
         const int64_t t = y.at(r);
@@ -194,7 +194,7 @@ adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, 
   float2* part = static_cast<float2*>(ws);
   float* said = reinterpret_cast<float*>(static_cast<char*>(ws) +
                                          align_up(sizeof(float2) * (size_t)groups_of(a.V) * (size_t)a.T, kAlign));
-  const ProductPlan plan = product_plan(a.T, a.V, a.D, true, false, compute_units());
+  const ProductPlan plan = product_plan(a.T, a.V, a.D, kAlong, kAlong, false, compute_units());
   const TileArgs t = tile_args(plan, along(a.h, a.ldh), along(a.w, a.ldw), a.T, a.V, a.D);
   tile_launch<kAlong, kAlong>(plan, t, StatsEpi{a.scale, y, part, said}, stream);
   const adahop_status st = check_launch("xent");
@@ -236,7 +236,7 @@ BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, 
   const int64_t last = V - (l.p.count - 1) * l.p.size;
   size_t split = 0;
   for (const int64_t n : {l.p.size < V ? l.p.size : V, last}) {
-    const size_t s = dh ? tile_product_bytes(T, D, n, true) : 0, u = dw ? tile_product_bytes(n, D, T, false) : 0;
+    const size_t s = dh ? tile_product_bytes(T, D, n, kAlong, kAcross) : 0, u = dw ? tile_product_bytes(n, D, T, kAcross, kAcross) : 0;
     split = split > s ? split : s;
     split = split > u ? split : u;
   }
@@ -267,7 +267,7 @@ adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t
   for (int64_t q = 0; q < l.p.count; ++q) {
     const int64_t v0 = q * l.p.size, n = a.V - v0 < l.p.size ? a.V - v0 : l.p.size;
     const uint16_t* w = a.w + v0 * a.ldw;
-    const ProductPlan plan = product_plan(a.T, n, a.D, true, false, compute_units());
+    const ProductPlan plan = product_plan(a.T, n, a.D, kAlong, kAlong, false, compute_units());
     const TileArgs t = tile_args(plan, along(a.h, a.ldh), along(w, a.ldw), a.T, n, a.D);
     tile_launch<kAlong, kAlong>(plan, t, GradEpi{a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, l.p.size}, stream);
     adahop_status st = check_launch("xent_backward logits");

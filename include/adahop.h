@@ -766,15 +766,16 @@ ADAHOP_API adahop_status adahop_xent(const adahop_xent_args* args, void* ws, siz
  * dloss of a row that is left out does not count; its dlse does. dh and dw are
  * bf16 or fp32; either may be NULL. The logits are formed again, `piece` entries
  * of the vocabulary at a time (0: as many as keep g within 1 GiB; rounded up to a
- * multiple of 256, at most 2^21); g of a piece is held in bf16, sums are fp32,
+ * multiple of 256); g of a piece is held in bf16, sums are fp32,
  * dh and dw are rounded once. Needs
  * adahop_xent_backward_args_workspace_size(args) bytes of 16-byte aligned
- * workspace (0 for arguments that the call refuses): 2 * rows * piece for g, dh
+ * workspace (0 for arguments that the call refuses): 2 * rows * piece (rows
+ * rounded up to a multiple of 64) for g, dh
  * in fp32 where there are several pieces, and the parts of products split over
  * their sums.
  * Errors: as adahop_xent, and INVALID for NULL lse or dloss (rows > 0), dh and dw
  * both NULL (rows > 0), ld_dh or ld_dw below dim, a bad dtype, piece < 0; UNSUPPORTED for
- * rows * dim of 2^46 and more. */
+ * rows of 2^22 and more. */
 typedef struct {
   int64_t rows, vocab, dim;
   const uint16_t* h; int64_t ld_h;

@@ -266,13 +266,15 @@ adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, bool e
 // along K ([m][K]) or across it ([K][m]), B across ([K][n]), or, with A across,
 // in MXFP8 across ([K][n] codes, scales per 32 columns). Leading dimensions of
 // operands in bytes, those of bf16 multiples of 16 and below 8 MB; 16-byte
-// aligned; K of an A along it may end inside 16 bytes if what follows in them is
-// finite; n a multiple of 8 (codes: 32), m of an A across it likewise, or A's
-// rows reach to the next multiple; m, n, K below 2^30, m * n below 2^46. ws:
+// aligned; K of an A along it may end inside 16 bytes if zeros follow in them; n a
+// multiple of 8 (codes: 32), m of an A across it likewise, or A's rows reach to the
+// next multiple; an A in chunks of 64 columns has zeros from row K up to a multiple
+// of 64, and 4 chunks are below 2 GB; m, n, K below 2^30, m * n below 2^46. ws:
 // tile_product_bytes(...) bytes.
 struct TileOperand {
   const void* p;
   int64_t ld;
+  int64_t chunk;             // A: bytes from 64 columns to the next 64 (128: plain rows)
   const uint8_t* scales;
   int64_t ld_scales;
   int kind;                  // tiles::Kind

@@ -132,8 +132,8 @@ size_t tile_product_bytes(int64_t m, int64_t n, int64_t K, int a, int b) {
 adahop_status tile_product_launch(const TileOperand& a, const TileOperand& b, int64_t m, int64_t n, int64_t K,
                                   const TileOut& out, float* ws, hipStream_t stream) {
   const ProductPlan plan = plan_of(m, n, K, a.kind, b.kind);
-  TileArgs t = tile_args(plan, {static_cast<const uint8_t*>(a.p), a.ld, a.scales, a.ld_scales},
-                         {static_cast<const uint8_t*>(b.p), b.ld, b.scales, b.ld_scales}, m, n, K);
+  TileArgs t = tile_args(plan, {static_cast<const uint8_t*>(a.p), a.ld, a.chunk, a.scales, a.ld_scales},
+                         {static_cast<const uint8_t*>(b.p), b.ld, b.chunk, b.scales, b.ld_scales}, m, n, K);
   t.split_ws = ws;
   const StoreEpi epi = {out.p, out.ld, out.f32, out.prev, out.ld_prev};
   if (b.kind == kCodes) tile_launch<kAcross, kCodes>(plan, t, epi, stream);
@@ -151,7 +151,7 @@ size_t wgrad_mx8_ws_bytes(int64_t T, int64_t Din, int64_t Dout) {
 
 adahop_status wgrad_mx8_launch(const uint16_t* gy, int64_t ldgy, const Mx8Matrix& x, int64_t T, int64_t Din,
                                int64_t Dout, void* out, int out_f32, int64_t ldo, float* ws, hipStream_t stream) {
-  return tile_product_launch({gy, 2 * ldgy, nullptr, 0, kAcross}, {x.codes, x.ldc, x.scales, x.lds, kCodes}, Dout, Din,
+  return tile_product_launch({gy, 2 * ldgy, 128, nullptr, 0, kAcross}, {x.codes, x.ldc, 0, x.scales, x.lds, kCodes}, Dout, Din,
                              T, {out, ldo, out_f32, nullptr, 0}, ws, stream);
 }
 

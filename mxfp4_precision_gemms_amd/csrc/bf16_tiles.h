@@ -77,6 +77,7 @@ constexpr int kGroupM = 8;                 // tile rows that run together on one
 struct Operand {
   const uint8_t* p;
   int64_t ld;                // bytes from a row to the next
+  int64_t chunk;             // bf16: bytes from 64 columns to the next 64 (128: plain rows)
   const uint8_t* scales;     // kCodes: a byte per 32 columns
   int64_t ld_scales;
 };
@@ -124,16 +125,17 @@ struct Spot {
 __device__ __forceinline__ int64_t chunks(int64_t n) { return 2 * ((n + 7) & ~(int64_t)7); }
 // A stage's rows of an operand: the descriptor starts at its first byte and ends
 // with its last, so that rows and K-rows past the ends read as 0. p: the tile's
-// first byte at k = 0; bytes: from there to the end of the tile's rows (across
-// K: of one K-row); left: elements of K from the stage's first.
+// first byte at k = 0; span: bytes of the tile's rows (across K: columns) but for
+// the last one's own; left: elements of K from the stage's first.
 template <Kind K>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t source_of(const uint8_t* p, int bytes, int64_t ld, int k, int left) {
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t source_of(const uint8_t* p, int span, int64_t ld, int64_t chunk, int k,
+                                                            int left) {
   if constexpr (K == kAlong) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + (int64_t)128 * k), 0,
-                                             left > 0 ? bytes - 128 * k : 0, kBufferFlags);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + chunk * k), 0,
+                                             left > 0 ? span + (int)chunks(left) : 0, kBufferFlags);
   } else {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + (int64_t)kStageK * k * ld), 0,
-                                             left > 0 ? (left - 1) * (int)ld + bytes : 0, kBufferFlags);
+                                             left > 0 ? (left - 1) * (int)ld + span : 0, kBufferFlags);
   }
 }
 // Elements of K from stage k's first, at most a stage.
@@ -141,15 +143,17 @@ __device__ __forceinline__ int left_at(int64_t K, int k) {
   const int64_t rest = K - (int64_t)kStageK * k;
   return (int)(rest < 0 ? 0 : rest < kStageK ? rest : kStageK);
 }
-// First byte of a tile's rows r0 .. and their extent, as source_of takes them.
+// First byte of a tile's rows r0 .. (a multiple of 64) and their span, as source_of
+// takes them.
 template <Kind K>
 __device__ __forceinline__ const uint8_t* tile_base(const Operand& o, int64_t r0) {
-  return K == kAlong ? o.p + r0 * o.ld : o.p + (K == kCodes ? 1 : 2) * r0;
+  return K == kAlong ? o.p + r0 * o.ld : K == kCodes ? o.p + r0 : o.p + r0 / 64 * o.chunk;
 }
 template <Kind K>
-__device__ __forceinline__ int tile_bytes(const Operand& o, int64_t rows, int64_t depth) {
-  if constexpr (K == kAlong) return (int)((rows - 1) * o.ld + chunks(depth));
-  else return (int)(K == kCodes ? rows : chunks(rows));
+__device__ __forceinline__ int tile_span(const Operand& o, int64_t rows) {
+  if constexpr (K == kAlong) return (int)((rows - 1) * o.ld);
+  else if constexpr (K == kCodes) return (int)rows;
+  else return (int)((rows - 1) / 64 * o.chunk + chunks((rows - 1) % 64 + 1));
 }
 // 16 K-rows' elements of a lane's column, transposed on their way from LDS: two
 // runs of four K-rows, `next` bytes apart.
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     const uint8_t* a;
     const uint8_t* b;
     const uint8_t* scales;
-    int a_bytes, b_bytes;
+    int a_span, b_span;
   };
   auto place = [&](int item) {
     // Without an item: a stage past the end of any K.
@@ -249,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     const int64_t m0 = (int64_t)p.tm * BM, n0 = (int64_t)p.tn * kTile;
     p.a = tile_base<AK>(t.a, m0);
     p.b = tile_base<BK>(t.b, n0);
-    p.a_bytes = tile_bytes<AK>(t.a, t.m - m0 < BM ? t.m - m0 : BM, t.K);
-    p.b_bytes = tile_bytes<BK>(t.b, t.n - n0 < kTile ? t.n - n0 : kTile, t.K);
+    p.a_span = tile_span<AK>(t.a, t.m - m0 < BM ? t.m - m0 : BM);
+    p.b_span = tile_span<BK>(t.b, t.n - n0 < kTile ? t.n - n0 : kTile);
     if constexpr (BK == kCodes) p.scales = t.b.scales + n0 / 32;
     return p;
   };
@@ -268,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     Source s;
     s.left = left_at(t.K, at);
     const int kk = s.left > 0 ? at : 0;
-    s.a = source_of<AK>(in ? now.a : next.a, in ? now.a_bytes : next.a_bytes, t.a.ld, kk, s.left);
-    s.b = source_of<BK>(in ? now.b : next.b, in ? now.b_bytes : next.b_bytes, t.b.ld, kk, s.left);
+    s.a = source_of<AK>(in ? now.a : next.a, in ? now.a_span : next.a_span, t.a.ld, t.a.chunk, kk, s.left);
+    s.b = source_of<BK>(in ? now.b : next.b, in ? now.b_span : next.b_span, t.b.ld, 128, kk, s.left);
     if constexpr (BK == kCodes)
-      s.scales = source_of<BK>(in ? now.scales : next.scales, (in ? now.b_bytes : next.b_bytes) / 32, t.b.ld_scales,
+      s.scales = source_of<BK>(in ? now.scales : next.scales, (in ? now.b_span : next.b_span) / 32, t.b.ld_scales, 0,
                                kk, s.left);
     return s;
   };
@@ -286,11 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   const int ka = 4 * wave + (lane >> 4), kb = 2 * wave + (lane >> 5);
   const int ga = ((lane & 15) >> 1) ^ ((ka & 3) + 4 * ((ka >> 3) & 1));
   const int gb0 = ((lane & 31) >> 1) ^ ((kb & 3) + 4 * ((kb >> 3) & 1));
+  const int chunk_a = BK == kCodes ? 128 : (int)t.a.chunk;   // beside codes, A lies in plain rows
   const int rowa = 32 * (wave >> 1) + 8 * (wave & 1) + (lane >> 3);
   // The second half holds, of 6 block rows, two: 16 rows of each wave row.
   const int rowr = FM == 8 ? 128 + rowa : 128 + 32 * ((wave >> 1) & 1) + 16 * (wave >> 2) + 8 * (wave & 1) + (lane >> 3);
   const int oa = AK == kAlong ? rowa * (int)t.a.ld + 16 * ca
-                              : ka * (int)t.a.ld + 64 * (ga & 3) + 32 * (ga >> 2) + 16 * (lane & 1);
+                              : ka * (int)t.a.ld + ((ga & 3) >> 1) * chunk_a + 64 * (ga & 1) + 32 * (ga >> 2) +
+                                    16 * (lane & 1);
   const int orest = rowr * (int)t.a.ld + 16 * ca;
   // Codes: two runs of 16 of a stage a thread, K-rows 32 u + thread / 16.
   const int kc = threadIdx.x >> 4, gc = threadIdx.x & 15;
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     if constexpr (q < 4) {
       int v;
       if constexpr (AK == kAlong) v = 8 * ca < s.left ? (q % 2 == 0 ? oa : orest) + 16 * (q / 2) * (int)t.a.ld : kPastEnd;
-      else v = oa + 32 * (q / 2) * (int)t.a.ld + 256 * (q % 2);
+      else v = oa + 32 * (q / 2) * (int)t.a.ld + 2 * (q % 2) * chunk_a;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)(half(I, Int<q % 2>{}) + 1024 * (8 * (q / 2) + wave)),
                                                16, v, 0, 0, 0);
     } else if constexpr (BK == kCodes) {
@@ -589,8 +595,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const uint8_t* base_a = tile_base<AK>(t.a, m0);
   const uint8_t* base_b = tile_base<BK>(t.b, n0);
-  const int bytes_a = tile_bytes<AK>(t.a, t.m - m0 < BM ? t.m - m0 : BM, t.K);
-  const int bytes_b = tile_bytes<BK>(t.b, t.n - n0 < BN ? t.n - n0 : BN, t.K);
+  const int span_a = tile_span<AK>(t.a, t.m - m0 < BM ? t.m - m0 : BM);
+  const int span_b = tile_span<BK>(t.b, t.n - n0 < BN ? t.n - n0 : BN);
 
   // ---- loads --------------------------------------------------------------------
   struct Source {
@@ -601,10 +607,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
     Source s;
     s.left = k < k1 ? left_at(t.K, k) : 0;
     const int kk = s.left > 0 ? k : 0;
-    s.a = source_of<AK>(base_a, bytes_a, t.a.ld, kk, s.left);
-    s.b = source_of<BK>(base_b, bytes_b, t.b.ld, kk, s.left);
+    s.a = source_of<AK>(base_a, span_a, t.a.ld, t.a.chunk, kk, s.left);
+    s.b = source_of<BK>(base_b, span_b, t.b.ld, 128, kk, s.left);
     if constexpr (BK == kCodes)
-      s.scales = source_of<BK>(t.b.scales + n0 / 32, bytes_b / 32, t.b.ld_scales, kk, s.left);
+      s.scales = source_of<BK>(t.b.scales + n0 / 32, span_b / 32, t.b.ld_scales, 0, kk, s.left);
     return s;
   };
   // Load q of an operand along K: rows 8 (Waves q + wave) + lane / 8; across:
@@ -635,8 +641,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   auto load_a = [&](auto I, auto Q, const Source& s) __attribute__((always_inline)) {
     constexpr int q = decltype(Q)::value;
     int v;
-    if constexpr (AK == kAlong) v = 8 * ca < s.left ? oa + 8 * Waves * q * (int)t.a.ld : kPastEnd;
-    else v = oa + 32 * (gx ^ (4 * ((Waves / 2 * q) & 1))) + 4 * Waves * q * (int)t.a.ld;
+    if constexpr (AK == kAlong) {
+      v = 8 * ca < s.left ? oa + 8 * Waves * q * (int)t.a.ld : kPastEnd;
+    } else {
+      const int c = gx ^ (4 * ((Waves / 2 * q) & 1));      // 16 columns
+      v = oa + (c >> 2) * (int)t.a.chunk + 32 * (c & 3) + 4 * Waves * q * (int)t.a.ld;
+    }
     __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)(pa(I) + 1024 * (Waves * q + wave)), 16, v, 0, 0, 0);
   };
   auto load_b = [&](auto I, auto Q, const Source& s) __attribute__((always_inline)) {

@@ -271,6 +271,8 @@ adahop_status wgrad_mx8(const adahop_gemm_wgrad_mx8_args* a, void* ws, size_t ws
 }
 
 // ---- cross entropy ------------------------------------------------------------
+constexpr int64_t kMaxBackRows = int64_t{1} << 22;  // 4 chunks of g below 2 GB
+
 // What both calls ask of their common arguments.
 template <typename Args>
 adahop_status check_xent(const Args& a) {
@@ -311,7 +313,7 @@ adahop_status xent(const adahop_xent_args* a, void* ws, size_t ws_bytes, hipStre
 adahop_status check_xent_back(const adahop_xent_backward_args& a) {
   ADAHOP_TRY(check_xent(a));
   if (a.rows > 0 && !a.dh && !a.dw) return invalid("xent_backward: neither dh nor dw");
-  if (!tiles_fit(a.rows, a.dim)) return unsupported("xent_backward: rows * dim of 2^46 or more");
+  if (a.rows >= kMaxBackRows) return unsupported("xent_backward: rows of 2^22 or more");
   if ((a.dh && (a.ld_dh < a.dim || !valid_dtype(a.dh_dtype))) ||
       (a.dw && (a.ld_dw < a.dim || !valid_dtype(a.dw_dtype))))
     return invalid("xent_backward: leading dimension of dh or dw below dim, or a bad dtype");

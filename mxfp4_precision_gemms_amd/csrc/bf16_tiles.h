@@ -1,19 +1,28 @@
-// Products of bf16 operands in 256 x 256 tiles fed through LDS, with an
-// epilogue of the caller's (gfx950): C[i, j] = sum_k A(i, k) B(j, k) in fp32.
+// Products of bf16 operands in tiles fed through LDS, with an epilogue of the
+// caller's (gfx950): C[i, j] = sum_k A(i, k) B(j, k) in fp32.
 //
 // An operand lies along K ([rows][K], row-major) or across it ([K][rows]); B
 // may also be MXFP8 codes and scales across K, widened to bf16 on their way into
 // LDS. Any sizes; K of an operand along it in 16-byte chunks, rows of one
 // across it too (the caller checks).
 //
-// A workgroup of 8 waves, two a SIMD, computes a tile, a wave 128 x 64 of it as
-// 8 x 4 blocks of v_mfma_f32_16x16x32_bf16 (B first, so that a lane holds four
-// neighbouring columns of a row). K advances 64 elements a stage through two
-// LDS slots of 64 KB. A slot's parts are refilled with the stage after next as
-// soon as all waves have read them: B after the first block row, A's halves
-// after the fourth and the last, so that every load has more than a stage of
-// time. Workgroups stay: the next tile's first stages are loaded during a tile's
-// last ones and its epilogue.
+// Large tiles, 256 (192) x 256: a workgroup of 8 waves, two a SIMD, a wave 128
+// (96) x 64 of it as 8 (6) x 4 blocks of v_mfma_f32_16x16x32_bf16 (B first, so that
+// a lane holds four neighbouring columns of a row). K advances 64 elements a
+// stage through two LDS slots of 64 (56) KB. A slot is refilled with the stage
+// after next in two parts, as soon as all waves have read them: B and the first
+// half of A after the second block row, the other half after the last but two,
+// so that every load has more than a stage of time for two barriers a stage (one
+// refill a stage leaves the matrix cores waiting; three, with B's own barrier,
+// were 1 % slower). LDS reads and loads are spread between the matrix
+// instructions: issued together they hold up the wave's own (operands across K:
+// 5 % of the time). Workgroups stay: the next tile's first stages are loaded
+// during a tile's last ones and its epilogue.
+//
+// Measured, 4.4e12 operations each: 8192 x 4096 x 65536 with A along K and B
+// across 1420 .. 1450 TFLOP/s, 65536 x 4096 x 8192 with both across 1390 .. 1440;
+// the matrix cores busy 75 % of the time at 1.66 .. 1.77 GHz, the clock that the
+// power limit leaves (16x16x32 and 32x32x16 blocks alike).
 //
 // LDS of an operand along K: rows of 128 bytes, the 16-byte chunks XORed with
 // row bits so that the 16 rows which a quarter of a wave reads at one chunk lie
@@ -393,55 +402,49 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     constexpr int Off = (FM * decltype(I)::value) % 4;
     auto read = [&](auto R) { read_a(I, Int<(decltype(R)::value + Off) % 4>{}, R); };
     const Source s = source(k + 2, now, next);
-    // A block row's matrix instructions with its LDS reads, `piece` of the codes'
-    // widening (one LDS write) and loads `First` .. of the stage's between them.
-    auto step = [&](auto R, auto Piece, auto First, auto Count) __attribute__((always_inline)) {
-      constexpr int r = decltype(R)::value, piece = decltype(Piece)::value, count = decltype(Count)::value;
+    // A block row's matrix instructions with its LDS reads, the widening of the
+    // codes' run `Run` (two LDS writes) and `Count` loads from `First` on between
+    // them.
+    auto step = [&](auto R, auto Reads, auto Run, auto First, auto Count) __attribute__((always_inline)) {
+      constexpr int r = decltype(R)::value, run = decltype(Run)::value, count = decltype(Count)::value;
       for_each<2>([&](auto S) { for_each<4>([&](auto J) { mma(R, Int<(r + Off) % 4>{}, S, J); }); });
-      if constexpr (piece >= 0) widen(I, Int<piece / 2>{}, Int<piece % 2>{});
+      if constexpr (run >= 0) for_each<2>([&](auto H) { widen(I, Run, H); });
       for_each<count>([&](auto C) { issue(I, Int<decltype(First)::value + decltype(C)::value>{}, s); });
       for_each<8>([&](auto X) {
         constexpr int x = decltype(X)::value;
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                          // MFMA
-        if constexpr (x < ReadsA) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // DS read
-        if constexpr (piece >= 0) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);                // VALU
-        if constexpr (piece >= 0 && x == 6) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);      // DS write
+        if constexpr (x < decltype(Reads)::value) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // DS read
+        if constexpr (run >= 0) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);                  // VALU
+        if constexpr (run >= 0 && x % 4 == 3) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);    // DS write
         if constexpr (x >= 4 && x - 4 < count) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // VMEM
       });
       __builtin_amdgcn_sched_barrier(0);
     };
     constexpr bool Codes = BK == kCodes;
-    // The codes of run u, a stage further ahead, once both its halves are widened.
-    auto recode = [&](auto U) __attribute__((always_inline)) {
-      if constexpr (Codes) {
-        const Source sb = source(k + 3, now, next);
-        issue(I, Int<4 + 2 * decltype(U)::value>{}, sb);
-        issue(I, Int<5 + 2 * decltype(U)::value>{}, sb);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
     read(Int<2>{});
-    step(Int<0>{}, Int<-1>{}, Int<0>{}, Int<0>{});
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));         // B and A 0 .. 2 are read
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
     read(Int<3>{});
-    step(Int<1>{}, Int<Codes ? 0 : -1>{}, Int<4>{}, Int<Codes ? 0 : 2>{});
-    read(Int<4>{});
-    step(Int<2>{}, Int<Codes ? 1 : -1>{}, Int<6>{}, Int<Codes ? 0 : 2>{});
-    recode(Int<0>{});
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, ReadsA + (Codes ? 1 : 0)));   // A 3 is read
+    step(Int<0>{}, Int<2 * ReadsA>{}, Int<-1>{}, Int<0>{}, Int<0>{});
+    step(Int<1>{}, Int<0>{}, Int<-1>{}, Int<0>{}, Int<0>{});
+    // B and A's first half are read, its second half has landed.
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+    read(Int<4>{});
+    step(Int<2>{}, Int<ReadsA>{}, Int<Codes ? 0 : -1>{}, Int<4>{}, Int<Codes ? 0 : 2>{});
     read(Int<5>{});
-    step(Int<3>{}, Int<Codes ? 2 : -1>{}, Int<0>{}, Int<1>{});
+    step(Int<3>{}, Int<ReadsA>{}, Int<Codes ? 1 : -1>{}, Int<6>{}, Int<Codes ? 0 : 2>{});
+    if constexpr (Codes) {
+      const Source sb = source(k + 3, now, next);
+      for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, sb); });
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if constexpr (FM == 8) {
       read(Int<6>{});
-      step(Int<4>{}, Int<Codes ? 3 : -1>{}, Int<2>{}, Int<1>{});
-      recode(Int<1>{});
+      step(Int<4>{}, Int<ReadsA>{}, Int<-1>{}, Int<0>{}, Int<1>{});
       read(Int<7>{});
-      step(Int<5>{}, Int<-1>{}, Int<0>{}, Int<0>{});
+      step(Int<5>{}, Int<ReadsA>{}, Int<-1>{}, Int<2>{}, Int<1>{});
     } else {
+      issue(I, Int<0>{}, s);
       issue(I, Int<2>{}, s);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -484,15 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     whole(Int<0>{});
     for_each<4>([&](auto Q) { issue(Int<1>{}, Int<4 + Q>{}, s1); });
     whole(Int<1>{});
-    issue(Int<0>{}, Int<4>{}, s2);
-    issue(Int<0>{}, Int<5>{}, s2);
+    for_each<4>([&](auto Q) { issue(Int<0>{}, Int<4 + Q>{}, s2); });
     __builtin_amdgcn_sched_barrier(0);
     issue(Int<1>{}, Int<0>{}, s1);
     issue(Int<1>{}, Int<2>{}, s1);
-    __builtin_amdgcn_sched_barrier(0);
-    issue(Int<0>{}, Int<6>{}, s2);
-    issue(Int<0>{}, Int<7>{}, s2);
-    __builtin_amdgcn_sched_barrier(0);
     issue(Int<1>{}, Int<1>{}, s1);
     issue(Int<1>{}, Int<3>{}, s1);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <initializer_list>
 
 namespace adahop {
 namespace tiles {
@@ -24,6 +25,10 @@ struct ProductPlan {
   double us;                 // estimate
 };
 
+// Columns of B of one row of small tiles: a launch of one tile a workgroup stays
+// far below 2^32 threads.
+constexpr int64_t kMostSmall = int64_t{1} << 28;
+
 // Estimates in microseconds from measurements on the whole device (256 CUs): a
 // launch and a tile's first loads and epilogue 5, a stage of K as below; parts of
 // K a second launch and their sums written and read at 4.5 TB/s. The last round
@@ -37,9 +42,11 @@ inline ProductPlan product_plan(int64_t m, int64_t n, int64_t K, Kind a, Kind b,
   const int64_t units = (K + 127) / 128;
   for (const Tile tile : {k256x256, k192x256, k128x128, k64x128}) {
     if (a != kAlong && (tile == k192x256 || tile == k64x128)) continue;
-    if (a == kAlong && m <= 128 && tile < k128x128) continue;
+    const bool small = tile >= k128x128;
+    if (a == kAlong && m <= 128 && !small && n <= kMostSmall) continue;
     const int64_t bm = tile_rows(tile), bn = tile_cols(tile);
     const int64_t all = ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
+    if (small && all > kMostSmall / 128) continue;
     const double stage = tile == k256x256 ? 1.1 : tile == k192x256 ? 0.86
                          : tile == k64x128 ? 0.4 : b == kCodes ? 0.8 : a == kAcross ? 0.6 : 0.46;
     const int64_t rem = all % cus;

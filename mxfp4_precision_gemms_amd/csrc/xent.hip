@@ -158,24 +158,27 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 __global__ void __launch_bounds__(256) xent_finish_kernel(FinishArgs a) {
   __shared__ float2 red[16][17];
   const int row = threadIdx.x & 15, lane = threadIdx.x >> 4;
-  const int64_t r = (int64_t)blockIdx.x * 16 + row;
-  float2 s = {kMinusInf, 0.0f};
-  if (r < a.rows) {
+  for (int64_t base = (int64_t)blockIdx.x * 16; base < a.rows; base += (int64_t)gridDim.x * 16) {
+    const int64_t r = base + row;
+    float2 s = {kMinusInf, 0.0f};
+    if (r < a.rows) {
 #pragma unroll 8
-    for (int64_t p = lane; p < a.parts; p += 16) s = join(s, a.part[p * a.rows + r]);
-  }
-  red[lane][row] = s;
+      for (int64_t p = lane; p < a.parts; p += 16) s = join(s, a.part[p * a.rows + r]);
+    }
+    red[lane][row] = s;
 #pragma unroll
-  for (int half = 8; half >= 1; half /= 2) {
+    for (int half = 8; half >= 1; half /= 2) {
+      __syncthreads();
+      if (lane < half) red[lane][row] = join(red[lane][row], red[lane + half][row]);
+    }
+    if (lane == 0 && r < a.rows) {
+      s = red[0][row];
+      const float lse = shift_of(s.x) + logf(s.y);
+      const int64_t t = a.y.at(r);
+      a.lse[r] = lse;
+      a.loss[r] = t >= 0 && t < a.vocab ? lse - a.said[r] : 0.0f;
+    }
     __syncthreads();
-    if (lane < half) red[lane][row] = join(red[lane][row], red[lane + half][row]);
-  }
-  if (lane == 0 && r < a.rows) {
-    s = red[0][row];
-    const float lse = shift_of(s.x) + logf(s.y);
-    const int64_t t = a.y.at(r);
-    a.lse[r] = lse;
-    a.loss[r] = t >= 0 && t < a.vocab ? lse - a.said[r] : 0.0f;
   }
 }
 
@@ -205,7 +208,8 @@ adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, 
   const adahop_status st = check_launch("xent");
   if (st != ADAHOP_OK) return st;
   const FinishArgs f = {part, said, y, a.T, a.V, (int64_t)t.tiles_n * (t.bn / 64), loss, lse};
-  xent_finish_kernel<<<dim3((unsigned)((a.T + 15) / 16)), dim3(256), 0, stream>>>(f);
+  const int64_t groups = (a.T + 15) / 16;
+  xent_finish_kernel<<<dim3((unsigned)(groups < 1 << 20 ? groups : 1 << 20)), dim3(256), 0, stream>>>(f);
   return check_launch("xent_finish");
 }
 

@@ -147,10 +147,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t source_of(const uint8_t* p, in
                                              left > 0 ? (left - 1) * (int)ld + span : 0, kBufferFlags);
   }
 }
-// Elements of K from stage k's first, at most a stage.
+// Elements of K from stage k's first, at most a stage. In 32 bits and scalar: what
+// 64-bit comparisons yield lies in vector registers, and a descriptor made from it
+// turns every load into a loop over lanes.
+__device__ __forceinline__ int stages_of(int64_t K) { return ((int)K + kStageK - 1) / kStageK; }   // K below 2^30
 __device__ __forceinline__ int left_at(int64_t K, int k) {
-  const int64_t rest = K - (int64_t)kStageK * k;
-  return (int)(rest < 0 ? 0 : rest < kStageK ? rest : kStageK);
+  const int rest = k < stages_of(K) ? (int)K - kStageK * k : 0;
+  return __builtin_amdgcn_readfirstlane(rest < kStageK ? rest : kStageK);
 }
 // First byte of a tile's rows r0 .. (a multiple of 64) and their span, as source_of
 // takes them.
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int tm = __builtin_amdgcn_readfirstlane(m_), tn = __builtin_amdgcn_readfirstlane(n_);
   const int k0 = __builtin_amdgcn_readfirstlane(split ? 2 * (int)((int64_t)t.units * part / t.parts) : 0);
   const int end = __builtin_amdgcn_readfirstlane(2 * (split ? (int)((int64_t)t.units * (part + 1) / t.parts) : t.units));
-  const int stages = (int)((t.K + kStageK - 1) / kStageK), k1 = end < stages ? end : stages;
+  const int stages = stages_of(t.K), k1 = end < stages ? end : stages;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const uint8_t* base_a = tile_base<AK>(t.a, m0);
   const uint8_t* base_b = tile_base<BK>(t.b, n0);
@@ -622,17 +625,19 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int oa = AK == kAlong ? row8 * (int)t.a.ld + 16 * ca : k4 * (int)t.a.ld + 16 * (lane & 1);
   const int ob = BK == kAlong ? row8 * (int)t.b.ld : k4 * (int)t.b.ld + 16 * (lane & 1);
   const int kc = threadIdx.x >> 3, gc = threadIdx.x & 7;     // + 8 Waves K-rows a run
-  v4i codes[Runs];
-  uint8_t scale[Runs];
+  // A slot's next codes, loaded four stages before they are widened into it.
+  v4i codes[4][Runs];
+  uint8_t scale[4][Runs];
   const int sw = (gc >> 2) & 1;
   auto widen = [&](auto I) __attribute__((always_inline)) {
     for_each<Runs>([&](auto U) {
       constexpr int u = decltype(U)::value;
+      constexpr int slot = decltype(I)::value;
       uint8_t* to = pb(I) + kc * 256 + 32 * (gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1))) + 2048 * Waves * u;
       for_each<2>([&](auto H) {
         const bool last = decltype(H)::value != sw;
         *reinterpret_cast<v4i*>(to + (last ? 16 : 0)) =
-            widen8((uint32_t)(last ? codes[u][2] : codes[u][0]), (uint32_t)(last ? codes[u][3] : codes[u][1]), scale[u]);
+            widen8((uint32_t)(last ? codes[slot][u][2] : codes[slot][u][0]), (uint32_t)(last ? codes[slot][u][3] : codes[slot][u][1]), scale[slot][u]);
       });
     });
   };
@@ -652,10 +657,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
     if constexpr (BK == kCodes) {
       constexpr int u = q / 2;
       if constexpr (q % 2 == 0)
-        codes[u] = __builtin_bit_cast(
+        codes[decltype(I)::value][u] = __builtin_bit_cast(
             v4i, __builtin_amdgcn_raw_buffer_load_b128(s.b, (kc + 8 * Waves * u) * (int)t.b.ld + 16 * gc, 0, 0));
       else
-        scale[u] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, (kc + 8 * Waves * u) * (int)t.b.ld_scales + gc / 2, 0,
+        scale[decltype(I)::value][u] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, (kc + 8 * Waves * u) * (int)t.b.ld_scales + gc / 2, 0,
                                                        0);
     } else {
       int v;
@@ -702,14 +707,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   };
   // Stage k in slot I: enters with its B fragments and its first two A fragments
   // read; leaves with the next stage's. Fragment i of A sits in buffer
-  // (i + Off) % 4. Codes are loaded five stages ahead, a stage before they are
-  // widened into the slot.
+  // (i + Off) % 4. Codes are loaded eight stages ahead, and widened into the slot
+  // after four (a stage ahead they made a stage as long as a load: 0.8 us instead
+  // of 0.XX).
   auto stage = [&](auto I, int k) __attribute__((always_inline)) {
     constexpr int slot = decltype(I)::value;
     using Next = Int<(slot + 1) % 4>;
     constexpr int Off = (FM * slot) % 4;
     const Source s = source(k + 4);
-    const Source sb = BK == kCodes ? source(k + 5) : s;
+    const Source sb = BK == kCodes ? source(k + 8) : s;
     for_each<FM - 2>([&](auto R) {
       constexpr int i = decltype(R)::value;
       read_a(I, Int<(i + 2 + Off) % 4>{}, Int<i + 2>{});
@@ -749,17 +755,29 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-  for_each<4>([&](auto I) {
-    const Source s = source(k0 + I);
-    for_each<LB>([&](auto Q) { load_b(I, Q, s); });
-    if constexpr (BK == kCodes) widen(I);
-    for_each<LA>([&](auto Q) { load_a(I, Q, s); });
-  });
   if constexpr (BK == kCodes) {
-    const Source s = source(k0 + 4);
-    for_each<LB>([&](auto Q) { load_b(Int<0>{}, Q, s); });
+    for_each<4>([&](auto I) {
+      const Source s = source(k0 + I);
+      for_each<LB>([&](auto Q) { load_b(I, Q, s); });
+    });
+    for_each<4>([&](auto I) { widen(I); });
+    __builtin_amdgcn_sched_barrier(0);
+    // From here on in a stage's order, so that the waits for codes are as loose.
+    for_each<4>([&](auto I) {
+      const Source s = source(k0 + I), sb = source(k0 + 4 + I);
+      for_each<LB>([&](auto Q) { load_b(I, Q, sb); });
+      __builtin_amdgcn_sched_barrier(0);
+      for_each<LA>([&](auto Q) { load_a(I, Q, s); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  } else {
+    for_each<4>([&](auto I) {
+      const Source s = source(k0 + I);
+      for_each<LB>([&](auto Q) { load_b(I, Q, s); });
+      for_each<LA>([&](auto Q) { load_a(I, Q, s); });
+    });
   }
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(BK == kCodes ? LA + LB : 3 * Loads, 0));
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * Loads, 0));
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
   read_a(Int<0>{}, Int<0>{}, Int<0>{});

@@ -138,8 +138,8 @@ struct GradEpi {
 };
 
 // ---- joining ------------------------------------------------------------------
-// lse and loss of a row from its parts' maxima and sums: 16 rows a workgroup,
-// 16 lanes a row, lane l taking parts l, l + 16, ...; then the lanes in pairs.
+// lse and loss of a row from its parts' maxima and sums: 256 / Rows lanes a row,
+// lane l taking parts l, l + lanes, ...; then the lanes in pairs.
 struct FinishArgs {
   const float2* part;
   const float* said;
@@ -155,19 +155,21 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   auto shifted = [&](float2 p) { return p.x == kMinusInf ? p.y : p.y * exp_of(shift_of(p.x) - by); };
   return float2{top, shifted(a) + shifted(b)};
 }
+template <int Rows>
 __global__ void __launch_bounds__(256) xent_finish_kernel(FinishArgs a) {
-  __shared__ float2 red[16][17];
-  const int row = threadIdx.x & 15, lane = threadIdx.x >> 4;
-  for (int64_t base = (int64_t)blockIdx.x * 16; base < a.rows; base += (int64_t)gridDim.x * 16) {
+  constexpr int Lanes = 256 / Rows;
+  __shared__ float2 red[Lanes][Rows + 1];
+  const int row = threadIdx.x % Rows, lane = threadIdx.x / Rows;
+  for (int64_t base = (int64_t)blockIdx.x * Rows; base < a.rows; base += (int64_t)gridDim.x * Rows) {
     const int64_t r = base + row;
     float2 s = {kMinusInf, 0.0f};
     if (r < a.rows) {
 #pragma unroll 8
-      for (int64_t p = lane; p < a.parts; p += 16) s = join(s, a.part[p * a.rows + r]);
+      for (int64_t p = lane; p < a.parts; p += Lanes) s = join(s, a.part[p * a.rows + r]);
     }
     red[lane][row] = s;
 #pragma unroll
-    for (int half = 8; half >= 1; half /= 2) {
+    for (int half = Lanes / 2; half >= 1; half /= 2) {
       __syncthreads();
       if (lane < half) red[lane][row] = join(red[lane][row], red[lane + half][row]);
     }
@@ -208,8 +210,13 @@ adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, 
   const adahop_status st = check_launch("xent");
   if (st != ADAHOP_OK) return st;
   const FinishArgs f = {part, said, y, a.T, a.V, (int64_t)t.tiles_n * (t.bn / 64), loss, lse};
-  const int64_t groups = (a.T + 15) / 16;
-  xent_finish_kernel<<<dim3((unsigned)(groups < 1 << 20 ? groups : 1 << 20)), dim3(256), 0, stream>>>(f);
+  // Few rows: more lanes a row (1 row of 500 parts: 7 us with 16 lanes, X with 128).
+  auto groups = [&](int rows) {
+    const int64_t n = (a.T + rows - 1) / rows;
+    return dim3((unsigned)(n < 1 << 20 ? n : 1 << 20));
+  };
+  if (a.T <= 512) xent_finish_kernel<2><<<groups(2), dim3(256), 0, stream>>>(f);
+  else xent_finish_kernel<16><<<groups(16), dim3(256), 0, stream>>>(f);
   return check_launch("xent_finish");
 }
 

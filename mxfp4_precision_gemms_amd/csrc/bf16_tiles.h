@@ -134,26 +134,12 @@ struct Spot {
 __device__ __forceinline__ int64_t chunks(int64_t n) { return 2 * ((n + 7) & ~(int64_t)7); }
 // A stage's rows of an operand: the descriptor starts at its first byte and ends
 // with its last, so that rows and K-rows past the ends read as 0. p: the tile's
-// first byte at k = 0; span: bytes of the tile's rows (across K: columns) but for
+// first byte at the stage's first k; span: bytes of the tile's rows (across K: columns) but for
 // the last one's own; left: elements of K from the stage's first.
 template <Kind K>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t source_of(const uint8_t* p, int span, int64_t ld, int64_t chunk, int k,
-                                                            int left) {
-  if constexpr (K == kAlong) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + chunk * k), 0,
-                                             left > 0 ? span + (int)chunks(left) : 0, kBufferFlags);
-  } else {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + (int64_t)kStageK * k * ld), 0,
-                                             left > 0 ? (left - 1) * (int)ld + span : 0, kBufferFlags);
-  }
-}
-// Elements of K from stage k's first, at most a stage. In 32 bits and scalar: what
-// 64-bit comparisons yield lies in vector registers, and a descriptor made from it
-// turns every load into a loop over lanes.
-__device__ __forceinline__ int stages_of(int64_t K) { return ((int)K + kStageK - 1) / kStageK; }   // K below 2^30
-__device__ __forceinline__ int left_at(int64_t K, int k) {
-  const int rest = k < stages_of(K) ? (int)K - kStageK * k : 0;
-  return __builtin_amdgcn_readfirstlane(rest < kStageK ? rest : kStageK);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t source_of(const uint8_t* p, int span, int64_t ld, int left) {
+  const int bytes = K == kAlong ? span + (int)chunks(left) : (left - 1) * (int)ld + span;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, left > 0 ? bytes : 0, kBufferFlags);
 }
 // First byte of a tile's rows r0 .. (a multiple of 64) and their span, as source_of
 // takes them.
@@ -232,17 +218,23 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     const int cnt = items - base < G ? items - base : G;
     return (int)blockIdx.x < cnt ? base + xcd_band(blockIdx.x, cnt) : -1;
   };
-  // An item's place, all scalar. Stages k0 .. k1 - 1, an even number.
+  // An item's place, all scalar: of its tile, and where its operands' stages start.
+  // rest: elements of K from its first stage's on; end: the same, once its last
+  // stage (of an even number) is taken.
   struct Place {
-    int tm, tn, k0, k1, part, split_tile;
+    int tm, tn, part, split_tile, stages, rest, end;
     const uint8_t* a;
     const uint8_t* b;
     const uint8_t* scales;
     int a_span, b_span;
   };
+  // Bytes from a stage to the next.
+  const uint32_t step_a = (uint32_t)(AK == kAlong ? t.a.chunk : kStageK * t.a.ld);
+  const uint32_t step_b = BK == kAlong ? 128 : (uint32_t)(kStageK * t.b.ld);
+  const uint32_t step_scales = (uint32_t)(kStageK * t.b.ld_scales);
   auto place = [&](int item) {
-    // Without an item: a stage past the end of any K.
-    Place p{0, 0, 1 << 28, 1 << 28, -1, 0, t.a.p, t.b.p, t.b.scales, 0, 0};
+    // Without an item: stages past the end of any K, without an end.
+    Place p{0, 0, -1, 0, 0, 0, 1, t.a.p, t.b.p, t.b.scales, 0, 0};
     if (item < 0) return p;
     int tile = item, part = -1;
     if (item >= t.full) {
@@ -256,41 +248,61 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     p.tm = __builtin_amdgcn_readfirstlane(m_);
     p.tn = __builtin_amdgcn_readfirstlane(n_);
     p.part = __builtin_amdgcn_readfirstlane(part);
-    p.k0 = 0;
-    p.k1 = 2 * t.units;
+    int k0 = 0, k1 = 2 * t.units;
     if (p.part >= 0) {
-      p.k0 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)t.units * p.part / t.parts));
-      p.k1 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)t.units * (p.part + 1) / t.parts));
+      k0 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)t.units * p.part / t.parts));
+      k1 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)t.units * (p.part + 1) / t.parts));
     }
+    p.stages = k1 - k0;
+    p.rest = (int)t.K - kStageK * k0;
+    p.end = (int)t.K - kStageK * k1;
     const int64_t m0 = (int64_t)p.tm * BM, n0 = (int64_t)p.tn * kTile;
-    p.a = tile_base<AK>(t.a, m0);
-    p.b = tile_base<BK>(t.b, n0);
+    p.a = tile_base<AK>(t.a, m0) + (int64_t)k0 * step_a;
+    p.b = tile_base<BK>(t.b, n0) + (int64_t)k0 * step_b;
     p.a_span = tile_span<AK>(t.a, t.m - m0 < BM ? t.m - m0 : BM);
     p.b_span = tile_span<BK>(t.b, t.n - n0 < kTile ? t.n - n0 : kTile);
-    if constexpr (BK == kCodes) p.scales = t.b.scales + n0 / 32;
+    if constexpr (BK == kCodes) p.scales = t.b.scales + n0 / 32 + (int64_t)k0 * step_scales;
     return p;
   };
 
   // ---- loads: this wave's share of a stage ------------------------------------
+  // An operand's stages in the order of their loads. A step on from the last
+  // stage is a few scalar instructions between the matrix instructions of a
+  // stage's first two block rows; descriptors formed anew from k, some 60 in one
+  // run, held the matrix cores up (4 % of the time, beside codes 8 %). Selects keep
+  // the stages free of branches.
+  struct Cursor {
+    const uint8_t* p;
+    const uint8_t* scales;
+    int span, rest, end;
+  };
   struct Source {
-    __amdgpu_buffer_rsrc_t a, b, scales;
+    __amdgpu_buffer_rsrc_t v, scales;
     int left;
   };
-  // Stage k of item `now`, or, past its last, of item `next`: the scalar
-  // selects keep the stages free of branches.
-  auto source = [&](int k, const Place& now, const Place& next) __attribute__((always_inline)) {
-    const bool in = k < now.k1;
-    const int at = in ? k : k - now.k1 + next.k0;
+  // The next stage's descriptors; past an item's last stage, item `next`'s first.
+  auto take = [&](auto IsB, Cursor& c, const Place& next) __attribute__((always_inline)) {
+    constexpr bool Is = decltype(IsB)::value;
+    constexpr Kind K = Is ? BK : AK;
+    const bool over = c.rest == c.end;
+    c.p = over ? (Is ? next.b : next.a) : c.p;
+    c.span = over ? (Is ? next.b_span : next.a_span) : c.span;
+    c.rest = over ? next.rest : c.rest;
+    c.end = over ? next.end : c.end;
     Source s;
-    s.left = left_at(t.K, at);
-    const int kk = s.left > 0 ? at : 0;
-    s.a = source_of<AK>(in ? now.a : next.a, in ? now.a_span : next.a_span, t.a.ld, t.a.chunk, kk, s.left);
-    s.b = source_of<BK>(in ? now.b : next.b, in ? now.b_span : next.b_span, t.b.ld, 128, kk, s.left);
-    if constexpr (BK == kCodes)
-      s.scales = source_of<BK>(in ? now.scales : next.scales, (in ? now.b_span : next.b_span) / 32, t.b.ld_scales, 0,
-                               kk, s.left);
+    s.left = c.rest < kStageK ? c.rest : kStageK;        // none: 0 or less
+    s.v = source_of<K>(c.p, c.span, Is ? t.b.ld : t.a.ld, s.left);
+    c.p += Is ? step_b : step_a;
+    if constexpr (K == kCodes) {
+      c.scales = over ? next.scales : c.scales;
+      s.scales = source_of<K>(c.scales, (int)((unsigned)c.span / 32), t.b.ld_scales, s.left);
+      c.scales += step_scales;
+    }
+    c.rest -= kStageK;
     return s;
   };
+  auto take_a = [&](Cursor& c, const Place& next) __attribute__((always_inline)) { return take(Int<0>{}, c, next); };
+  auto take_b = [&](Cursor& c, const Place& next) __attribute__((always_inline)) { return take(Int<1>{}, c, next); };
   // Block row i of wave row wm is rows 32 i + 16 wm .. +15 of the tile, so that a
   // tile of few rows has work for both. Along K, load q of this wave fills rows
   // 64 q' + 8 wave + lane / 8 of B or of a half of A (loads 0 and 2 the first, 1 and
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   // widening into the slot that the stage before them frees.
   v4i codes[2];
   uint8_t scale[2];
-  const int oc = kc * 512 + 32 * (gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1)));
+  const int oc = kc * 512 + 32 * (gc ^ ((kc & 3) + 4 * ((kc >> 3) & 1))) + 16 * ((gc >> 2) & 1);
   // Half h of run u. Of 8 threads, 4 begin with their second half, so that a
   // write's 16-byte pieces lie 16 bytes apart over 128.
   const int sw = (gc >> 2) & 1;
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     constexpr int u = decltype(U)::value, h = decltype(H)::value;
     const bool last = h != sw;
     const v4i w = widen8((uint32_t)(last ? codes[u][2] : codes[u][0]), (uint32_t)(last ? codes[u][3] : codes[u][1]), scale[u]);
-    *reinterpret_cast<v4i*>(wide(I).b + oc + 16384 * u + (last ? 16 : 0)) = w;
+    *reinterpret_cast<v4i*>(wide(I).b + (oc ^ (16 * h)) + 16384 * u) = w;
   };
   // Across K, a row's last bytes are followed by the next row's: columns past
   // the tile's end reach only sums that are not stored.
@@ -335,12 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       int v;
       if constexpr (AK == kAlong) v = 8 * ca < s.left ? (q % 2 == 0 ? oa : orest) + 16 * (q / 2) * (int)t.a.ld : kPastEnd;
       else v = oa + 32 * (q / 2) * (int)t.a.ld + 2 * (q % 2) * chunk_a;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)(half(I, Int<q % 2>{}) + 1024 * (8 * (q / 2) + wave)),
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.v, (lds_void*)(half(I, Int<q % 2>{}) + 1024 * (8 * (q / 2) + wave)),
                                                16, v, 0, 0, 0);
     } else if constexpr (BK == kCodes) {
       constexpr int u = (q - 4) / 2;
       if constexpr (q % 2 == 0)
-        codes[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(s.b, ob + 32 * u * (int)t.b.ld, 0, 0));
+        codes[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(s.v, ob + 32 * u * (int)t.b.ld, 0, 0));
       else
         scale[u] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, (kc + 32 * u) * (int)t.b.ld_scales + gc / 2, 0, 0);
     } else {
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       } else {
         v = ob + 16 * j * (int)t.b.ld;
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.b, (lds_void*)&wide(I).b[1024 * (8 * j + wave)], 16, v, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.v, (lds_void*)&wide(I).b[1024 * (8 * j + wave)], 16, v, 0, 0, 0);
     }
   };
 
@@ -396,26 +408,30 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   };
   constexpr int ReadsA = AK == kAlong ? 2 : 4;       // LDS reads of a block row's fragments
 
-  // Stage k in slot I: enters with its B fragments and first two A fragments
+  Cursor cur_a, cur_b;
+  // A stage in slot I: enters with its B fragments and first two A fragments
   // read; leaves with the next stage's. Fragment i of A sits in buffer
   // (i + Off) % 4. Loads still in flight at the first and the last wait: a
   // stage's, issued since those of the parts that are due.
-  auto stage = [&](auto I, int k, const Place& now, const Place& next) __attribute__((always_inline)) {
+  auto stage = [&](auto I, const Place& next) __attribute__((always_inline)) {
     using Next = Int<1 - decltype(I)::value>;
     constexpr int Off = (FM * decltype(I)::value) % 4;
     auto read = [&](auto R) { read_a(I, Int<(decltype(R)::value + Off) % 4>{}, R); };
-    const Source s = source(k + 2, now, next);
     // A block row's matrix instructions with its LDS reads, the widening of the
-    // codes' run `Run` (two LDS writes) and `Count` loads from `First` on between
-    // them.
-    auto step = [&](auto R, auto Reads, auto Run, auto First, auto Count) __attribute__((always_inline)) {
+    // codes' run `Run` (two LDS writes) and `Count` loads from `First` on (of A
+    // every other) between them.
+    auto step = [&](auto R, auto Reads, auto Run, auto First, auto Count, const Source& from) __attribute__((always_inline)) {
       constexpr int r = decltype(R)::value, run = decltype(Run)::value, count = decltype(Count)::value;
       for_each<2>([&](auto S) { for_each<4>([&](auto J) { mma(R, Int<(r + Off) % 4>{}, S, J); }); });
       if constexpr (run >= 0) for_each<2>([&](auto H) { widen(I, Run, H); });
-      for_each<count>([&](auto C) { issue(I, Int<decltype(First)::value + decltype(C)::value>{}, s); });
+      for_each<count>([&](auto C) {
+        constexpr int first = decltype(First)::value;
+        issue(I, Int<first + decltype(C)::value * (first < 4 ? 2 : 1)>{}, from);
+      });
       for_each<8>([&](auto X) {
         constexpr int x = decltype(X)::value;
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                          // MFMA
+        if constexpr (r < 2) __builtin_amdgcn_sched_group_barrier(0x004, 3, 0);                     // SALU
         if constexpr (x < decltype(Reads)::value) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // DS read
         if constexpr (run >= 0) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);                  // VALU
         if constexpr (run >= 0 && x % 4 == 3) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);    // DS write
@@ -426,30 +442,41 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     constexpr bool Codes = BK == kCodes;
     read(Int<2>{});
     read(Int<3>{});
-    step(Int<0>{}, Int<2 * ReadsA>{}, Int<-1>{}, Int<0>{}, Int<0>{});
-    step(Int<1>{}, Int<0>{}, Int<-1>{}, Int<0>{}, Int<0>{});
+    const Source sb = take_b(cur_b, next);
+    step(Int<0>{}, Int<2 * ReadsA>{}, Int<-1>{}, Int<0>{}, Int<0>{}, sb);
+    const Source s = take_a(cur_a, next);
+    step(Int<1>{}, Int<0>{}, Int<-1>{}, Int<0>{}, Int<0>{}, s);
     // B and A's first half are read, its second half has landed.
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read(Int<4>{});
-    step(Int<2>{}, Int<ReadsA>{}, Int<Codes ? 0 : -1>{}, Int<4>{}, Int<Codes ? 0 : 2>{});
-    read(Int<5>{});
-    step(Int<3>{}, Int<ReadsA>{}, Int<Codes ? 1 : -1>{}, Int<6>{}, Int<Codes ? 0 : 2>{});
     if constexpr (Codes) {
-      const Source sb = source(k + 3, now, next);
-      for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, sb); });
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (FM == 8) {
+      // A run's codes of the stage after, once those before are widened; all of
+      // them before A's loads: waiting for them then waits for none of those that
+      // are due later.
+      read(Int<4>{});
+      step(Int<2>{}, Int<ReadsA>{}, Int<0>{}, Int<0>{}, Int<0>{}, s);
+      read(Int<5>{});
+      step(Int<3>{}, Int<ReadsA>{}, Int<1>{}, Int<4>{}, Int<2>{}, sb);
       read(Int<6>{});
-      step(Int<4>{}, Int<ReadsA>{}, Int<-1>{}, Int<0>{}, Int<1>{});
+      step(Int<4>{}, Int<ReadsA>{}, Int<-1>{}, Int<6>{}, Int<2>{}, sb);
       read(Int<7>{});
-      step(Int<5>{}, Int<ReadsA>{}, Int<-1>{}, Int<2>{}, Int<1>{});
+      step(Int<5>{}, Int<ReadsA>{}, Int<-1>{}, Int<0>{}, Int<2>{}, s);
     } else {
-      issue(I, Int<0>{}, s);
-      issue(I, Int<2>{}, s);
-      __builtin_amdgcn_sched_barrier(0);
+      read(Int<4>{});
+      step(Int<2>{}, Int<ReadsA>{}, Int<-1>{}, Int<4>{}, Int<2>{}, sb);
+      read(Int<5>{});
+      step(Int<3>{}, Int<ReadsA>{}, Int<-1>{}, Int<6>{}, Int<2>{}, sb);
+      if constexpr (FM == 8) {
+        read(Int<6>{});
+        step(Int<4>{}, Int<ReadsA>{}, Int<-1>{}, Int<0>{}, Int<1>{}, s);
+        read(Int<7>{});
+        step(Int<5>{}, Int<ReadsA>{}, Int<-1>{}, Int<2>{}, Int<1>{}, s);
+      } else {
+        issue(I, Int<0>{}, s);
+        issue(I, Int<2>{}, s);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
     __builtin_amdgcn_s_barrier();
@@ -477,20 +504,23 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
   if (item < 0) return;
   Place now = place(item), next = place(item_at(1));
   int round = 1;
+  cur_a = {now.a, nullptr, now.a_span, now.rest, now.end};
+  cur_b = {now.b, now.scales, now.b_span, now.rest, now.end};
   if constexpr (BK == kCodes) {
     // The order of the loads after slot 0's is a stage's, so that the waits for
     // codes are as loose here as there.
-    const Source s = source(now.k0, now, next), s1 = source(now.k0 + 1, now, next), s2 = source(now.k0 + 2, now, next);
+    const Source b0 = take_b(cur_b, next), b1 = take_b(cur_b, next), b2 = take_b(cur_b, next);
+    const Source s = take_a(cur_a, next), s1 = take_a(cur_a, next);
     auto whole = [&](auto I) __attribute__((always_inline)) {
       for_each<4>([&](auto X) { widen(I, Int<decltype(X)::value / 2>{}, Int<decltype(X)::value % 2>{}); });
       __builtin_amdgcn_sched_barrier(0);
     };
-    for_each<4>([&](auto Q) { issue(Int<0>{}, Int<4 + Q>{}, s); });
+    for_each<4>([&](auto Q) { issue(Int<0>{}, Int<4 + Q>{}, b0); });
     for_each<4>([&](auto Q) { issue(Int<0>{}, Q, s); });
     whole(Int<0>{});
-    for_each<4>([&](auto Q) { issue(Int<1>{}, Int<4 + Q>{}, s1); });
+    for_each<4>([&](auto Q) { issue(Int<1>{}, Int<4 + Q>{}, b1); });
     whole(Int<1>{});
-    for_each<4>([&](auto Q) { issue(Int<0>{}, Int<4 + Q>{}, s2); });
+    for_each<4>([&](auto Q) { issue(Int<0>{}, Int<4 + Q>{}, b2); });
     __builtin_amdgcn_sched_barrier(0);
     issue(Int<1>{}, Int<0>{}, s1);
     issue(Int<1>{}, Int<2>{}, s1);
@@ -499,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
   } else {
     for_each<2>([&](auto I) {
-      const Source s = source(now.k0 + I, now, next);
-      for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, s); });
+      const Source s = take_a(cur_a, next), sb = take_b(cur_b, next);
+      for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, sb); });
       issue(I, Int<0>{}, s);
       issue(I, Int<2>{}, s);
       issue(I, Int<1>{}, s);
@@ -519,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    for (int k = now.k0; k < now.k1; k += 2) {
-      stage(Int<0>{}, k, now, next);
-      stage(Int<1>{}, k + 1, now, next);
+    for (int k = 0; k < now.stages; k += 2) {
+      stage(Int<0>{}, next);
+      stage(Int<1>{}, next);
     }
     Spot at;
     at.lrow = 16 * wm + r16;
@@ -592,7 +622,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int tm = __builtin_amdgcn_readfirstlane(m_), tn = __builtin_amdgcn_readfirstlane(n_);
   const int k0 = __builtin_amdgcn_readfirstlane(split ? 2 * (int)((int64_t)t.units * part / t.parts) : 0);
   const int end = __builtin_amdgcn_readfirstlane(2 * (split ? (int)((int64_t)t.units * (part + 1) / t.parts) : t.units));
-  const int stages = stages_of(t.K), k1 = end < stages ? end : stages;
+  const int stages = ((int)t.K + kStageK - 1) / kStageK, k1 = end < stages ? end : stages;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const uint8_t* base_a = tile_base<AK>(t.a, m0);
   const uint8_t* base_b = tile_base<BK>(t.b, n0);
@@ -600,18 +630,38 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int span_b = tile_span<BK>(t.b, t.n - n0 < BN ? t.n - n0 : BN);
 
   // ---- loads --------------------------------------------------------------------
+  // As above, an operand's stages in the order of their loads; past k1 nothing is
+  // loaded. All in 32 bits (K below 2^30) but the addresses: what 64-bit
+  // comparisons yield lies in vector registers, and a descriptor made from it
+  // turns every load into a loop over lanes.
+  const int end_rest = (int)t.K - kStageK * k1;
+  const uint32_t step_a = (uint32_t)(AK == kAlong ? t.a.chunk : kStageK * t.a.ld);
+  const uint32_t step_b = BK == kAlong ? 128 : (uint32_t)(kStageK * t.b.ld);
+  const uint32_t step_scales = (uint32_t)(kStageK * t.b.ld_scales);
+  struct Cursor {
+    const uint8_t* p;
+    const uint8_t* scales;
+    int rest;
+  };
+  Cursor cur_a{base_a + (int64_t)k0 * step_a, nullptr, (int)t.K - kStageK * k0};
+  Cursor cur_b{base_b + (int64_t)k0 * step_b, nullptr, cur_a.rest};
+  if constexpr (BK == kCodes) cur_b.scales = t.b.scales + n0 / 32 + (int64_t)k0 * step_scales;
   struct Source {
-    __amdgpu_buffer_rsrc_t a, b, scales;
+    __amdgpu_buffer_rsrc_t v, scales;
     int left;
   };
-  auto source = [&](int k) __attribute__((always_inline)) {
+  auto take = [&](auto IsB, Cursor& c) __attribute__((always_inline)) {
+    constexpr bool Is = decltype(IsB)::value;
+    constexpr Kind K = Is ? BK : AK;
     Source s;
-    s.left = k < k1 ? left_at(t.K, k) : 0;
-    const int kk = s.left > 0 ? k : 0;
-    s.a = source_of<AK>(base_a, span_a, t.a.ld, t.a.chunk, kk, s.left);
-    s.b = source_of<BK>(base_b, span_b, t.b.ld, 128, kk, s.left);
-    if constexpr (BK == kCodes)
-      s.scales = source_of<BK>(t.b.scales + n0 / 32, span_b / 32, t.b.ld_scales, 0, kk, s.left);
+    s.left = c.rest <= end_rest ? 0 : c.rest < kStageK ? c.rest : kStageK;
+    s.v = source_of<K>(c.p, Is ? span_b : span_a, Is ? t.b.ld : t.a.ld, s.left);
+    c.p += Is ? step_b : step_a;
+    if constexpr (K == kCodes) {
+      s.scales = source_of<K>(c.scales, (int)((unsigned)span_b / 32), t.b.ld_scales, s.left);
+      c.scales += step_scales;
+    }
+    c.rest -= kStageK;
     return s;
   };
   // Load q of an operand along K: rows 8 (Waves q + wave) + lane / 8; across:
@@ -650,7 +700,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
       const int c = gx ^ (4 * ((Waves / 2 * q) & 1));      // 16 columns
       v = oa + (c >> 2) * (int)t.a.chunk + 32 * (c & 3) + 4 * Waves * q * (int)t.a.ld;
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(s.a, (lds_void*)(pa(I) + 1024 * (Waves * q + wave)), 16, v, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(s.v, (lds_void*)(pa(I) + 1024 * (Waves * q + wave)), 16, v, 0, 0, 0);
   };
   auto load_b = [&](auto I, auto Q, const Source& s) __attribute__((always_inline)) {
     constexpr int q = decltype(Q)::value;
@@ -658,7 +708,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
       constexpr int u = q / 2;
       if constexpr (q % 2 == 0)
         codes[decltype(I)::value][u] = __builtin_bit_cast(
-            v4i, __builtin_amdgcn_raw_buffer_load_b128(s.b, (kc + 8 * Waves * u) * (int)t.b.ld + 16 * gc, 0, 0));
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(s.v, (kc + 8 * Waves * u) * (int)t.b.ld + 16 * gc, 0, 0));
       else
         scale[decltype(I)::value][u] = __builtin_amdgcn_raw_buffer_load_b8(s.scales, (kc + 8 * Waves * u) * (int)t.b.ld_scales + gc / 2, 0,
                                                        0);
@@ -670,7 +720,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
       } else {
         v = ob + 32 * (gx ^ (4 * ((Waves / 2 * q) & 1))) + 4 * Waves * q * (int)t.b.ld;
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.b, (lds_void*)(pb(I) + 1024 * (Waves * q + wave)), 16, v, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(s.v, (lds_void*)(pb(I) + 1024 * (Waves * q + wave)), 16, v, 0, 0, 0);
     }
   };
 
@@ -705,17 +755,19 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
       B[j][1] = read_across(p + at + 8192, 1024);
     }
   };
-  // Stage k in slot I: enters with its B fragments and its first two A fragments
+  // First of the loads issued with block column j; codes' after their widening,
+  // all with column 2.
+  constexpr auto first = [](int j) { return BK != kCodes ? Loads * j / 4 : j < 3 ? 0 : j == 3 ? LB : Loads; };
+  // A stage in slot I: enters with its B fragments and its first two A fragments
   // read; leaves with the next stage's. Fragment i of A sits in buffer
   // (i + Off) % 4. Codes are loaded eight stages ahead, and widened into the slot
   // after four (a stage ahead they made a stage as long as a load: 0.8 us instead
-  // of 0.XX).
-  auto stage = [&](auto I, int k) __attribute__((always_inline)) {
+  // of 0.6).
+  auto stage = [&](auto I) __attribute__((always_inline)) {
     constexpr int slot = decltype(I)::value;
     using Next = Int<(slot + 1) % 4>;
     constexpr int Off = (FM * slot) % 4;
-    const Source s = source(k + 4);
-    const Source sb = BK == kCodes ? source(k + 8) : s;
+    const Source sb = take(Int<1>{}, cur_b), s = take(Int<0>{}, cur_a);
     for_each<FM - 2>([&](auto R) {
       constexpr int i = decltype(R)::value;
       read_a(I, Int<(i + 2 + Off) % 4>{}, Int<i + 2>{});
@@ -731,7 +783,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * Loads, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (BK == kCodes) widen(I);
     read_a(Next{}, Int<(FM + Off) % 4>{}, Int<0>{});
     read_a(Next{}, Int<(FM + 1 + Off) % 4>{}, Int<1>{});
     for_each<4>([&](auto J) {
@@ -742,8 +793,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
         acc[FM - 1][j] = product16(B[j][x], A[(FM - 1 + Off) % 4][x], acc[FM - 1][j]);
       });
       read_b(Next{}, J);
-      for_each<Loads * (j + 1) / 4 - Loads * j / 4>([&](auto Q) {
-        constexpr int q = Loads * j / 4 + decltype(Q)::value;
+      if constexpr (BK == kCodes && j == 1) widen(I);
+      for_each<first(j + 1) - first(j)>([&](auto Q) {
+        constexpr int q = first(j) + decltype(Q)::value;
         if constexpr (q < LB) load_b(I, Int<q>{}, sb);
         else load_a(I, Int<q - LB>{}, s);
       });
@@ -757,14 +809,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
     for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
   if constexpr (BK == kCodes) {
     for_each<4>([&](auto I) {
-      const Source s = source(k0 + I);
-      for_each<LB>([&](auto Q) { load_b(I, Q, s); });
+      const Source sb = take(Int<1>{}, cur_b);
+      for_each<LB>([&](auto Q) { load_b(I, Q, sb); });
     });
     for_each<4>([&](auto I) { widen(I); });
     __builtin_amdgcn_sched_barrier(0);
     // From here on in a stage's order, so that the waits for codes are as loose.
     for_each<4>([&](auto I) {
-      const Source s = source(k0 + I), sb = source(k0 + 4 + I);
+      const Source sb = take(Int<1>{}, cur_b), s = take(Int<0>{}, cur_a);
       for_each<LB>([&](auto Q) { load_b(I, Q, sb); });
       __builtin_amdgcn_sched_barrier(0);
       for_each<LA>([&](auto Q) { load_a(I, Q, s); });
@@ -772,8 +824,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
     });
   } else {
     for_each<4>([&](auto I) {
-      const Source s = source(k0 + I);
-      for_each<LB>([&](auto Q) { load_b(I, Q, s); });
+      const Source sb = take(Int<1>{}, cur_b), s = take(Int<0>{}, cur_a);
+      for_each<LB>([&](auto Q) { load_b(I, Q, sb); });
       for_each<LA>([&](auto Q) { load_a(I, Q, s); });
     });
   }
@@ -784,9 +836,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   read_a(Int<0>{}, Int<1>{}, Int<1>{});
   for_each<4>([&](auto J) { read_b(Int<0>{}, J); });
   int k = k0;
-  for (; k + 4 <= k1; k += 4) for_each<4>([&](auto I) { stage(I, k + I); });
+  for (; k + 4 <= k1; k += 4) for_each<4>([&](auto I) { stage(I); });
   for_each<3>([&](auto I) {
-    if (k + I < k1) stage(I, k + I);
+    if (k + I < k1) stage(I);
   });
   Spot at;
   at.lrow = 16 * FM * wm + r16;

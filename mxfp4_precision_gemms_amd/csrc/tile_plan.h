@@ -32,10 +32,12 @@ constexpr int64_t kMostSmall = int64_t{1} << 28;
 // Estimates in microseconds from measurements on the whole device (256 CUs): a
 // launch and a tile's first loads and epilogue 5, a stage of K as below; parts of
 // K a second launch and their sums written and read at 4.5 TB/s. The last round
-// of tiles is split where it leaves half of the compute units or more without
-// one. Up to 128 rows the small tiles alone: what binds there is B's way from
-// memory, which four slots keep busier than two (1 x 131072 x 4096: 192 us with
-// 64 x 128 tiles, 206 with 128 x 128, 260 with 256 x 256).
+// of tiles may be split where it leaves half of the compute units or more without
+// one (dh of 1000 x 1024 x 3000: 128 tiles of 64 x 128 whole 18 us, in two parts
+// 19; 37 x 1032 x 8191: 9 tiles of it 39 us, in 16 parts 11). Up to 128 rows the
+// small tiles alone: what binds there is B's way from memory, which four slots
+// keep busier than two (1 x 131072 x 4096: 179 us with 64 x 128 tiles, 188 with
+// 128 x 128, 245 with 256 x 256).
 inline ProductPlan product_plan(int64_t m, int64_t n, int64_t K, Kind a, Kind b, bool splits, int64_t cus) {
   ProductPlan best{};
   best.us = 1e30;
@@ -47,20 +49,28 @@ inline ProductPlan product_plan(int64_t m, int64_t n, int64_t K, Kind a, Kind b,
     const int64_t bm = tile_rows(tile), bn = tile_cols(tile);
     const int64_t all = ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
     if (small && all > kMostSmall / 128) continue;
-    const double stage = tile == k256x256 ? 1.1 : tile == k192x256 ? 0.86
-                         : tile == k64x128 ? 0.4 : b == kCodes ? 0.8 : a == kAcross ? 0.6 : 0.46;
     const int64_t rem = all % cus;
     int64_t parts = splits && rem > 0 ? cus / rem : 1;
     if (parts > units / 4) parts = units / 4;
     if (parts > 32) parts = 32;
-    ProductPlan p{tile, all, 0, 1, 0};
-    if (parts >= 2) p = {tile, all - rem, rem, (int)parts, 0};
-    const int64_t rounds = (p.full + cus - 1) / cus;
-    p.us = 5 + stage * 2 * (double)units * (double)rounds;
-    if (p.split)
-      p.us += 4 + stage * 2 * (double)((units + p.parts - 1) / p.parts) +
-              p.parts * ((double)p.split / (double)all) * (double)m * (double)n * 8 / 4.5e6;
-    if (p.us < best.us) best = p;
+    for (const bool split : {false, true}) {
+      if (split && parts < 2) continue;
+      // The smallest tiles on half of the compute units are not yet held up by the
+      // way of their operands.
+      const double stage = tile == k256x256   ? (b == kCodes ? 1.4 : 1.1)
+                           : tile == k192x256 ? 0.86
+                           : tile == k64x128  ? (!split && 2 * all <= cus ? 0.3 : 0.4)
+                           : a == kAcross     ? 0.6
+                                              : 0.46;
+      ProductPlan p{tile, all, 0, 1, 0};
+      if (split) p = {tile, all - rem, rem, (int)parts, 0};
+      const int64_t rounds = (p.full + cus - 1) / cus;
+      p.us = 5 + stage * 2 * (double)units * (double)rounds;
+      if (split)
+        p.us += 4 + stage * 2 * (double)((units + p.parts - 1) / p.parts) +
+                p.parts * ((double)p.split / (double)all) * (double)m * (double)n * 8 / 4.5e6;
+      if (p.us < best.us) best = p;
+    }
   }
   return best;
 }

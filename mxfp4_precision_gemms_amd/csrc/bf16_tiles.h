@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     issue(Int<1>{}, Int<2>{}, s1);
     issue(Int<1>{}, Int<1>{}, s1);
     issue(Int<1>{}, Int<3>{}, s1);
+    __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Loads, 0));
   } else {
     for_each<2>([&](auto I) {
@@ -533,8 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
       for_each<4>([&](auto Q) { issue(I, Int<4 + Q>{}, sb); });
       issue(I, Int<0>{}, s);
       issue(I, Int<2>{}, s);
+      __builtin_amdgcn_sched_barrier(0);               // the waits count loads in this order
       issue(I, Int<1>{}, s);
       if constexpr (FM == 8) issue(I, Int<3>{}, s);
+      __builtin_amdgcn_sched_barrier(0);
     });
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(Rest / 2 + Loads, 15));
   }
@@ -827,6 +830,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
       const Source sb = take(Int<1>{}, cur_b), s = take(Int<0>{}, cur_a);
       for_each<LB>([&](auto Q) { load_b(I, Q, sb); });
       for_each<LA>([&](auto Q) { load_a(I, Q, s); });
+      __builtin_amdgcn_sched_barrier(0);               // the waits count loads in this order
     });
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * Loads, 0));

@@ -15,6 +15,9 @@
 // added up over the pieces in fp32 and rounded once.
 //
 // Bound by the matrix cores: 2 T V D operations forward, 6 T V D backward.
+// Measured: 8192 x 131072 x 4096 (T, V, D) forward 6.1 ms, 1440 TFLOP/s, backward 18.1
+// ms, 1460 TFLOP/s; 1531 x 50021 x 2048 in 245 and 793 us. One row by the weights'
+// bytes: 1 x 131072 x 4096 in 177 us, 6.1 TB/s.
 #include "bf16_tiles.h"
 
 namespace adahop {
@@ -34,15 +37,58 @@ __device__ __forceinline__ float shift_of(float max) {
 }
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(kLog2e * x); }
 
+// A wave's block rows in the tile; past the last row, that one.
+struct Rows {
+  int64_t first;             // the tile's
+  int lrow, step, last;
+  __device__ __forceinline__ Rows(const Spot& at, int64_t m) : first(at.row0 - at.lrow), lrow(at.lrow), step(at.step) {
+    const int64_t rows = m - first;
+    last = rows < 256 ? (int)rows - 1 : 255;
+  }
+  template <typename T>
+  __device__ __forceinline__ T of(const T* p, int i) const {
+    const int r = lrow + step * i;
+    return (p + first)[(unsigned)(r < last ? r : last)];
+  }
+};
 struct Targets {
   const void* p;
   int wide;                  // int64, else int32
   __device__ __forceinline__ int64_t at(int64_t row) const {
     return wide ? static_cast<const int64_t*>(p)[row] : (int64_t)static_cast<const int32_t*>(p)[row];
   }
+  // Those of a wave's block rows.
+  template <int FM>
+  __device__ __forceinline__ void at(const Rows& rows, int64_t (&t)[FM]) const {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) t[i] = rows.of(static_cast<const int64_t*>(p), i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) t[i] = rows.of(static_cast<const int32_t*>(p), i);
+    }
+  }
 };
 
+// A row's value from those of its four lanes, 16 lanes apart.
+template <typename F>
+__device__ __forceinline__ float of_row(float x, F&& f) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const uint32_t v = __builtin_bit_cast(uint32_t, x);
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t u = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1])));
+  const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  x = f(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+#endif
+  return x;
+}
+
 // ---- epilogues ----------------------------------------------------------------
+// What they need of their rows is loaded for all of them before the first is
+// stored: loads and stores are waited for in their order, so a row's loads between
+// two rows' stores would wait for the first's (gradient of 8192 x 32000 x 1024:
+// 1290 us, so 1258).
+//
 // The logits' maximum and sum over the wave's 64 columns of each row, and the
 // target's logit.
 struct StatsEpi {
@@ -55,41 +101,68 @@ struct StatsEpi {
     static_assert(Wide, "");
     float2* to = part + at.group * m;
     const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
+    const Rows rows(at, m);
+    int64_t t[FM];             // first used after the sums
+    y.at(rows, t);
+    __builtin_amdgcn_sched_barrier(0);
+    // Step by step for all block rows, so that the exchanges between lanes have
+    // others beside them (row by row, through LDS, 8192 x 32000 x 1024 took 435 us;
+    // so 412).
+    float top[FM], sum[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][e / 4][e % 4] *= scale;
+    if (inside < 16) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e >= inside) acc[i][e / 4][e % 4] = kMinusInf;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      top[i] = kMinusInf;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top[i] = __builtin_fmaxf(top[i], acc[i][e / 4][e % 4]);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) top[i] = of_row(top[i], [](float a, float b) { return __builtin_fmaxf(a, b); });
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const float by = shift_of(top[i]);
+      sum[i] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sum[i] += exp_of(acc[i][e / 4][e % 4] - by);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sum[i] = of_row(sum[i], [](float a, float b) { return a + b; });
+    // All targets are here: one that no lane used would otherwise be waited for, with
+    // the next stages' loads, where its register is taken again.
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int64_t r = at.row0 + at.step * i;
-      float z[16], top = kMinusInf;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        z[e] = e < inside ? scale * acc[i][e / 4][e % 4] : kMinusInf;
-        top = __builtin_fmaxf(top, z[e]);
-      }
-      top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-      const float by = shift_of(top);
-      float sum = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sum += exp_of(z[e] - by);
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
       if (r < m) {
-        if ((threadIdx.x & 48) == 0) to[r] = float2{top, sum};
-        const int64_t d = y.at(r) - at.col0;
+        if ((threadIdx.x & 48) == 0) to[r] = float2{top[i], sum[i]};
+        const int64_t d = t[i] - at.col0;
         if (d >= 0 && d < inside) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (d == e) said[r] = z[e];
+            if (d == e) said[r] = acc[i][e / 4][e % 4];
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
 
 // The gradient of a piece's logits, columns v0 .. of the vocabulary, 64 columns of
 // all rows together: a stage of either product then reads whole stretches of
-// memory (dh of 1531 x 2048 x 50021 from rows of 100 KB 276 us, so 2XX). A tile's
-// columns past the piece's end are written as zeros.
+// memory (from whole rows dh of 8192 x 65536 x 4096 took 2904 us, so 2861; of
+// 1531 x 50021 x 2048 269 and 264). A tile's columns past the piece's end are
+// written as zeros. all and the target's place of each row are held, its share is
+// read again by the lane that needs it: its registers would be spilled.
 struct GradEpi {
   float scale;
   Targets y;
@@ -103,26 +176,47 @@ struct GradEpi {
   __device__ __forceinline__ void store(v4f (&acc)[FM][4], const Spot& at, int64_t m, int64_t n) const {
     static_assert(Wide, "");
     const int inside = n - at.col0 < 16 ? (int)(n - at.col0) : 16;
+    const Rows rows(at, m);
+    int place[FM];             // the target's, in the lane's columns
+    float less[FM], all[FM];
+    {
+      int64_t t[FM];
+      y.at(rows, t);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        less[i] = rows.of(lse, i);
+        all[i] = rows.of(dloss, i);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if (t[i] < 0 || t[i] >= vocab) all[i] = 0.0f;
+        const int64_t d = t[i] - v0 - at.col0;
+        place[i] = d >= 0 && d < inside ? (int)d : -1;
+      }
+      if (dlse != nullptr) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) all[i] += rows.of(dlse, i);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) all[i] *= scale;
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int64_t r = at.row0 + at.step * i;
       mx8::u32x4 w[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
       if (r < m) {
-        const float less = lse[r];
-        const int64_t t = y.at(r);
-        const float own = t >= 0 && t < vocab ? dloss[r] : 0.0f;
-        const float all = scale * (dlse == nullptr ? own : own + dlse[r]);
-        const int64_t d = t - v0 - at.col0;
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          v[e] = all * exp_of(__builtin_fmaf(acc[i][e / 4][e % 4], scale, -less));
+          v[e] = all[i] * exp_of(__builtin_fmaf(acc[i][e / 4][e % 4], scale, -less[i]));
           if (e >= inside) v[e] = 0.0f;
         }
-        if (d >= 0 && d < inside) {
+        if (place[i] >= 0) {
+          const float own = scale * dloss[r];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (d == e) v[e] -= scale * own;
+            if (place[i] == e) v[e] -= own;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
@@ -210,7 +304,7 @@ adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, 
   const adahop_status st = check_launch("xent");
   if (st != ADAHOP_OK) return st;
   const FinishArgs f = {part, said, y, a.T, a.V, (int64_t)t.tiles_n * (t.bn / 64), loss, lse};
-  // Few rows: more lanes a row (1 row of 500 parts: 7 us with 16 lanes, X with 128).
+  // Few rows: more lanes a row (1 row of 500 parts: 7 us with 16 lanes, 4 with 128).
   auto groups = [&](int rows) {
     const int64_t n = (a.T + rows - 1) / rows;
     return dim3((unsigned)(n < 1 << 20 ? n : 1 << 20));

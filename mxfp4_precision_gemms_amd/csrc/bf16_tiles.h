@@ -20,9 +20,10 @@
 // during a tile's last ones and its epilogue.
 //
 // Measured, 4.4e12 operations each: 8192 x 4096 x 65536 with A along K and B
-// across 1420 .. 1450 TFLOP/s, 65536 x 4096 x 8192 with both across 1390 .. 1440;
-// the matrix cores busy 75 % of the time at 1.66 .. 1.77 GHz, the clock that the
-// power limit leaves (16x16x32 and 32x32x16 blocks alike).
+// across 1430 .. 1500 TFLOP/s, 65536 x 4096 x 8192 with both across 1410 .. 1500; 4096
+// x 14336 x 32768 with both across 1380 .. 1440, from codes 1290 .. 1360; the matrix
+// cores busy 75 % of the time at 1.66 .. 1.77 GHz, the clock that the power limit
+// leaves (16x16x32 and 32x32x16 blocks alike).
 //
 // LDS of an operand along K: rows of 128 bytes, the 16-byte chunks XORed with
 // row bits so that the 16 rows which a quarter of a wave reads at one chunk lie

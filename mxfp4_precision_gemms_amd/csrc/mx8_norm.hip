@@ -132,7 +132,8 @@ struct NormBackArgs {
 // group of rows) and goes out once. Bound by HBM: 8 columns a thread, so that
 // 16 waves a compute unit fit, each with its next row's loads in flight
 // (16384 x 2048 in bf16 with dh: 45 .. 48 us, 5.6 .. 5.9 TB/s; a wave a row
-// without loads ahead 76).
+// without loads ahead 76; from MXFP8 h 39 .. 43 us, 5.5 .. 6 TB/s, 3001 x 4096 in fp32
+// 24 .. 25 us).
 // Once: every row starts at a cache line. Kept: h is kept in MXFP8, dx and dh are
 // of HF32's type.
 template <bool DyF32, bool HF32, bool Kept, bool Once, int Waves, int NV>

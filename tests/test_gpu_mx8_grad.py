@@ -122,6 +122,21 @@ def test_rmsnorm_backward(rows, cols, yt, xt, with_dh):
         assert over.data_ptr() == dev_dh.data_ptr() and torch.equal(over, dx) and torch.equal(g2, dgain)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(3, 96), (70, 544), (6, 2080), (2, 16416), (2, 32768), (4500, 64)])
+def test_rmsnorm_backward_over_dy(rows, cols, dt):
+    """dx in dy's place: the same bits."""
+    c, s, h = kept(rows, cols, seed=12)
+    dy = rand(rows, cols, seed=13).to(DT[dt])
+    gain = (1 + rand(cols, seed=14, std=0.2)).to(DEV)
+    rstd = ((h.square().mean(1) + 1e-5) ** -0.5).float().to(DEV)
+    for place in (lambda t: t.to(DEV), lambda t: strided(t, 1, 1)):
+        dx, dgain = A.adahop_rmsnorm_backward_mx8(place(dy), spread(c, s, 3), gain, rstd, dx_dtype=DT[dt])
+        over = place(dy)
+        got, g2 = A.adahop_rmsnorm_backward_mx8(over, spread(c, s, 3), gain, rstd, dx=over)
+        assert got.data_ptr() == over.data_ptr() and torch.equal(got, dx) and torch.equal(g2, dgain)
+
+
 def test_rmsnorm_backward_no_rows():
     z = torch.empty(0, 64, device=DEV)
     h = torch.empty(0, 64, dtype=torch.uint8, device=DEV), torch.empty(0, 2, dtype=torch.uint8, device=DEV)

@@ -118,3 +118,39 @@ def test_long_gradients_past_4_gb():
     a, b = gy[:, r].double(), values(codes[:, c].contiguous(), scales[:, c.start // 32:].contiguous())
     want = a.t() @ b
     check("dw", got[r][:, c], want, (T + 2) * U * (a.abs().t() @ b.abs()) + U * want.abs())
+
+
+def apart(t, ld):
+    """A copy of t in rows ld elements apart; what lies between is NaN."""
+    buf = torch.full(((t.shape[0] - 1) * ld + t.shape[1],), float("nan") if t.is_floating_point() else 255,
+                     dtype=t.dtype, device=DEV)
+    view = buf.as_strided(t.shape, (ld, 1))
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("T,Din,Dout", [(70, 288, 264), (300, 96, 1032), (70, 8224, 2056)])
+def test_wgrad_rows_nearly_8_mb_apart(T, Din, Dout):
+    say("8 MB", T, Din, Dout)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    gy = torch.randn(T, Dout, generator=g, device=DEV).to(torch.bfloat16)
+    x = A.adahop_mx8_quant(torch.randn(T, Din, generator=g, device=DEV))
+    far = apart(x[0], (1 << 23) - 16), apart(x[1], (1 << 23) - 1)
+    got = A.adahop_gemm_wgrad_mx8(apart(gy, (1 << 22) - 8), far)
+    assert torch.equal(got, A.adahop_gemm_wgrad_mx8(gy, x))
+
+
+@pytest.mark.parametrize("T,V,D", [(37, 300, 520), (300, 200, 520), (520, 777, 264)])
+def test_cross_entropy_rows_nearly_8_mb_apart(T, V, D):
+    say("8 MB", T, V, D)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    h = torch.randn(T, D, generator=g, device=DEV).to(torch.bfloat16)
+    w = (torch.randn(V, D, generator=g, device=DEV) / D ** 0.5).to(torch.bfloat16)
+    y = torch.randint(0, V, (T,), generator=g, device=DEV)
+    dloss = torch.rand(T, generator=g, device=DEV)
+    want = A.adahop_xent(h, w, y)
+    far = apart(h, (1 << 22) - 8), apart(w, (1 << 22) - 8)
+    got = A.adahop_xent(*far, y)
+    assert torch.equal(got.loss, want.loss) and torch.equal(got.lse, want.lse)
+    for a, b in zip(A.adahop_xent_backward(*far, y, got.lse, dloss), A.adahop_xent_backward(h, w, y, got.lse, dloss)):
+        assert torch.equal(a, b)

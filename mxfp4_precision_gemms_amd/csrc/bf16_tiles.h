@@ -759,6 +759,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
       B[j][1] = read_across(p + at + 8192, 1024);
     }
   };
+  constexpr int ReadsA = AK == kAlong ? 2 : 4, ReadsB = BK == kAlong ? 2 : 4;   // LDS reads of a block's fragments
   // First of the loads issued with block column j; codes' after their widening,
   // all with column 2.
   constexpr auto first = [](int j) { return BK != kCodes ? Loads * j / 4 : j < 3 ? 0 : j == 3 ? LB : Loads; };
@@ -779,6 +780,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
         constexpr int x = decltype(X)::value;
         acc[i][x % 4] = product16(B[x % 4][x / 4], A[(i + Off) % 4][x / 4], acc[i][x % 4]);
       });
+      for_each<8>([&](auto X) {
+        constexpr int x = decltype(X)::value;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x004, 4, 0);
+        if constexpr (x < ReadsA) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      });
       __builtin_amdgcn_sched_barrier(0);
     });
     // All of this slot's reads are in; the next stage's loads of this wave have
@@ -787,9 +794,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * Loads, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_a(Next{}, Int<(FM + Off) % 4>{}, Int<0>{});
-    read_a(Next{}, Int<(FM + 1 + Off) % 4>{}, Int<1>{});
     for_each<4>([&](auto J) {
+      if constexpr (J < 2) read_a(Next{}, Int<(FM + J + Off) % 4>{}, Int<J>{});
       constexpr int j = decltype(J)::value;
       for_each<2>([&](auto S) {
         constexpr int x = decltype(S)::value;
@@ -802,6 +808,18 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
         constexpr int q = first(j) + decltype(Q)::value;
         if constexpr (q < LB) load_b(I, Int<q>{}, sb);
         else load_a(I, Int<q - LB>{}, s);
+      });
+      // One by one between the matrix instructions (3 to 5 % of a wave of tiles).
+      constexpr int reads = (J < 2 ? ReadsA : 0) + ReadsB, loads = first(j + 1) - first(j);
+      for_each<4>([&](auto X) {
+        constexpr int x = decltype(X)::value;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                            // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, reads * (x + 1) / 4 - reads * x / 4, 0);          // DS read
+        if constexpr (BK == kCodes && j == 1) {
+          __builtin_amdgcn_sched_group_barrier(0x002, 8 * Runs, 0);                                   // VALU
+          if constexpr (Runs > 1 || x % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);    // DS write
+        }
+        __builtin_amdgcn_sched_group_barrier(0x010, loads * (x + 1) / 4 - loads * x / 4, 0);          // VMEM
       });
       __builtin_amdgcn_sched_barrier(0);
     });

@@ -21,8 +21,8 @@
 //
 // Measured, 4.4e12 operations each: 8192 x 4096 x 65536 with A along K and B
 // across 1430 .. 1500 TFLOP/s, 65536 x 4096 x 8192 with both across 1410 .. 1500; 4096
-// x 14336 x 32768 with both across 1380 .. 1440, from codes 1290 .. 1360; the matrix
-// cores busy 75 % of the time at 1.66 .. 1.77 GHz, the clock that the power limit
+// x 14336 x 32768 with both across 1380 .. 1440, from codes 1290 .. 1380; the matrix
+// cores busy 74 .. 83 % of the time at 1.66 .. 1.77 GHz, the clock that the power limit
 // leaves (16x16x32 and 32x32x16 blocks alike).
 //
 // LDS of an operand along K: rows of 128 bytes, the 16-byte chunks XORed with

@@ -15,9 +15,9 @@
 // added up over the pieces in fp32 and rounded once.
 //
 // Bound by the matrix cores: 2 T V D operations forward, 6 T V D backward.
-// Measured: 8192 x 131072 x 4096 (T, V, D) forward 6.1 ms, 1440 TFLOP/s, backward 18.1
-// ms, 1460 TFLOP/s; 1531 x 50021 x 2048 in 245 and 793 us. One row by the weights'
-// bytes: 1 x 131072 x 4096 in 177 us, 6.1 TB/s.
+// Measured: 8192 x 131072 x 4096 (T, V, D) forward 6.0 .. 6.1 ms, 1440 .. 1470
+// TFLOP/s, backward 17.9 .. 18.1 ms, 1460 .. 1480; 1531 x 50021 x 2048 in 245 and
+// 781 us. One row by the weights' bytes: 1 x 131072 x 4096 in 177 us, 6.1 TB/s.
 #include "bf16_tiles.h"
 
 namespace adahop {

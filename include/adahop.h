@@ -758,6 +758,13 @@ ADAHOP_API size_t adahop_xent_workspace_size(int64_t rows, int64_t vocab);
 ADAHOP_API adahop_status adahop_xent(const adahop_xent_args* args, void* ws, size_t ws_bytes,
                                      void* stream);
 
+/* How the gradient of the logits, g, is held between its products. SPLIT: as the
+ * sum of two bf16 numbers, off by at most 2^-16 of each element. BF16: as the
+ * nearest bf16, off by at most 2^-8 of each element, with three fifths of the
+ * operations (2.3e-3 to 2.6e-3 of dh and dw in the root mean square, where bf16
+ * outputs' own rounding is 1.7e-3). */
+typedef enum { ADAHOP_XENT_G_SPLIT = 0, ADAHOP_XENT_G_BF16 = 1 } adahop_xent_g;
+
 /* Its gradient, from dloss (fp32 [T], the gradient of each row's loss) and, if
  * not NULL, dlse (fp32 [T], that of each row's lse, as a penalty on the
  * normalizer gives it), with the lse that adahop_xent returned:
@@ -766,15 +773,16 @@ ADAHOP_API adahop_status adahop_xent(const adahop_xent_args* args, void* ws, siz
  * dloss of a row that is left out does not count; its dlse does. dh and dw are
  * bf16 or fp32; either may be NULL. The logits are formed again, `piece` entries
  * of the vocabulary at a time (0: as many as keep g within 1 GiB; rounded up to a
- * multiple of 256); g of a piece is held in bf16, sums are fp32,
- * dh and dw are rounded once. Needs
+ * multiple of 256); g of a piece is held as `g` says, sums are fp32,
+ * dh and dw are rounded once. Where SPLIT's second numbers meet an infinity of h
+ * or w, the sum may be a NaN instead of an infinity. Needs
  * adahop_xent_backward_args_workspace_size(args) bytes of 16-byte aligned
- * workspace (0 for arguments that the call refuses): 2 * rows * piece (rows
- * rounded up to a multiple of 64) for g, dh
+ * workspace (0 for arguments that the call refuses): 4 (BF16: 2) * rows * piece
+ * (rows rounded up to a multiple of 64) for g, dh
  * in fp32 where there are several pieces, and the parts of products split over
  * their sums.
  * Errors: as adahop_xent, and INVALID for NULL lse or dloss (rows > 0), dh and dw
- * both NULL (rows > 0), ld_dh or ld_dw below dim, a bad dtype, piece < 0; UNSUPPORTED for
+ * both NULL (rows > 0), ld_dh or ld_dw below dim, a bad dtype or g, piece < 0; UNSUPPORTED for
  * rows of 2^22 and more. */
 typedef struct {
   int64_t rows, vocab, dim;
@@ -790,7 +798,8 @@ typedef struct {
   float scale;
   int32_t target_dtype;
   int32_t dh_dtype, dw_dtype;                    /* adahop_out_dtype */
-  int32_t reserved[4];
+  int32_t g;                                     /* adahop_xent_g */
+  int32_t reserved[5];
 } adahop_xent_backward_args;
 
 ADAHOP_API size_t adahop_xent_backward_args_workspace_size(const adahop_xent_backward_args* args);

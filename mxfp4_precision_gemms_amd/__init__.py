@@ -128,7 +128,7 @@ class XentBackwardArgs(ctypes.Structure):
                 ("w", _p), ("ld_w", _i64), ("targets", _p), ("lse", _p), ("dloss", _p), ("dlse", _p),
                 ("dh", _p), ("ld_dh", _i64), ("dw", _p), ("ld_dw", _i64), ("piece", _i64),
                 ("scale", ctypes.c_float), ("target_dtype", _i32), ("dh_dtype", _i32),
-                ("dw_dtype", _i32), ("reserved", _i32 * 4)]
+                ("dw_dtype", _i32), ("g", _i32), ("reserved", _i32 * 5)]
 
 
 # Exported symbols and their C signatures (argtypes, restype).
@@ -940,6 +940,7 @@ def adahop_gemm_wgrad_mx8(GY: torch.Tensor, x: Tuple[torch.Tensor, torch.Tensor]
 # ---------------------------------------------------------------------------
 _INDEX = {torch.int32: 0, torch.int64: 1}
 _F32 = {torch.float32: 1}
+XENT_G = {"SPLIT": 0, "BF16": 1}
 
 
 class XentOut(NamedTuple):
@@ -970,11 +971,13 @@ def adahop_xent_backward(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
                          h_grad: bool = True, w_grad: bool = True, dh_dtype=torch.bfloat16,
                          dw_dtype=torch.bfloat16, dh: Optional[torch.Tensor] = None,
                          dw: Optional[torch.Tensor] = None, piece: int = 0,
-                         ws: Optional[torch.Tensor] = None):
+                         ws: Optional[torch.Tensor] = None, g: str = "SPLIT"):
     """(dh [T, D], dw [V, D]), None where not asked for, from the gradients of
     each row's loss and, if given, lse (fp32 [T]). The logits are formed again,
     `piece` entries of the vocabulary at a time (0: chosen). dh and dw may be
-    given (bf16 or fp32), else they have dh_dtype and dw_dtype."""
+    given (bf16 or fp32), else they have dh_dtype and dw_dtype. g: how the
+    logits' gradient is held, "SPLIT" (as two bf16 numbers) or "BF16" (as one: two
+    fifths fewer operations, for an error beside bf16 outputs' own rounding)."""
     T, D = _size(h, "h")
     V, _ = _size(w, "w")
     dev, d = h.device, h.get_device()
@@ -984,7 +987,8 @@ def adahop_xent_backward(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     lp, _ = _vector(lse, "lse", _F32, T, d)
     gp, _ = _vector(dloss, "dloss", _F32, T, d)
     ep = None if dlse is None else _vector(dlse, "dlse", _F32, T, d)[0]
-    a = XentBackwardArgs(T, V, D, hp, ldh, wp, ldw, tp, lp, gp, ep, None, D, None, D, piece, scale, tk)
+    a = XentBackwardArgs(T, V, D, hp, ldh, wp, ldw, tp, lp, gp, ep, None, D, None, D, piece, scale, tk,
+                         g=XENT_G[g])
     if h_grad:
         if dh is None:
             dh = torch.empty((T, D), dtype=dh_dtype, device=dev)

@@ -278,6 +278,7 @@ struct TileOperand {
   const uint8_t* scales;
   int64_t ld_scales;
   int kind;                  // tiles::Kind
+  int64_t term = 0;          // A the sum of two such matrices (B bf16): bytes from one to the other
 };
 struct TileOut {
   void* p;
@@ -318,16 +319,17 @@ struct XentGrad {
   void* dw;                  // or null
   int64_t lddw;
   int dw_f32;
+  int terms;                 // bf16 numbers that hold an element of g: 1 or 2
 };
 // Pieces of the vocabulary in the backward pass: their columns (0: chosen), a
 // multiple of 256, and how many there are.
 struct XentPieces {
   int64_t size, count;
 };
-XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece);
+XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece, int terms);
 size_t xent_ws_bytes(int64_t T, int64_t V);
 adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t stream);
-size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, bool dw);
+size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, int terms, bool dh, bool dw);
 adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t piece, void* ws,
                                    hipStream_t stream);
 

@@ -133,12 +133,14 @@ size_t tile_product_bytes(int64_t m, int64_t n, int64_t K, int a, int b) {
 adahop_status tile_product_launch(const TileOperand& a, const TileOperand& b, int64_t m, int64_t n, int64_t K,
                                   const TileOut& out, float* ws, hipStream_t stream) {
   const ProductPlan plan = plan_of(m, n, K, a.kind, b.kind);
-  TileArgs t = tile_args(plan, {static_cast<const uint8_t*>(a.p), a.ld, a.chunk, a.scales, a.ld_scales},
+  TileArgs t = tile_args(plan, {static_cast<const uint8_t*>(a.p), a.ld, a.chunk, a.scales, a.ld_scales, a.term},
                          {static_cast<const uint8_t*>(b.p), b.ld, b.chunk, b.scales, b.ld_scales}, m, n, K);
   t.split_ws = ws;
   const StoreEpi epi = {out.p, out.ld, out.f32, out.prev, out.ld_prev};
   if (b.kind == kCodes) tile_launch<kAcross, kCodes>(plan, t, epi, stream);
+  else if (a.kind == kAcross && a.term != 0) tile_launch<kAcross, kAcross, 2>(plan, t, epi, stream);
   else if (a.kind == kAcross) tile_launch<kAcross, kAcross>(plan, t, epi, stream);
+  else if (a.term != 0) tile_launch<kAlong, kAcross, 2>(plan, t, epi, stream);
   else tile_launch<kAlong, kAcross>(plan, t, epi, stream);
   adahop_status st = check_launch("tile product");
   if (st != ADAHOP_OK || t.split == 0) return st;

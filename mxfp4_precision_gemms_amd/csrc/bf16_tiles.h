@@ -90,6 +90,7 @@ struct Operand {
   int64_t chunk;             // bf16: bytes from 64 columns to the next 64 (128: plain rows)
   const uint8_t* scales;     // kCodes: a byte per 32 columns
   int64_t ld_scales;
+  int64_t term = 0;          // A of two terms: bytes from the first to the second
 };
 
 struct TileArgs {
@@ -182,13 +183,15 @@ struct Wide {
   uint8_t b[256 * 128];
 };
 
-template <Kind AK, Kind BK, typename Epi, int FM>
+// Terms: A is the sum of so many matrices of its layout; B is read once for each.
+template <Kind AK, Kind BK, typename Epi, int FM, int Terms>
 __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi epi) {
 #ifdef __HIP_DEVICE_COMPILE__                        // the host pass needs the launch stub alone
   // Tile rows; a wave's block rows in A's second half; loads of a wave and stage:
   // of A (2 of the first half) and 4 of B.
   constexpr int BM = 32 * FM, Rest = FM - 4, LA = FM / 2, Loads = LA + 4;
   static_assert(FM == 8 || (FM == 6 && AK == kAlong), "");
+  static_assert(Terms == 1 || (Terms == 2 && BK != kCodes), "");
   // One LDS object for each part that is filled at once: alias analysis then
   // sees that loads into one do not touch another, and adds no wait before
   // the reads.
@@ -553,9 +556,23 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    for (int k = 0; k < now.stages; k += 2) {
-      stage(Int<0>{}, next);
-      stage(Int<1>{}, next);
+    if constexpr (Terms == 1) {
+      for (int k = 0; k < now.stages; k += 2) {
+        stage(Int<0>{}, next);
+        stage(Int<1>{}, next);
+      }
+    } else {
+      // The first term's last stages load the second's first, whose own the next item's.
+      Place to = now;
+      to.a += t.a.term;
+#pragma unroll 1
+      for (int term = 0; term < Terms; ++term) {
+        for (int k = 0; k < now.stages; k += 2) {
+          stage(Int<0>{}, to);
+          stage(Int<1>{}, to);
+        }
+        to = next;
+      }
     }
     Spot at;
     at.lrow = 16 * wm + r16;
@@ -588,7 +605,7 @@ struct RingPart {
   static_assert(!Across || Rows == 128, "K-rows of 256 bytes");
 };
 
-template <Kind AK, Kind BK, typename Epi, int WM, int WN, int FM>
+template <Kind AK, Kind BK, typename Epi, int WM, int WN, int FM, int Terms>
 __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, Epi epi) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int Waves = WM * WN, BM = 16 * FM * WM, BN = 64 * WN;
@@ -634,8 +651,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   const int span_b = tile_span<BK>(t.b, t.n - n0 < BN ? t.n - n0 : BN);
 
   // ---- loads --------------------------------------------------------------------
-  // As above, an operand's stages in the order of their loads; past k1 nothing is
-  // loaded. All in 32 bits (K below 2^30) but the addresses: what 64-bit
+  // As above, an operand's stages in the order of their loads; past k1 A's second
+  // term follows, if there is one, and past that nothing is loaded. All in 32 bits (K below 2^30) but the addresses: what 64-bit
   // comparisons yield lies in vector registers, and a descriptor made from it
   // turns every load into a loop over lanes.
   const int end_rest = (int)t.K - kStageK * k1;
@@ -646,9 +663,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
     const uint8_t* p;
     const uint8_t* scales;
     int rest;
+    int terms;               // still to come
   };
-  Cursor cur_a{base_a + (int64_t)k0 * step_a, nullptr, (int)t.K - kStageK * k0};
-  Cursor cur_b{base_b + (int64_t)k0 * step_b, nullptr, cur_a.rest};
+  const int first_rest = (int)t.K - kStageK * k0;
+  const uint8_t* first_a = base_a + (int64_t)k0 * step_a;
+  const uint8_t* first_b = base_b + (int64_t)k0 * step_b;
+  Cursor cur_a{first_a, nullptr, first_rest, Terms - 1};
+  Cursor cur_b{first_b, nullptr, first_rest, Terms - 1};
   if constexpr (BK == kCodes) cur_b.scales = t.b.scales + n0 / 32 + (int64_t)k0 * step_scales;
   struct Source {
     __amdgpu_buffer_rsrc_t v, scales;
@@ -657,6 +678,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   auto take = [&](auto IsB, Cursor& c) __attribute__((always_inline)) {
     constexpr bool Is = decltype(IsB)::value;
     constexpr Kind K = Is ? BK : AK;
+    if constexpr (Terms > 1) {
+      const bool over = c.rest == end_rest && c.terms > 0;
+      c.p = over ? (Is ? first_b : first_a + t.a.term) : c.p;
+      c.rest = over ? first_rest : c.rest;
+      c.terms = over ? 0 : c.terms;
+    }
     Source s;
     s.left = c.rest <= end_rest ? 0 : c.rest < kStageK ? c.rest : kStageK;
     s.v = source_of<K>(c.p, Is ? span_b : span_a, Is ? t.b.ld : t.a.ld, s.left);
@@ -858,10 +885,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) bf16_ring_kernel(TileArgs t, 
   read_a(Int<0>{}, Int<0>{}, Int<0>{});
   read_a(Int<0>{}, Int<1>{}, Int<1>{});
   for_each<4>([&](auto J) { read_b(Int<0>{}, J); });
+  const int last = Terms == 1 ? k1 : k0 + Terms * (k1 - k0);
   int k = k0;
-  for (; k + 4 <= k1; k += 4) for_each<4>([&](auto I) { stage(I); });
+  for (; k + 4 <= last; k += 4) for_each<4>([&](auto I) { stage(I); });
   for_each<3>([&](auto I) {
-    if (k + I < k1) stage(I);
+    if (k + I < last) stage(I);
   });
   Spot at;
   at.lrow = 16 * FM * wm + r16;
@@ -899,7 +927,7 @@ inline TileArgs tile_args(const ProductPlan& p, Operand a, Operand b, int64_t m,
   return t;
 }
 
-template <Kind AK, Kind BK, typename Epi>
+template <Kind AK, Kind BK, int Terms = 1, typename Epi>
 void tile_launch(const ProductPlan& p, TileArgs t, const Epi& epi, hipStream_t stream) {
   const int64_t items = p.full + p.split * p.parts, cus = compute_units();
   const dim3 most((unsigned)(items < cus ? items : cus)), all((unsigned)items);
@@ -907,15 +935,15 @@ void tile_launch(const ProductPlan& p, TileArgs t, const Epi& epi, hipStream_t s
     case k256x256:
       // Codes are loaded three stages ahead, which has to stay within the next tile.
       if (BK == kCodes && t.units < 2) t.units = 2;
-      bf16_tile_kernel<AK, BK, Epi, 8><<<most, dim3(kThreads), 0, stream>>>(t, epi);
+      bf16_tile_kernel<AK, BK, Epi, 8, Terms><<<most, dim3(kThreads), 0, stream>>>(t, epi);
       break;
     case k192x256:
-      if constexpr (AK == kAlong) bf16_tile_kernel<AK, BK, Epi, 6><<<most, dim3(kThreads), 0, stream>>>(t, epi);
+      if constexpr (AK == kAlong) bf16_tile_kernel<AK, BK, Epi, 6, Terms><<<most, dim3(kThreads), 0, stream>>>(t, epi);
       break;
     case k64x128:
-      if constexpr (AK == kAlong) bf16_ring_kernel<AK, BK, Epi, 2, 2, 2><<<all, dim3(256), 0, stream>>>(t, epi);
+      if constexpr (AK == kAlong) bf16_ring_kernel<AK, BK, Epi, 2, 2, 2, Terms><<<all, dim3(256), 0, stream>>>(t, epi);
       break;
-    default: bf16_ring_kernel<AK, BK, Epi, 4, 2, 2><<<all, dim3(512), 0, stream>>>(t, epi);
+    default: bf16_ring_kernel<AK, BK, Epi, 4, 2, 2, Terms><<<all, dim3(512), 0, stream>>>(t, epi);
   }
 }
 

@@ -318,19 +318,23 @@ adahop_status check_xent_back(const adahop_xent_backward_args& a) {
       (a.dw && (a.ld_dw < a.dim || !valid_dtype(a.dw_dtype))))
     return invalid("xent_backward: leading dimension of dh or dw below dim, or a bad dtype");
   if (a.piece < 0) return invalid("xent_backward: piece must be >= 0");
+  if (a.g != ADAHOP_XENT_G_SPLIT && a.g != ADAHOP_XENT_G_BF16) return invalid("xent_backward: bad g");
   if (a.rows > 0 && (!a.lse || !a.dloss)) return invalid("xent_backward: null lse or dloss");
   return ADAHOP_OK;
 }
 
+int terms_of(const adahop_xent_backward_args& a) { return a.g == ADAHOP_XENT_G_SPLIT ? 2 : 1; }
+
 size_t xent_back_bytes(const adahop_xent_backward_args& a) {
-  return xent_backward_ws_bytes(a.rows, a.vocab, a.dim, a.piece, a.dh != nullptr, a.dw != nullptr);
+  return xent_backward_ws_bytes(a.rows, a.vocab, a.dim, a.piece, terms_of(a), a.dh != nullptr, a.dw != nullptr);
 }
 
 adahop_status xent_back(const adahop_xent_backward_args* a, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (a == nullptr) return invalid("xent_backward: null arguments");
   ADAHOP_TRY(check_xent_back(*a));
   ADAHOP_TRY(need_workspace(ws, ws_bytes, xent_back_bytes(*a), "xent_backward"));
-  const XentGrad g = {a->lse, a->dloss, a->dlse, a->dh, a->ld_dh, a->dh_dtype, a->dw, a->ld_dw, a->dw_dtype};
+  const XentGrad g = {a->lse, a->dloss, a->dlse, a->dh, a->ld_dh, a->dh_dtype, a->dw, a->ld_dw, a->dw_dtype,
+                      terms_of(*a)};
   return xent_backward_launch(xent_args(*a), g, a->piece, ws, stream);
 }
 

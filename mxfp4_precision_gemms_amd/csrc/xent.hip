@@ -9,15 +9,19 @@
 // for each row and 64 columns, their maximum and the sum of their exponentials
 // under it, and the target's logit; a second kernel joins them in a fixed order.
 // Backward: the vocabulary in pieces; for each the logits again, whose epilogue
-// writes g of the piece in bf16, and the two products of g. g is rounded to
-// bf16 (at most 2^-8 of each element, no sum is formed in it) since only
-// then its products run on the bf16 matrix cores; everything else is fp32. dh is
+// writes g of the piece, and the two products of g. Only bf16 runs on the bf16
+// matrix cores, so g is held as the sum of two bf16 numbers, the nearest and the
+// nearest to what that leaves: off by at most 2^-16 of each element. The caller
+// may take the first alone (at most 2^-8; no sum is formed in it), which saves two
+// fifths of the operations: bf16 outputs, whose own rounding is 1.7e-3 in the root
+// mean square, are then 2.3e-3 .. 2.6e-3 off. Everything else is fp32. dh is
 // added up over the pieces in fp32 and rounded once.
 //
-// Bound by the matrix cores: 2 T V D operations forward, 6 T V D backward.
-// Measured: 8192 x 131072 x 4096 (T, V, D) forward 6.0 .. 6.1 ms, 1440 .. 1470
-// TFLOP/s, backward 17.9 .. 18.1 ms, 1460 .. 1480; 1531 x 50021 x 2048 in 245 and
-// 781 us. One row by the weights' bytes: 1 x 131072 x 4096 in 177 us, 6.1 TB/s.
+// Bound by the matrix cores: 2 T V D operations forward, 10 T V D backward (6 with
+// one number). Measured: 8192 x 131072 x 4096 (T, V, D) forward 6.0 .. 6.1 ms,
+// 1440 .. 1470 TFLOP/s, backward 30.8 .. 31.0 ms, 1420 .. 1430 (one number 17.9 ..
+// 18.4, 1440 .. 1480); 1531 x 50021 x 2048 in 245 and 1310 us (781 .. 797). One row
+// by the weights' bytes: 1 x 131072 x 4096 in 177 us, 6.1 TB/s.
 #include "bf16_tiles.h"
 
 namespace adahop {
@@ -163,6 +167,8 @@ struct StatsEpi {
 // 1531 x 50021 x 2048 269 and 264). A tile's columns past the piece's end are
 // written as zeros. all and the target's place of each row are held, its share is
 // read again by the lane that needs it: its registers would be spilled.
+// Terms: 2, g's nearest bf16 and, `term` elements on, that of what it leaves.
+template <int Terms>
 struct GradEpi {
   float scale;
   Targets y;
@@ -171,7 +177,13 @@ struct GradEpi {
   const float* dlse;         // or null
   int64_t v0, vocab;
   uint16_t* g;               // [64 columns][padded][64]
+  int64_t term;
   int64_t padded;            // T rounded up to a multiple of 64; rows from T on are zeros
+  // What the bf16 of these bits leaves of v (exact); nothing where it is no number.
+  static __device__ __forceinline__ float left(float v, uint32_t bits) {
+    const float near = __builtin_bit_cast(float, bits);
+    return __builtin_fabsf(near) < __builtin_inff() ? v - near : 0.0f;
+  }
   template <bool Wide, int FM>
   __device__ __forceinline__ void store(v4f (&acc)[FM][4], const Spot& at, int64_t m, int64_t n) const {
     static_assert(Wide, "");
@@ -204,27 +216,31 @@ struct GradEpi {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int64_t r = at.row0 + at.step * i;
-      mx8::u32x4 w[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-      if (r < m) {
-        float v[16];
+      float own = 0.0f;
+      if (r < m && place[i] >= 0) own = scale * dloss[r];
+      uint16_t* to = g + (at.group * padded + r) * 64 + at.col0 % 64;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          v[e] = all[i] * exp_of(__builtin_fmaf(acc[i][e / 4][e % 4], scale, -less[i]));
-          if (e >= inside) v[e] = 0.0f;
+      for (int e0 = 0; e0 < 16; e0 += 8) {
+        mx8::u32x4 w[Terms] = {};
+        if (r < m) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = all[i] * exp_of(__builtin_fmaf(acc[i][(e0 + e) / 4][e % 4], scale, -less[i]));
+            if (e0 + e >= inside) v[e] = 0.0f;
+            if (place[i] == e0 + e) v[e] -= own;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[0][e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+            if constexpr (Terms == 2)
+              w[1][e] = f32x2_to_bf16x2(left(v[2 * e], w[0][e] << 16), left(v[2 * e + 1], w[0][e] & 0xFFFF0000u));
+          }
         }
-        if (place[i] >= 0) {
-          const float own = scale * dloss[r];
+        if (r < padded) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (place[i] == e) v[e] -= own;
+          for (int s = 0; s < Terms; ++s) *reinterpret_cast<mx8::u32x4*>(to + s * term + e0) = w[s];
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
-      }
-      if (r < padded) {
-        mx8::u32x4* to = reinterpret_cast<mx8::u32x4*>(g + (at.group * padded + r) * 64 + at.col0 % 64);
-        to[0] = w[0];
-        to[1] = w[1];
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -315,11 +331,11 @@ adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, 
 }
 
 // ---- backward -------------------------------------------------------------------
-XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece) {
+XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece, int terms) {
   const int64_t all = whole(V);
   if (piece == 0) {
     // g of a piece within 1 GiB, in pieces of about the same size.
-    piece = (int64_t{1} << 29) / (T > 0 ? T : 1) / kTile * kTile;
+    piece = (int64_t{1} << 29) / terms / (T > 0 ? T : 1) / kTile * kTile;
     if (piece < kTile) piece = kTile;
     if (piece > all) piece = all;
     const int64_t count = (all + piece - 1) / piece;
@@ -334,10 +350,10 @@ struct BackLayout {
   XentPieces p;
   size_t off_sum, off_split, bytes;
 };
-BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, bool dw) {
+BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, int terms, bool dh, bool dw) {
   BackLayout l{};
-  l.p = xent_pieces(T, V, piece);
-  size_t at = align_up(2 * (size_t)padded_rows(T) * (size_t)l.p.size, kAlign);
+  l.p = xent_pieces(T, V, piece, terms);
+  size_t at = align_up(2 * (size_t)terms * (size_t)padded_rows(T) * (size_t)l.p.size, kAlign);
   l.off_sum = at;
   if (dh && l.p.count > 1) at += align_up(4 * (size_t)T * (size_t)D, kAlign);
   l.off_split = at;
@@ -354,8 +370,8 @@ BackLayout back_layout(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, 
 
 }  // namespace
 
-size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, bool dh, bool dw) {
-  return T == 0 ? 0 : back_layout(T, V, D, piece, dh, dw).bytes;
+size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, int terms, bool dh, bool dw) {
+  return T == 0 ? 0 : back_layout(T, V, D, piece, terms, dh, dw).bytes;
 }
 
 adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t piece, void* ws,
@@ -367,19 +383,21 @@ adahop_status xent_backward_launch(const XentArgs& a, const XentGrad& b, int64_t
     return tile_product_launch(operand(nullptr, 8, kAcross), operand(nullptr, 8, kAcross), a.V, a.D, 0, to, nullptr,
                                stream);
   }
-  const BackLayout l = back_layout(a.T, a.V, a.D, piece, b.dh != nullptr, b.dw != nullptr);
+  const BackLayout l = back_layout(a.T, a.V, a.D, piece, b.terms, b.dh != nullptr, b.dw != nullptr);
   uint16_t* g = static_cast<uint16_t*>(ws);
   float* sum = reinterpret_cast<float*>(static_cast<char*>(ws) + l.off_sum);
   float* split = reinterpret_cast<float*>(static_cast<char*>(ws) + l.off_split);
   const Targets y = {a.targets, a.wide_targets};
-  const int64_t padded = padded_rows(a.T);
-  auto part = [&](Kind kind) { return TileOperand{g, 128, 128 * padded, nullptr, 0, kind}; };
+  const int64_t padded = padded_rows(a.T), term = padded * l.p.size;
+  auto part = [&](Kind kind) { return TileOperand{g, 128, 128 * padded, nullptr, 0, kind, b.terms == 2 ? 2 * term : 0}; };
   for (int64_t q = 0; q < l.p.count; ++q) {
     const int64_t v0 = q * l.p.size, n = a.V - v0 < l.p.size ? a.V - v0 : l.p.size;
     const uint16_t* w = a.w + v0 * a.ldw;
     const ProductPlan plan = product_plan(a.T, n, a.D, kAlong, kAlong, false, compute_units());
     const TileArgs t = tile_args(plan, along(a.h, a.ldh), along(w, a.ldw), a.T, n, a.D);
-    tile_launch<kAlong, kAlong>(plan, t, GradEpi{a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, padded}, stream);
+    auto logits = [&](auto epi) { tile_launch<kAlong, kAlong>(plan, t, epi, stream); };
+    if (b.terms == 2) logits(GradEpi<2>{a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, term, padded});
+    else logits(GradEpi<1>{a.scale, y, b.lse, b.dloss, b.dlse, v0, a.V, g, term, padded});
     adahop_status st = check_launch("xent_backward logits");
     if (st != ADAHOP_OK) return st;
     if (b.dh != nullptr) {

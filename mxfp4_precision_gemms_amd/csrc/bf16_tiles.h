@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) bf16_tile_kernel(TileArgs t, Epi 
     __builtin_amdgcn_sched_barrier(0);
     issue(Int<1>{}, Int<0>{}, s1);
     issue(Int<1>{}, Int<2>{}, s1);
+    __builtin_amdgcn_sched_barrier(0);               // the waits count loads in this order
     issue(Int<1>{}, Int<1>{}, s1);
     issue(Int<1>{}, Int<3>{}, s1);
     __builtin_amdgcn_sched_barrier(0);

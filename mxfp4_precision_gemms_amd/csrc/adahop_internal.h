@@ -321,12 +321,6 @@ struct XentGrad {
   int dw_f32;
   int terms;                 // bf16 numbers that hold an element of g: 1 or 2
 };
-// Pieces of the vocabulary in the backward pass: their columns (0: chosen), a
-// multiple of 256, and how many there are.
-struct XentPieces {
-  int64_t size, count;
-};
-XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece, int terms);
 size_t xent_ws_bytes(int64_t T, int64_t V);
 adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, hipStream_t stream);
 size_t xent_backward_ws_bytes(int64_t T, int64_t V, int64_t D, int64_t piece, int terms, bool dh, bool dw);

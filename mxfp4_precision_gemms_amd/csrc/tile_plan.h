@@ -1,5 +1,6 @@
-// Which tiles a product of bf16 operands takes (bf16_tiles.h): plain C++, so that
-// the host can evaluate it without a GPU.
+// Which tiles a product of bf16 operands takes (bf16_tiles.h), and the pieces of the
+// vocabulary in the cross entropy's gradient (xent.hip): plain C++, so that the host
+// can evaluate it without a GPU.
 #pragma once
 
 #include <cstdint>
@@ -73,6 +74,30 @@ inline ProductPlan product_plan(int64_t m, int64_t n, int64_t K, Kind a, Kind b,
     }
   }
   return best;
+}
+
+// Whole columns of 256, which every tile's columns divide.
+inline int64_t whole_tiles(int64_t n) { return (n + 255) / 256 * 256; }
+// Rows that g is held in.
+inline int64_t padded_rows(int64_t T) { return (T + 63) / 64 * 64; }
+
+// Pieces of V entries: their columns, a multiple of 256, and how many there are.
+struct XentPieces {
+  int64_t size, count;
+};
+// piece: columns that the caller asks for, 0: as many as keep g, `terms` bf16
+// numbers an element, within 1 GiB, but 256 at least; pieces of about the same size.
+inline XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece, int terms) {
+  if (piece == 0) {
+    const int64_t all = whole_tiles(V);
+    piece = (int64_t{1} << 29) / terms / padded_rows(T > 0 ? T : 1) / 256 * 256;
+    if (piece < 256) piece = 256;
+    if (piece > all) piece = all;
+    const int64_t count = (all + piece - 1) / piece;
+    piece = (all + count - 1) / count;
+  }
+  piece = whole_tiles(piece < V ? piece : V);
+  return {piece, (V + piece - 1) / piece};
 }
 
 }  // namespace tiles

@@ -296,12 +296,9 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(FinishArgs a) {
 
 // ---- host ---------------------------------------------------------------------
 Operand along(const uint16_t* p, int64_t ld) { return {reinterpret_cast<const uint8_t*>(p), 2 * ld, 128, nullptr, 0}; }
-// Whole columns of 256, which every tile's columns divide.
-int64_t whole(int64_t n) { return (n + kTile - 1) / kTile * kTile; }
 // Groups of 64 columns that leave a maximum and a sum for a row.
-int64_t groups_of(int64_t V) { return whole(V) / 64; }
+int64_t groups_of(int64_t V) { return whole_tiles(V) / 64; }
 TileOperand operand(const uint16_t* p, int64_t ld, Kind kind) { return {p, 2 * ld, 128, nullptr, 0, kind}; }
-int64_t padded_rows(int64_t T) { return (T + 63) / 64 * 64; }
 
 }  // namespace
 
@@ -331,20 +328,6 @@ adahop_status xent_launch(const XentArgs& a, float* loss, float* lse, void* ws, 
 }
 
 // ---- backward -------------------------------------------------------------------
-XentPieces xent_pieces(int64_t T, int64_t V, int64_t piece, int terms) {
-  const int64_t all = whole(V);
-  if (piece == 0) {
-    // g of a piece within 1 GiB, in pieces of about the same size.
-    piece = (int64_t{1} << 29) / terms / (T > 0 ? T : 1) / kTile * kTile;
-    if (piece < kTile) piece = kTile;
-    if (piece > all) piece = all;
-    const int64_t count = (all + piece - 1) / piece;
-    piece = whole((all + count - 1) / count);
-  }
-  piece = whole(piece < V ? piece : V);
-  return {piece, (V + piece - 1) / piece};
-}
-
 namespace {
 struct BackLayout {
   XentPieces p;

@@ -26,10 +26,10 @@ class LmHead:
         self.gain, self.w, self.eps, self.z_loss = gain, w, eps, z_loss
 
     def forward(self, x, stream, targets):
-        """(loss, what backward needs); targets int64 [T], negative: left out."""
+        """(loss, what backward needs); targets int64 [T], one outside 0 .. V - 1: left out."""
         n = A.adahop_rmsnorm(x, self.gain, stream, eps=self.eps, mx8=False, bf16=True, save_rstd=True)
         r = A.adahop_xent(n.y, self.w, targets)
-        counts = (targets >= 0).float()
+        counts = ((targets >= 0) & (targets < self.w.shape[0])).float()
         total = counts.sum().clamp(min=1)
         loss = (r.loss.sum() + self.z_loss * (r.lse.square() * counts).sum()) / total
         return loss, (n, r.lse, targets, counts / total)

@@ -84,6 +84,27 @@ def test_head(T, V, D, z_loss):
     close(dstream, dx, 3)
 
 
+@pytest.mark.parametrize("z_loss", [0.0, 1e-2])
+@pytest.mark.parametrize("T,V,D", [(2, 33, 64), (37, 1000, 128)])
+def test_head_with_targets_past_the_vocabulary(T, V, D, z_loss):
+    """Padding by a number past the vocabulary's last is padding as -100 is: the same
+    loss and the same gradients."""
+    gain = (1 + rand(D, seed=51, std=0.1)).to(torch.bfloat16).to(DEV)
+    w = rand(V, D, seed=52, std=2 * D ** -0.5, dtype=torch.bfloat16).to(DEV)
+    x, stream = (rand(T, D, seed=s, dtype=torch.bfloat16).to(DEV) for s in (53, 54))
+    y = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(55)).to(DEV)
+    head = lm_head.LmHead(gain, w, z_loss=z_loss)
+    got = []
+    for padding in (-100, V, 2 ** 40):
+        y[::2] = padding
+        loss, saved = head.forward(x, stream, y)
+        got.append([loss, *head.backward(saved)])
+    assert float(got[0][0]) > 0
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a, b)
+
+
 def test_step_in_a_graph():
     """Block, head and their gradients captured together, replayed on new inputs
     with eager work between, equal the eager step."""

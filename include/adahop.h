@@ -773,7 +773,7 @@ typedef enum { ADAHOP_XENT_G_SPLIT = 0, ADAHOP_XENT_G_BF16 = 1 } adahop_xent_g;
  * dloss of a row that is left out does not count; its dlse does. dh and dw are
  * bf16 or fp32; either may be NULL. The logits are formed again, `piece` entries
  * of the vocabulary at a time (0: as many as keep g within 1 GiB, but 256, which
- * take more from 2^20 rows on (BF16: 2^21); rounded up to a multiple of 256); g of a piece is held as `g` says, sums are fp32,
+ * take more past 2^20 rows (BF16: 2^21); rounded up to a multiple of 256); g of a piece is held as `g` says, sums are fp32,
  * dh and dw are rounded once. Where SPLIT's second numbers meet an infinity of h
  * or w, the sum may be a NaN instead of an infinity. Needs
  * adahop_xent_backward_args_workspace_size(args) bytes of 16-byte aligned

@@ -5,7 +5,10 @@ Tolerances beyond those derived in test_gpu_xent.py (u = 2^-24): the nearest bf1
 is off by at most 2^-8 |g|; what it leaves is exact in fp32 (a number of 24 bits less
 its first 8), and the nearest bf16 to that is off by at most 2^-8 of it: 2^-16 |g|
 together. SPLIT's sums have twice the terms, whose magnitudes add up to at most (1 +
-2^-7) |g|."""
+2^-7) |g|. What lies below fp32's (and bf16's) smallest normal number, m = 2^-126, may
+count as 0: an exponential, which takes |dloss + dlse| |scale| m from g; g; and its
+second number; and a product or sum of dh and dw, 2 (n + 1) of them. (Logits 1e3 apart
+have probabilities of 1e-90 and below, which no fp32 number stands for.)"""
 import pytest
 import torch
 
@@ -14,6 +17,7 @@ from test_gpu_xent import DEV, U, case, check, logits, say
 from tile_cases import DH, DW, flat
 
 pytestmark = pytest.mark.gpu
+M = 2.0 ** -126
 
 
 def gradients(h, w, y, lse, dloss, dlse, scale, dt, g):
@@ -31,13 +35,14 @@ def gradients(h, w, y, lse, dloss, dlse, scale, dt, g):
     eg = abs(scale) * every.abs()[:, None] * p * torch.expm1(ez[:, None] + (4 + 3 * x.abs()) * U)
     eg = eg + 4 * U * abs(scale) * own[:, None].abs() * hot
     step = 2.0 ** -16 if g == "SPLIT" else 2.0 ** -8
-    eg = eg * (1 + step) + step * gz.abs()
+    eg = eg * (1 + step) + step * gz.abs() + M * (abs(scale) * every.abs()[:, None] + 2)
     terms = 2 * (1 + 2.0 ** -7) if g == "SPLIT" else 1 + 2.0 ** -8
     hd, wd = h.double(), w.double()
     half = torch.finfo(dt).eps / 2
     dh, dw = gz @ wd, gz.t() @ hd
     eh = eg @ wd.abs() + terms * (V + 2) * U * (gz.abs() @ wd.abs())
     ew = eg.t() @ hd.abs() + terms * (h.shape[0] + 2) * U * (gz.abs().t() @ hd.abs())
+    eh, ew = eh + 2 * (V + 1) * M, ew + 2 * (h.shape[0] + 1) * M
     return dh, dw, eh * (1 + half) + half * dh.abs(), ew * (1 + half) + half * dw.abs()
 
 

@@ -799,7 +799,7 @@ typedef struct {
   int32_t target_dtype;
   int32_t dh_dtype, dw_dtype;                    /* adahop_out_dtype */
   int32_t g;                                     /* adahop_xent_g */
-  int32_t reserved[5];
+  int32_t reserved[3];
 } adahop_xent_backward_args;
 
 ADAHOP_API size_t adahop_xent_backward_args_workspace_size(const adahop_xent_backward_args* args);

@@ -123,12 +123,18 @@ class XentArgs(ctypes.Structure):
                 ("scale", ctypes.c_float), ("target_dtype", _i32), ("reserved", _i32 * 4)]
 
 
+class _XentBackwardEnd(ctypes.Union):
+    """`reserved` counts from g on, which was the first of four."""
+    _fields_ = [("g", _i32), ("reserved", _i32 * 4)]
+
+
 class XentBackwardArgs(ctypes.Structure):
+    _anonymous_ = ("end",)
     _fields_ = [("rows", _i64), ("vocab", _i64), ("dim", _i64), ("h", _p), ("ld_h", _i64),
                 ("w", _p), ("ld_w", _i64), ("targets", _p), ("lse", _p), ("dloss", _p), ("dlse", _p),
                 ("dh", _p), ("ld_dh", _i64), ("dw", _p), ("ld_dw", _i64), ("piece", _i64),
                 ("scale", ctypes.c_float), ("target_dtype", _i32), ("dh_dtype", _i32),
-                ("dw_dtype", _i32), ("g", _i32), ("reserved", _i32 * 5)]
+                ("dw_dtype", _i32), ("end", _XentBackwardEnd)]
 
 
 # Exported symbols and their C signatures (argtypes, restype).

@@ -126,7 +126,7 @@ def test_pieces_exactly(T, V, D, piece):
 def test_one_number_in_pieces(T, V, D, piece):
     h, w, y, dloss, dlse = case(T, V, D, seed=T + piece)
     lse = torch.logsumexp(logits(h, w, 1.0)[0], 1).float()
-    a = A.XentBackwardArgs(T, V, D, 16, D, 16, D, 16, 16, 16, None, 16, D, 16, D, piece, 1.0, 1, 1, 0, A.XENT_G["BF16"])
+    a = A.XentBackwardArgs(T, V, D, 16, D, 16, D, 16, 16, 16, None, 16, D, 16, D, piece, 1.0, 1, 1, 0, g=A.XENT_G["BF16"])
     need = A.lib().adahop_xent_backward_args_workspace_size(a)
     ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
     dh, dw = A.adahop_xent_backward(h, w, y, lse, dloss, dlse, dh_dtype=torch.float32, piece=piece, g="BF16", ws=ws)

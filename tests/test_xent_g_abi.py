@@ -1,6 +1,9 @@
 """How g of the cross entropy's gradient is held, on the host: what is refused, the
 workspace that each way asks for, and the binding. No GPU."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -16,10 +19,28 @@ def test_refusals(g, want):
 
 
 def test_reserved():
-    for i in range(5):
+    for i in (1, 2, 3):
         a = xent_back_args()
         a.reserved[i] = 1
         assert status("adahop_xent_backward", a) == INVALID
+
+
+def test_layout(tmp_path):
+    """g took a reserved field's place: a program that was compiled when there was
+    none passes as many bytes as are read, and asks for SPLIT."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "adahop.h"\nint main(void) {\n'
+                   'printf("%zu %zu %zu\\n", sizeof(adahop_xent_backward_args), offsetof(adahop_xent_backward_args, g),'
+                   ' offsetof(adahop_xent_backward_args, dw_dtype));\nreturn ADAHOP_XENT_G_SPLIT; }\n')
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run([cc, "-I" + include, str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
+    a = A.XentBackwardArgs
+    assert [int(v) for v in got] == [160, 144, 140]
+    assert ctypes.sizeof(a) == 160 and a.g.offset == a.reserved.offset == 144 and a.dw_dtype.offset == 140
 
 
 def size(**kw):

@@ -149,3 +149,46 @@ def test_past_the_largest_bf16():
     for g in ("SPLIT", "BF16"):
         dh, _ = A.adahop_xent_backward(h, w, y, zero, zero, far, g=g, dh_dtype=torch.float32)
         assert bool((dh == float("inf")).all())
+
+
+@pytest.mark.parametrize("g", ["SPLIT", "BF16"])
+def test_targets_of_32_bits(g):
+    h, w, y, dloss, dlse = case(300, 2049, 136, seed=13)
+    lse = A.adahop_xent(h, w, y).lse
+    both = [A.adahop_xent_backward(h, w, t, lse, dloss, dlse, g=g) for t in (y, y.to(torch.int32))]
+    for a, b in zip(*both):
+        assert torch.equal(a, b)
+
+
+def test_in_a_graph():
+    """Both ways captured with a workspace each, replayed together on new inputs with
+    eager work between."""
+    T, V, D = 200, 5000, 264
+    h, w, y, dloss, dlse = case(T, V, D, seed=14)
+    lse = A.adahop_xent(h, w, y).lse
+    held, graphs = [], []
+    for g in ("SPLIT", "BF16"):
+        a = A.XentBackwardArgs(T, V, D, 16, D, 16, D, 16, 16, 16, None, 16, D, 16, D, 1024, 1.0, 1, g=A.XENT_G[g])
+        ws = torch.empty(A.lib().adahop_xent_backward_args_workspace_size(a), dtype=torch.uint8, device=DEV)
+        dh, dw = torch.empty_like(h), torch.empty_like(w)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            A.adahop_xent_backward(h, w, y, lse, dloss, dlse, dh=dh, dw=dw, piece=1024, ws=ws, g=g)
+        graphs.append(graph)
+        held.append((g, dh, dw, ws))
+    for s in (15, 16, 17):
+        for to, new in zip((h, w, y, dloss, dlse), case(T, V, D, seed=s)):
+            to.copy_(new)
+        lse.copy_(A.adahop_xent(h, w, y).lse)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for g, dh, dw, _ in held:
+            want = A.adahop_xent_backward(h, w, y, lse, dloss, dlse, piece=1024, g=g)
+            assert torch.equal(dh, want[0]) and torch.equal(dw, want[1])
+            dh.zero_(), dw.zero_()
+        torch.cuda.synchronize()

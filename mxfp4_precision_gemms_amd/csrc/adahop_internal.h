@@ -260,7 +260,7 @@ size_t linear_mx_scratch_bytes(int64_t m, int64_t n, int64_t K, int b_fp4, int g
 adahop_status linear_mx_launch(const LinearArgs& a, int b_fp4, int gated, bool exact, void* scratch,
                                hipStream_t stream);
 
-// ---- products in 256 x 256 tiles ---------------------------------------------
+// ---- products of bf16 operands in tiles ---------------------------------------
 // C[i, j] = sum_k A(i, k) B(j, k) of bf16 operands, in fp32; then, on top of
 // `prev` (fp32 [m][ld_prev], or null), rounded to bf16 or stored in fp32. A lies
 // along K ([m][K]) or across it ([K][m]), B across ([K][n]), or, with A across,

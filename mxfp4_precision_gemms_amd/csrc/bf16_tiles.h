@@ -19,11 +19,14 @@
 // 5 % of the time). Workgroups stay: the next tile's first stages are loaded
 // during a tile's last ones and its epilogue.
 //
-// Measured, 4.4e12 operations each: 8192 x 4096 x 65536 with A along K and B
-// across 1430 .. 1500 TFLOP/s, 65536 x 4096 x 8192 with both across 1410 .. 1500; 4096
-// x 14336 x 32768 with both across 1380 .. 1440, from codes 1290 .. 1380; the matrix
-// cores busy 74 .. 83 % of the time at 1.66 .. 1.77 GHz, the clock that the power limit
-// leaves (16x16x32 and 32x32x16 blocks alike).
+// Measured: 8192 x 4096 x 65536 (4.4e12 operations) with A along K and B across
+// 1430 .. 1500 TFLOP/s (A of two terms, 32768 each, 1540 .. 1570), 65536 x 4096 x 8192
+// with both across 1410 .. 1500 (two terms, 32768 x 4096 x 8192, 1450 .. 1490), the
+// matrix cores busy 80 .. 83 % of the time at 1.75 .. 1.77 GHz, the clock that the power
+// limit leaves (16x16x32 and 32x32x16 blocks alike); 4096 x 14336 x 32768 (3.8e12) with
+// both across 1380 .. 1440, from codes 1280 .. 1390, busy 65 % at 1.87 .. 1.88 GHz. The
+// kernel that reads codes keeps four registers in memory from before its tiles to
+// their epilogues.
 //
 // LDS of an operand along K: rows of 128 bytes, the 16-byte chunks XORed with
 // row bits so that the 16 rows which a quarter of a wave reads at one chunk lie

@@ -30,9 +30,15 @@ struct ProductPlan {
 // far below 2^32 threads.
 constexpr int64_t kMostSmall = int64_t{1} << 28;
 
-// Estimates in microseconds from measurements on the whole device (256 CUs): a
-// launch and a tile's first loads and epilogue 5, a stage of K as below; parts of
-// K a second launch and their sums written and read at 4.5 TB/s. The last round
+// Estimates in microseconds, to rank the tiles by: constants set to products of one
+// to a few rounds of tiles on the whole device (256 CUs), a launch and a tile's first
+// loads and epilogue 5, a stage of K as below; parts of K a second launch and their
+// sums written and read at 4.5 TB/s. They are no times of large tiles in many
+// rounds, nor of epilogues longer than a store (333 x 50021 x 2080 with the cross
+// entropy's statistics: estimate 64, measured 100; 1531 x 50021 x 2048 with its
+// gradient: 181 and 273; 1531 x 2048 x 50021 in parts: 200 and 270; 8192 x 4096 x
+// 65536: 2258 and 2860), and so rank those before smaller ones by up to a half too
+// much. An A of two terms takes the tiles of one. The last round
 // of tiles may be split where it leaves half of the compute units or more without
 // one (dh of 1000 x 1024 x 3000: 128 tiles of 64 x 128 whole 18 us, in two parts
 // 19; 37 x 1032 x 8191: 9 tiles of it 39 us, in 16 parts 11). Up to 128 rows the

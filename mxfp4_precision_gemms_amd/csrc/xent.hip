@@ -5,7 +5,7 @@
 //   g_tv = scale ((dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = y(t)])
 //   dh = g w,  dw = g^T h
 //
-// Forward: one product in 256 x 256 tiles (bf16_tiles.h) whose epilogue leaves,
+// Forward: one product in tiles (bf16_tiles.h) whose epilogue leaves,
 // for each row and 64 columns, their maximum and the sum of their exponentials
 // under it, and the target's logit; a second kernel joins them in a fixed order.
 // Backward: the vocabulary in pieces; for each the logits again, whose epilogue
@@ -28,7 +28,6 @@ namespace adahop {
 namespace {
 
 using namespace tiles;
-using mx8::f32_to_bf16;
 using mx8::f32x2_to_bf16x2;
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -90,8 +89,8 @@ __device__ __forceinline__ float of_row(float x, F&& f) {
 // ---- epilogues ----------------------------------------------------------------
 // What they need of their rows is loaded for all of them before the first is
 // stored: loads and stores are waited for in their order, so a row's loads between
-// two rows' stores would wait for the first's (gradient of 8192 x 32000 x 1024:
-// 1290 us, so 1258).
+// two rows' stores would wait for the first's (gradient of 8192 x 32000 x 1024, g
+// in one number: 1290 us, so 1258).
 //
 // The logits' maximum and sum over the wave's 64 columns of each row, and the
 // target's logit.
